@@ -1,4 +1,4 @@
-"""ctypes view of the C ABI in include/spec_verify.h (libspecverify.so).
+"""ctypes view of the C ABI in include/spec_verify.h and include/spec_kv.h (libspecverify.so).
 
 Loading fails loudly when the shared library has not been built: there is no
 other implementation behind these calls."""
@@ -8,7 +8,7 @@ import ctypes
 import os
 import re
 
-from .build import INCLUDE, LIB, LIB_BOUNDS
+from .build import INCLUDE, LIB, LIB_BOUNDS, PUBLIC
 
 SPEC_OK = 0
 SPEC_ERR_INVALID_ARG = 1
@@ -24,6 +24,8 @@ SPEC_DEV_OFFSETS = 4
 SPEC_DEV_TIMEOUT = 8
 SPEC_DEV_POSITION = 16
 SPEC_DEV_BOUNDS = 32  # only set by the bounds-checked build
+
+SPEC_DEV_PAGE = 64
 
 SPEC_F32 = 0
 SPEC_BF16 = 1
@@ -62,10 +64,29 @@ class SpecOptions(ctypes.Structure):
                 ("block_tokens", ctypes.c_void_p), ("stats", ctypes.c_void_p), ("stats_bucket", ctypes.c_int64)]
 
 
+class SpecKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class SpecKvRows(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("sequences", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("row_seq", ctypes.c_void_p), ("row_pos", ctypes.c_void_p)]
+
+
+class SpecAttnBatch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("gamma", ctypes.c_int32), ("total_draft", ctypes.c_int32),
+                ("cu_draft", ctypes.c_void_p), ("q_heads", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("prefix_len", ctypes.c_int32),
+                ("prefix_table", ctypes.c_void_p), ("parent", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _F = ctypes.c_float
 _S = ctypes.c_size_t
+_L = ctypes.c_int64
 
 SIGNATURES = {
     "spec_workspace_bytes": (_S, [SpecBatch, ctypes.c_int, ctypes.c_int]),
@@ -90,6 +111,10 @@ SIGNATURES = {
     "spec_verify_multi": (ctypes.c_int, [SpecMultiBatch, ctypes.c_int, _I, _P, _P, _P, _F, _P, _P, _F, _F, _P, _P,
                                          _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
     "spec_selftest_wait_timeout": (ctypes.c_int, [_P, _P, _S, _P]),
+    "spec_kv_append": (ctypes.c_int, [SpecKvCache, SpecKvRows, ctypes.c_int, _P, _L, _L, _P, _L, _L, _P, _P]),
+    "spec_kv_read": (ctypes.c_int, [SpecKvCache, SpecKvRows, ctypes.c_int, _P, _P, _P, _P]),
+    "spec_attention_workspace_bytes": (_S, [SpecAttnBatch, SpecKvCache, ctypes.c_int]),
+    "spec_attention": (ctypes.c_int, [SpecAttnBatch, SpecKvCache, ctypes.c_int, _P, _L, _L, _P, _P, _P, _P, _S, _P]),
     "spec_status_str": (ctypes.c_char_p, [ctypes.c_int]),
 }
 
@@ -97,9 +122,11 @@ _LIB = None
 
 
 def declared_functions() -> list:
-    """Names of the functions include/spec_verify.h declares."""
-    with open(os.path.join(INCLUDE, "spec_verify.h")) as f:
-        text = f.read()
+    """Names of the functions the public headers declare."""
+    text = ""
+    for header in PUBLIC:
+        with open(os.path.join(INCLUDE, header)) as f:
+            text += f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(spec_[a-z_]+)\s*\(", text)))
 

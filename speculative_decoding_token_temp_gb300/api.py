@@ -459,3 +459,212 @@ def spec_verify_multi(target: torch.Tensor, draft: torch.Tensor, draft_tokens: t
         _ptr(pn), _ptr(cons), _ptr(div), _ptr(device_status), _ptr(ws), ws.numel(), _stream(dev))
     check("spec_verify_multi", code)
     return o
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit key/value cache and the attention over it (include/spec_kv.h)
+
+class KVCache:
+    """A paged key/value cache in 8 bits: k, v [num_pages, kv_heads, page_size, head_dim]
+    (torch.float8_e4m3fn codes), k_exp, v_exp [num_pages, kv_heads, page_size] (uint8); an
+    element stands for its code * 2^(exp - 127). It holds the four tensors and the
+    descriptor that the calls take; `KVCache.empty` allocates them. Pages need no
+    initialisation: places that nothing was appended to are never looked at."""
+
+    __slots__ = ("k", "v", "k_exp", "v_exp", "num_pages", "kv_heads", "page_size", "head_dim", "device", "desc")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor):
+        _need(k, "k", torch.float8_e4m3fn)
+        if k.dim() != 4:
+            raise ValueError(f"k must be [num_pages, kv_heads, page_size, head_dim], got {tuple(k.shape)}")
+        dev = k.device
+        _need(v, "v", torch.float8_e4m3fn, k.numel(), dev)
+        P, H, S, D = k.shape
+        _need(k_exp, "k_exp", torch.uint8, P * H * S, dev)
+        _need(v_exp, "v_exp", torch.uint8, P * H * S, dev)
+        if S not in (16, 32, 64, 128, 256):
+            raise ValueError(f"page_size must be 16, 32, 64, 128 or 256, got {S}")
+        if D not in (64, 128):
+            raise ValueError(f"head_dim must be 64 or 128, got {D}")
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim, self.device = P, H, S, D, dev
+        self.desc = _lib.SpecKvCache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), P, S, H, D)
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, device) -> "KVCache":
+        shape = (int(num_pages), int(kv_heads), int(page_size))
+        k, v = (torch.empty(*shape, int(head_dim), dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
+        k_exp, v_exp = (torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2))
+        return cls(k, v, k_exp, v_exp)
+
+
+def _status_word(o: dict, device_status, dev) -> torch.Tensor:
+    if device_status is None:
+        device_status = _out(o, "device_status", lambda: torch.zeros(1, dtype=torch.int32, device=dev))
+    else:
+        _need(device_status, "device_status", torch.int32, 1, dev)
+        o["device_status"] = device_status
+    return device_status
+
+
+def _strides(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dev):
+    """(row, head) strides of a [rows, heads, dim] view whose vectors are contiguous; the
+    view may be a slice of a wider buffer."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}, got {t.device}")
+    if t.dim() == 4 and t.shape[0] * t.shape[1] == rows:
+        if t.shape[0] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
+            raise ValueError(f"{name}: the rows of a [B, rows, heads, dim] view must be evenly spaced")
+        t = t.flatten(0, 1)
+    if t.dim() != 3 or tuple(t.shape) != (rows, heads, dim):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return t.stride(0), t.stride(1)
+
+
+def _kv_rows(cache: KVCache, page_table, row_seq, row_pos) -> _lib.SpecKvRows:
+    dev = cache.device
+    _need(page_table, "page_table", torch.int32, device=dev)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [sequences, pages], got {tuple(page_table.shape)}")
+    n = row_seq.numel()
+    _need(row_seq, "row_seq", torch.int32, device=dev)
+    _need(row_pos, "row_pos", torch.int32, n, dev)
+    return _lib.SpecKvRows(n, page_table.shape[0], page_table.shape[1], page_table.data_ptr(), row_seq.data_ptr(),
+                           row_pos.data_ptr())
+
+
+def spec_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, row_seq: torch.Tensor,
+                   row_pos: torch.Tensor, *, out: dict | None = None, device_status=None) -> dict:
+    """Quantise rows of keys and values into the cache as they are written.
+
+    k, v [rows, kv_heads, head_dim] in bfloat16 or float32 (slices of a fused projection
+    are taken as they are); row n goes to position row_pos[n] of sequence row_seq[n]
+    (int32 [rows]), whose pages are page_table[row_seq[n]] (int32 [sequences, pages]); a
+    negative position leaves the row out. Returns the dict with device_status."""
+    dt = _dtype_code(k)
+    if v.dtype != k.dtype:
+        raise TypeError(f"v must be {k.dtype}, got {v.dtype}")
+    dev = cache.device
+    r = _kv_rows(cache, page_table, row_seq, row_pos)
+    k_row, k_head = _strides(k, "k", r.rows, cache.kv_heads, cache.head_dim, dev)
+    v_row, v_head = _strides(v, "v", r.rows, cache.kv_heads, cache.head_dim, dev)
+    o = {} if out is None else out
+    st = _status_word(o, device_status, dev)
+    check("spec_kv_append", _lib.lib().spec_kv_append(cache.desc, r, dt, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row,
+                                                      v_head, st.data_ptr(),
+                                                      torch.cuda.current_stream(dev).cuda_stream))
+    return o
+
+
+def spec_kv_read(cache: KVCache, page_table: torch.Tensor, row_seq: torch.Tensor, row_pos: torch.Tensor, *,
+                 dtype: torch.dtype = torch.bfloat16, want_k: bool = True, want_v: bool = True,
+                 out: dict | None = None, device_status=None) -> dict:
+    """Read cached rows back as numbers: k, v [rows, kv_heads, head_dim] of dtype (bfloat16
+    or float32, both exact), plus device_status. Rows with a negative position are zeros."""
+    dev = cache.device
+    r = _kv_rows(cache, page_table, row_seq, row_pos)
+    o = {} if out is None else out
+    shape = (r.rows, cache.kv_heads, cache.head_dim)
+
+    def dst(name, want):
+        if not want:
+            return None
+        t = _out(o, name, lambda: torch.empty(shape, dtype=dtype, device=dev))
+        _need(t, name, dtype, r.rows * cache.kv_heads * cache.head_dim, dev)
+        return t
+
+    k, v = dst("k", want_k), dst("v", want_v)
+    st = _status_word(o, device_status, dev)
+    code = {torch.bfloat16: _lib.SPEC_BF16, torch.float32: _lib.SPEC_F32}.get(dtype)
+    if code is None:
+        raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
+    check("spec_kv_read", _lib.lib().spec_kv_read(cache.desc, r, code, _ptr(k), _ptr(v), st.data_ptr(), _stream(dev)))
+    return o
+
+
+def _attn_batch(q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, prefix_table, prefix_len):
+    """(descriptor, rows, q_heads, keep-alive) of an attention call."""
+    dev = cache.device
+    _need(page_table, "page_table", torch.int32, device=dev)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [sequences, pages], got {tuple(page_table.shape)}")
+    B = page_table.shape[0]
+    _need(kv_len, "kv_len", torch.int32, B, dev)
+    H = q.shape[-2] if q.dim() >= 3 else 0
+    par = None
+    if parent is not None:
+        if gamma is not None and int(gamma) != len(parent):
+            raise ValueError(f"a tree of {len(parent)} nodes has gamma {len(parent)}, got {gamma}")
+        gamma = len(parent)
+        par = (ctypes.c_int32 * len(parent))(*[int(x) for x in parent])
+    if cu_draft is None:
+        if gamma is None:
+            if q.dim() != 4:
+                raise ValueError("a dense batch of [rows, heads, dim] queries needs gamma")
+            gamma = q.shape[1] - 1
+        total = B * int(gamma)
+    else:
+        if gamma is None:
+            raise ValueError("packed batches need gamma (an upper bound on every gamma_b)")
+        _need(cu_draft, "cu_draft", torch.int32, B + 1, dev)
+        total = (q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]) - B
+    n = int(prefix_len)
+    if n > 0:
+        _need(prefix_table, "prefix_table", torch.int32, device=dev)
+        if prefix_table.numel() < -(-n // cache.page_size):
+            raise ValueError(f"prefix_table has {prefix_table.numel()} pages, {n} tokens need {-(-n // cache.page_size)}")
+    g = _lib.SpecAttnBatch(B, int(gamma), total, None if cu_draft is None else cu_draft.data_ptr(), H,
+                           page_table.shape[1], page_table.data_ptr(), kv_len.data_ptr(), n,
+                           prefix_table.data_ptr() if n > 0 else None,
+                           None if par is None else ctypes.cast(par, ctypes.c_void_p),
+                           cache.head_dim ** -0.5 if scale is None else float(scale))
+    return g, total + B, H, par
+
+
+def spec_attention_workspace_bytes(q, cache: KVCache, page_table, kv_len, *, gamma=None, cu_draft=None, parent=None,
+                                   scale=None, prefix_table=None, prefix_len: int = 0) -> int:
+    """Workspace bytes of the same spec_attention call."""
+    g = _attn_batch(q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, prefix_table, prefix_len)[0]
+    return int(_lib.lib().spec_attention_workspace_bytes(g, cache.desc, _dtype_code(q)))
+
+
+def spec_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_len: torch.Tensor, *,
+                   gamma: int | None = None, cu_draft: torch.Tensor | None = None, parent=None,
+                   scale: float | None = None, prefix_table: torch.Tensor | None = None, prefix_len: int = 0,
+                   want_lse: bool = False, out: dict | None = None, workspace=None, device_status=None) -> dict:
+    """Attention of a verification round's rows over the cache.
+
+    q [rows, q_heads, head_dim] in bfloat16 or float32, rows packed as the target rows of
+    the verification calls (sequence b's gamma_b + 1 rows from cu_draft[b] + b on), or
+    [B, gamma + 1, q_heads, head_dim]; views of a wider buffer are taken as they are.
+    kv_len [B] int32: cached tokens of each sequence, this round's rows (appended before)
+    among them. Row i sees its sequence's earlier tokens, this round's rows up to i (with
+    `parent`, a host sequence as in spec_verify_tree: its ancestors) and, with prefix_len,
+    the shared prefix on the pages prefix_table. scale defaults to head_dim ** -0.5.
+    Returns o [rows, q_heads, head_dim], lse [rows, q_heads] (fp32, with want_lse) and
+    device_status."""
+    dt = _dtype_code(q)
+    dev = cache.device
+    g, rows, H, par = _attn_batch(q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, prefix_table, prefix_len)
+    q_row, q_head = _strides(q, "q", rows, H, cache.head_dim, dev)
+    o = {} if out is None else out
+    y = _out(o, "o", lambda: torch.empty(rows, H, cache.head_dim, dtype=q.dtype, device=dev))
+    _need(y, "o", q.dtype, rows * H * cache.head_dim, dev)
+    lse = None
+    if want_lse:
+        lse = _out(o, "lse", lambda: torch.empty(rows, H, dtype=torch.float32, device=dev))
+        _need(lse, "lse", torch.float32, rows * H, dev)
+    st = _status_word(o, device_status, dev)
+    lib = _lib.lib()
+    nbytes = int(lib.spec_attention_workspace_bytes(g, cache.desc, dt))
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if workspace is None:  # a default workspace for each stream: calls on two streams may overlap
+        workspace = _DEFAULT_WS.setdefault((dev.type, dev.index, stream), Workspace())
+    ws = _workspace(workspace, nbytes, dev)
+    check("spec_attention", lib.spec_attention(g, cache.desc, dt, q.data_ptr(), q_row, q_head, y.data_ptr(), _ptr(lse),
+                                               st.data_ptr(), ws.data_ptr(), ws.numel(), stream))
+    return o

@@ -1,6 +1,6 @@
 """Build step of the CUDA library: one nvcc invocation, sm_103a only, in-tree output.
 
-The library is plain C ABI (include/spec_verify.h) with the CUDA runtime linked
+The library is plain C ABI (include/spec_verify.h, include/spec_kv.h) with the CUDA runtime linked
 statically, so the Python layer loads it with ctypes and nothing else."""
 from __future__ import annotations
 
@@ -20,8 +20,10 @@ LIB = os.path.join(PKG, "libspecverify.so")
 # the same library with every computed access bounds-checked (SPEC_BOUNDS_CHECK=1): a debug
 # variant for tests, which reports an access outside its buffer as SPEC_DEV_BOUNDS
 LIB_BOUNDS = os.path.join(PKG, "libspecverify_bounds.so")
-SOURCES = ["spec_verify.cu"]
-HEADERS = ["kernels.cuh", "kernels_rows.cuh", "kernels_sample.cuh", "kernels_multi.cuh", "plan.h"]
+SOURCES = ["spec_verify.cu", "spec_kv.cu"]
+HEADERS = ["kernels.cuh", "kernels_rows.cuh", "kernels_sample.cuh", "kernels_multi.cuh", "plan.h",
+           "kernels_kv.cuh", "kernels_attn.cuh"]
+PUBLIC = ["spec_verify.h", "spec_kv.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,7 +36,7 @@ def nvcc_path() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files.append(os.path.join(INCLUDE, "spec_verify.h"))
+    files += [os.path.join(INCLUDE, f) for f in PUBLIC]
     files.append(os.path.abspath(__file__))
     return files
 
@@ -76,7 +78,7 @@ def up_to_date(lib: str = LIB) -> bool:
 
 def _command(lib: str, ptxas_info: bool) -> list:
     cmd = [nvcc_path(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-cudart", "static", "-I", INCLUDE, "-I", CSRC, "-o", lib + ".tmp"]
+           "-cudart", "static", "--threads", "0", "-I", INCLUDE, "-I", CSRC, "-o", lib + ".tmp"]
     if lib == LIB_BOUNDS:
         cmd.append("-DSPEC_BOUNDS_CHECK=1")
     if ptxas_info:

@@ -1,0 +1,522 @@
+// Attention of the rows of a verification round over the 8-bit paged cache: the work
+// split, the joining of its parts, and the 32-bit kernel.
+//
+// Work split. Rows that share keys (the gamma_b + 1 rows of a sequence times the G query
+// heads of a kv head) form row blocks of NR; a row block's keys, cut into tiles of 128
+// tokens, are a segment. The segments of all sequences, heads and row blocks laid end to
+// end are a line of tiles, of which every block of the grid takes an equal, contiguous
+// stretch: long and short sequences, few and many, keep all SMs equally busy, and what a
+// block reads does not depend on when it runs. A block that holds a whole segment writes
+// its rows' output; the parts of a segment that is cut between blocks go to the workspace
+// (running maximum, sum and weighted values of each row), and attn_merge_kernel joins them
+// in order, so the result does not depend on timing.
+//
+// The shared prefix is one more sequence whose "rows" are all rows of the batch: one pass
+// over its keys for the whole batch, whose normalised part and log-sum the pass over the
+// sequences' own tokens joins in.
+#pragma once
+
+#include "kernels_kv.cuh"
+
+namespace sv {
+
+constexpr int kTile = 128;  // tokens of a tile
+constexpr int kRowsS = 8;   // row block of the 32-bit kernel
+constexpr int kNegInfBits = 0xff800000;
+
+enum AttnMask : int { A_ALL = 0, A_CHAIN = 1, A_TREE = 2 };
+
+struct AttnParams {
+  const uint8_t *k, *v, *k_exp, *v_exp;
+  int num_pages, page_shift, Hk, Hq, G;
+  const void* q;
+  long long q_row, q_head;  // strides in elements
+  int B, gamma, total_draft, R;
+  const int32_t* cu;
+  const int32_t* table;
+  int pps;
+  const int32_t* kv_len;  // null: every sequence has fixed_len tokens
+  int fixed_len;
+  int mask;
+  float c;                  // scale * log2(e)
+  float* part;              // the parts of cut segments: two slots a block
+  long long part_floats;
+  const float *pre_o, *pre_lse;  // the prefix's part to join in (normalised values, log2 of the sum), or null
+  float *dst_o, *dst_lse;        // the prefix pass: its part goes here instead of o and lse
+  void* o;
+  float* lse;
+  uint32_t* status;
+  uint64_t sees[SPEC_MAX_TREE_NODES];  // node j: bit i set when node i sees it (i == j or a descendant of j)
+};
+
+struct SeqInfo {
+  int row0, rows, len;
+  bool bad;  // kv_len out of range: taken as 0, its rows are NaN
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
+  SeqInfo s;
+  if (p.cu != nullptr) {
+    const int lo = __ldg(p.cu + b);
+    s.row0 = lo + b;
+    s.rows = __ldg(p.cu + b + 1) - lo + 1;
+  } else {
+    s.row0 = b * (p.gamma + 1);
+    s.rows = p.gamma + 1;
+  }
+  s.len = p.kv_len != nullptr ? __ldg(p.kv_len + b) : p.fixed_len;
+  s.bad = s.len < 0 || (long long)s.len > ((long long)p.pps << p.page_shift);
+  if (s.bad) s.len = 0;
+  return s;
+}
+
+__device__ __forceinline__ int seq_ntiles(const SeqInfo& s) { return s.len > 0 ? (s.len - 1) / kTile + 1 : 1; }
+
+// Tiles of sequence b over all its row blocks and kv heads.
+template <int NR>
+__device__ __forceinline__ long long seq_tiles(const AttnParams& p, const SeqInfo& s) {
+  return (long long)((s.rows * p.G + NR - 1) / NR) * p.Hk * seq_ntiles(s);
+}
+
+// A place on the line of tiles: sequence b, tile `off` of it.
+struct Place {
+  int b;
+  long long off;
+};
+
+struct LocateShared {
+  long long warp_sum[32];
+  int bad;
+  Place at[2];
+};
+
+// Block-wide: the line's length and the places of the tiles at fraction i0 / n and i1 / n of
+// it. Each thread sums a stretch of sequences, the block scans the sums, and the thread
+// whose stretch holds a place walks to it. Returns false when cu is no valid prefix sum
+// (nothing else it says is then used).
+template <int NR, int THREADS>
+__device__ bool locate(const AttnParams& p, LocateShared& sh, int i0, int i1, int n, long long* begin, long long* end,
+                       long long* line) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) sh.bad = 0;
+  __syncthreads();
+  const int per = (p.B + THREADS - 1) / THREADS;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    if (p.cu != nullptr) {
+      const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1);
+      if (lo < 0 || hi > p.total_draft || hi < lo || hi - lo > p.gamma || (b == 0 && lo != 0) ||
+          (b == p.B - 1 && hi != p.total_draft)) {
+        sh.bad = 1;
+        continue;
+      }
+    }
+    sum += seq_tiles<NR>(p, seq_info(p, b));
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sh.warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += sh.warp_sum[w];
+    total += sh.warp_sum[w];
+  }
+  const long long excl = before + incl - sum;
+  const bool ok = sh.bad == 0;
+  if (ok) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const long long pos = total * (k ? i1 : i0) / n;
+      if (pos >= excl && pos < excl + sum) {
+        long long at = excl;
+        for (int b = b0; b < b1; ++b) {
+          const long long t = seq_tiles<NR>(p, seq_info(p, b));
+          if (pos < at + t) {
+            sh.at[k].b = b;
+            sh.at[k].off = pos - at;
+            break;
+          }
+          at += t;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  *begin = total * i0 / n;
+  *end = total * i1 / n;
+  *line = total;
+  return ok;
+}
+
+// One segment's stretch that a block works on.
+struct Seg {
+  int row0, rows, len, h, f0;  // f0: first flat row (row * G + head within the group) of the row block
+  int t0, n, nt;               // its tiles t0 .. t0 + n - 1 of nt
+  const int32_t* pages;
+  bool bad;
+};
+
+// The next stretch at `at` (advanced), at most `left` tiles (reduced).
+template <int NR>
+__device__ __forceinline__ Seg next_seg(const AttnParams& p, Place& at, long long& left) {
+  Seg g;
+  const SeqInfo s = seq_info(p, at.b);
+  g.row0 = s.row0, g.rows = s.rows, g.len = s.len, g.bad = s.bad;
+  g.nt = seq_ntiles(s);
+  const int nrb = (s.rows * p.G + NR - 1) / NR;
+  const int seg = (int)(at.off / g.nt);
+  g.t0 = (int)(at.off - (long long)seg * g.nt);
+  g.h = seg / nrb;
+  g.f0 = (seg - g.h * nrb) * NR;
+  g.n = (int)min((long long)(g.nt - g.t0), left);
+  g.pages = p.table + (long long)at.b * p.pps;
+  at.off += g.n;
+  left -= g.n;
+  if (at.off >= (long long)nrb * p.Hk * g.nt) {
+    at.b += 1;
+    at.off = 0;
+  }
+  return g;
+}
+
+// Whether row i of a segment sees token t (< len) of its sequence.
+__device__ __forceinline__ bool sees(const AttnParams& p, int i, int rows, int len, int t) {
+  const int j = t - (len - rows);  // the round's row whose token it is
+  if (p.mask == A_ALL || j < 0) return true;
+  if (p.mask == A_CHAIN || j == 0) return i >= j;
+  return i >= j && ((p.sees[j - 1] >> (i - 1)) & 1);
+}
+
+// ---------------------------------------------------------------------------
+// The end of a row: weights of its values and of the prefix's part, and its log-sum.
+struct Coef {
+  float a, b, lse2;
+};
+
+__device__ __forceinline__ Coef row_coef(const AttnParams& p, long long idx, float m, float l, bool bad) {
+  Coef r;
+  const float nan = __int_as_float(0x7fffffff), ninf = __int_as_float(kNegInfBits);
+  if (bad) return Coef{nan, 0.f, nan};
+  r.lse2 = l == 0.f ? ninf : m + log2f(l);
+  r.a = l == 0.f ? 0.f : 1.f / l;
+  r.b = 0.f;
+  if (p.pre_o != nullptr) {
+    const float q = __ldg(p.pre_lse + idx);
+    if (l == 0.f) {
+      r.b = q == ninf ? 0.f : 1.f;
+      r.lse2 = q;
+    } else if (q != ninf) {
+      const float mx = fmaxf(r.lse2, q), e1 = exp2f(r.lse2 - mx), e2 = exp2f(q - mx), s = e1 + e2;
+      r.a *= e1 / s;
+      r.b = e2 / s;
+      r.lse2 = mx + log2f(s);
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ void put(uint16_t* o, float x) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(x);
+  *o = *reinterpret_cast<const uint16_t*>(&h);
+}
+__device__ __forceinline__ void put(float* o, float x) { *o = x; }
+
+// Element d of row `idx` (row * Hq + head): the values' sum v under the row's weights.
+template <typename E, int D>
+__device__ __forceinline__ void finish(const AttnParams& p, long long idx, int d, float v, const Coef& r) {
+  const long long at = idx * D + d;
+  if (!in_idx(at, (long long)p.R * p.Hq * D, p.status)) return;
+  float x = v * r.a;
+  if (r.b != 0.f) x += __ldg(p.pre_o + at) * r.b;
+  if (p.dst_o != nullptr)
+    p.dst_o[at] = x;
+  else
+    put(static_cast<E*>(p.o) + at, x);
+}
+
+__device__ __forceinline__ void finish_lse(const AttnParams& p, long long idx, const Coef& r) {
+  if (p.dst_o != nullptr)
+    p.dst_lse[idx] = r.lse2;
+  else if (p.lse != nullptr)
+    p.lse[idx] = r.lse2 * 0.69314718055994530942f;
+}
+
+// A slot of the workspace: NR maxima, NR sums, NR x D values.
+template <int NR, int D>
+__device__ __forceinline__ float* slot_of(const AttnParams& p, int s) {
+  return p.part + (long long)s * (NR * (D + 2));
+}
+
+// A cu that is no prefix sum of the batch: every row is NaN.
+template <typename E, int D>
+__device__ void fill_nan(const AttnParams& p, int block, int blocks) {
+  if (block == 0 && threadIdx.x == 0) atomicOr(p.status, SPEC_DEV_OFFSETS);
+  const long long n = (long long)p.R * p.Hq * D;
+  const float nan = __int_as_float(0x7fffffff);
+  for (long long i = (long long)block * blockDim.x + threadIdx.x; i < n; i += (long long)blocks * blockDim.x) {
+    put(static_cast<E*>(p.o) + i, nan);
+    if (p.lse != nullptr && i % D == 0) p.lse[i / D] = nan;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joins the parts of cut segments. Block x looks at the cut between grid blocks x and
+// x + 1; if it is the first cut inside a segment, it joins all parts of that segment, in
+// order; block y takes 4 of its rows, one a warp.
+template <typename E, int D, int NR>
+__global__ void __launch_bounds__(128) attn_merge_kernel(AttnParams p, int grid) {
+  __shared__ LocateShared sh;
+  const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
+  long long prev, cut, total;
+  // what locate reads was there before the attention kernel began, which released this grid after its own wait
+  const bool ok = locate<NR, 128>(p, sh, i - 1, i, grid, &prev, &cut, &total);
+  griddep_wait();
+  griddep_launch();
+  if (!ok || cut >= total) return;
+  Place at = sh.at[1];
+  long long left = 1;
+  const Seg g = next_seg<NR>(p, at, left);
+  const long long first = cut - g.t0, last = first + g.nt;
+  if (g.t0 == 0 || prev > first) return;
+  const int c = blockIdx.y * 4 + (threadIdx.x >> 5), f = g.f0 + c;
+  if (f >= g.rows * p.G) return;
+  // parts: block i - 1 (slot 2 (i - 1) + 1), then every block from i on that has tiles before `last`
+  int e = i;
+  while (e < grid && total * e / grid < last) ++e;
+  const int parts = e - i + 1;
+  float m = __int_as_float(kNegInfBits);
+  for (int j = lane; j < parts; j += 32) {
+    const int blk = i - 1 + j;
+    if (j > 0 && total * blk / grid == total * (blk + 1) / grid) continue;
+    m = fmaxf(m, slot_of<NR, D>(p, j == 0 ? 2 * blk + 1 : 2 * blk)[c]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  const float mu = m == __int_as_float(kNegInfBits) ? 0.f : m;
+  float l = 0.f, acc[D / 32];
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
+  for (int j0 = 0; j0 < parts; j0 += 32) {
+    const int j = j0 + lane, blk = i - 1 + j;
+    float w = 0.f, lj = 0.f;
+    if (j < parts && (j == 0 || total * blk / grid != total * (blk + 1) / grid)) {
+      const float* s = slot_of<NR, D>(p, j == 0 ? 2 * blk + 1 : 2 * blk);
+      w = exp2f(s[c] - mu);
+      lj = s[NR + c];
+      if (!(lj == 0.f)) l += w * lj;
+      if (lj == 0.f) w = 0.f;
+    }
+    const int cnt = min(32, parts - j0);
+    for (int t = 0; t < cnt; ++t) {
+      const float wt = __shfl_sync(kFull, w, t);
+      if (wt == 0.f) continue;
+      const int jt = j0 + t, bt = i - 1 + jt;
+      const float* s = slot_of<NR, D>(p, jt == 0 ? 2 * bt + 1 : 2 * bt) + 2 * NR + c * D + lane * (D / 32);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) acc[k] += wt * s[k];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+  const long long idx = (long long)(g.row0 + f / p.G) * p.Hq + g.h * p.G + f % p.G;
+  const Coef r = row_coef(p, idx, mu, l, g.bad);
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) finish<E, D>(p, idx, lane * (D / 32) + k, acc[k], r);
+  if (lane == 0) finish_lse(p, idx, r);
+}
+
+// ---------------------------------------------------------------------------
+// The 32-bit kernel: fp32 products and sums throughout, for fp32 queries (whose accuracy
+// the tensor cores' 16-bit operands would lose). A block of 128 threads holds 8 rows; of a
+// tile, a thread computes the scores of one token, then sums the values of 4 elements over
+// its share of the tokens.
+template <typename E, int D>
+__global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
+  constexpr int NR = kRowsS, KS = D + 16;  // a key's stride: 16 bytes more than its codes, so that 8 lanes hit all banks
+  constexpr int NG = 128 / (D / 4);        // token groups of the values' sum
+  __shared__ LocateShared sh;
+  __shared__ __align__(16) float sq[NR][D];
+  __shared__ __align__(16) uint8_t skv[kTile * KS + kTile * D];
+  __shared__ __align__(16) float sp[kTile][NR];
+  __shared__ float ss[NR][kTile + 4];
+  __shared__ float sx[kTile];
+  __shared__ int sbad[kTile];
+  __shared__ float sm[NR], sl[NR], sf[NR];
+  static_assert(sizeof(float) * NG * NR * D <= sizeof(skv), "the sums of the token groups fit where the tile was");
+  uint8_t* sk = skv;
+  uint8_t* svv = skv + kTile * KS;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float ninf = __int_as_float(kNegInfBits), nan = __int_as_float(0x7fffffff);
+  griddep_wait();
+  griddep_launch();
+  long long begin, end, total;
+  if (!locate<NR, 128>(p, sh, blockIdx.x, blockIdx.x + 1, gridDim.x, &begin, &end, &total)) {
+    fill_nan<E, D>(p, blockIdx.x, gridDim.x);
+    return;
+  }
+  Place at = sh.at[0];
+  long long left = end - begin;
+  uint32_t bits = 0;
+  while (left > 0) {
+    const Seg g = next_seg<NR>(p, at, left);
+    if (g.bad) bits |= SPEC_DEV_OFFSETS;
+    __syncthreads();
+    for (int e = tid; e < NR * D; e += 128) {
+      const int c = e / D, d = e % D, f = g.f0 + c;
+      float x = 0.f;
+      if (f < g.rows * p.G) {
+        const long long a = (long long)(g.row0 + f / p.G) * p.q_row + (long long)(g.h * p.G + f % p.G) * p.q_head + d;
+        if constexpr (sizeof(E) == 2)
+          x = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.q) + a) << 16);
+        else
+          x = __ldg(static_cast<const float*>(p.q) + a);
+      }
+      sq[c][d] = x * p.c;
+    }
+    if (tid < NR) sm[tid] = ninf, sl[tid] = 0.f;
+    float acc[NR][4];
+#pragma unroll
+    for (int c = 0; c < NR; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+    const int wi = tid % (D / 4), tg = tid / (D / 4);
+    for (int tile = g.t0; tile < g.t0 + g.n; ++tile) {
+      sbad[tid] = 0;
+      __syncthreads();
+      for (int e = tid; e < kTile * (D / 16); e += 128) {
+        const int u = e / (D / 16), ch = e % (D / 16), t = tile * kTile + u;
+        uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
+        if (t < g.len) {
+          const int page = __ldg(g.pages + (t >> p.page_shift));
+          if ((unsigned)page < (unsigned)p.num_pages) {
+            const long long vec = (((long long)page * p.Hk + g.h) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
+            kw = __ldg(reinterpret_cast<const uint4*>(p.k + vec * D) + ch);
+            vw = __ldg(reinterpret_cast<const uint4*>(p.v + vec * D) + ch);
+            // NaN codes of values: zero, and the token marked (0 * NaN must not reach rows that do not see it)
+            uint32_t* w = &vw.x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t mk = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              if (mk) sbad[u] = 1;
+              w[k] &= ~mk;
+            }
+          } else {
+            bits |= SPEC_DEV_PAGE;
+            sbad[u] = 1;
+          }
+        }
+        *reinterpret_cast<uint4*>(sk + u * KS + ch * 16) = kw;
+        *reinterpret_cast<uint4*>(svv + u * D + ch * 16) = vw;
+      }
+      __syncthreads();
+      {
+        const int t = tile * kTile + tid;
+        float ke = 0.f, ve = 0.f;
+        if (t < g.len) {
+          if (sbad[tid]) {
+            ke = nan;
+          } else {
+            const int page = __ldg(g.pages + (t >> p.page_shift));
+            const long long vec = (((long long)page * p.Hk + g.h) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
+            ke = exp_value(__ldg(p.k_exp + vec));
+            ve = exp_value(__ldg(p.v_exp + vec));
+            if (ve != ve) ke = nan;
+          }
+        }
+        float s[NR];
+#pragma unroll
+        for (int c = 0; c < NR; ++c) s[c] = 0.f;
+        for (int ch = 0; ch < D / 4; ++ch) {
+          float x[4];
+          codes4(*reinterpret_cast<const uint32_t*>(sk + tid * KS + ch * 4), x);
+#pragma unroll
+          for (int c = 0; c < NR; ++c) {
+            const float4 y = *reinterpret_cast<const float4*>(&sq[c][ch * 4]);
+            s[c] = fmaf(x[0], y.x, fmaf(x[1], y.y, fmaf(x[2], y.z, fmaf(x[3], y.w, s[c]))));
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < NR; ++c)
+          ss[c][tid] = t < g.len && sees(p, (g.f0 + c) / p.G, g.rows, g.len, t) ? s[c] * ke : ninf;
+        sx[tid] = ve;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < NR / 4; ++k) {
+        const int c = warp * (NR / 4) + k;
+        float x[4], mx = sm[c];
+        const float m_old = mx;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx = fmaxf(mx, x[u] = ss[c][u * 32 + lane]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+        const float mu = mx == ninf ? 0.f : mx;
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float e = exp2f(x[u] - mu);
+          sum += e;
+          sp[u * 32 + lane][c] = e == 0.f ? 0.f : e * sx[u * 32 + lane];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        __syncwarp();
+        if (lane == 0) {
+          const float f = exp2f(m_old - mu);
+          sf[c] = f;
+          sl[c] = sl[c] * f + sum;
+          sm[c] = mx;
+        }
+        __syncwarp();
+      }
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < NR; ++c) {
+        const float f = sf[c];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[c][k] *= f;
+      }
+      for (int u = tg; u < kTile; u += NG) {
+        float x[4];
+        codes4(*reinterpret_cast<const uint32_t*>(svv + u * D + wi * 4), x);
+        const float4 y0 = *reinterpret_cast<const float4*>(&sp[u][0]), y1 = *reinterpret_cast<const float4*>(&sp[u][4]);
+        const float y[NR] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+        for (int c = 0; c < NR; ++c) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[c][k] = fmaf(y[c], x[k], acc[c][k]);
+        }
+      }
+    }
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(skv);
+#pragma unroll
+    for (int c = 0; c < NR; ++c)
+      *reinterpret_cast<float4*>(red + ((tg * NR + c) * D + wi * 4)) = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
+    __syncthreads();
+    const bool whole = g.n == g.nt;
+    float* slot = whole ? nullptr : slot_of<NR, D>(p, 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0));
+    if (!whole && tid < NR) slot[tid] = sm[tid], slot[NR + tid] = sl[tid];
+    for (int e = tid; e < NR * D; e += 128) {
+      const int c = e / D, d = e % D, f = g.f0 + c;
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < NG; ++k) v += red[(k * NR + c) * D + d];
+      if (!whole) {
+        slot[2 * NR + e] = v;
+      } else if (f < g.rows * p.G) {
+        const long long idx = (long long)(g.row0 + f / p.G) * p.Hq + g.h * p.G + f % p.G;
+        const Coef r = row_coef(p, idx, sm[c] == ninf ? 0.f : sm[c], sl[c], g.bad);
+        finish<E, D>(p, idx, d, v, r);
+        if (d == 0) finish_lse(p, idx, r);
+      }
+    }
+  }
+  if (bits) atomicOr(p.status, bits);
+}
+
+}  // namespace sv

@@ -1,0 +1,361 @@
+// Host entry points of the C ABI declared in include/spec_kv.h: argument checks, workspace
+// layout and launches of the cache's write and read-back and of the attention over it.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "kernels_attn.cuh"
+#include "kernels_kv.cuh"
+#include "spec_kv.h"
+
+#include <nvtx3/nvToolsExt.h>
+
+#include <atomic>
+
+namespace sv {
+namespace {
+
+struct KvRange {
+  explicit KvRange(const char* name) { nvtxRangePushA(name); }
+  ~KvRange() { nvtxRangePop(); }
+  KvRange(const KvRange&) = delete;
+  KvRange& operator=(const KvRange&) = delete;
+};
+
+inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+inline bool on(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
+
+int page_shift_of(int page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+spec_status check_cache(const spec_kv_cache& c) {
+  if (c.num_pages < 1 || page_shift_of(c.page_size) < 0 || c.kv_heads < 1 || c.kv_heads > 256 ||
+      (c.head_dim != 64 && c.head_dim != 128))
+    return SPEC_ERR_INVALID_ARG;
+  if (!c.k || !c.v || !c.k_exp || !c.v_exp) return SPEC_ERR_INVALID_ARG;
+  if (!on(c.k, 16) || !on(c.v, 16) || !on(c.k_exp, 16) || !on(c.v_exp, 16)) return SPEC_ERR_INVALID_ARG;
+  return SPEC_OK;
+}
+
+spec_status check_rows(const spec_kv_rows& r) {
+  if (r.rows < 0 || r.sequences < 0 || r.pages_per_seq < 0 || r.rows > (1 << 30)) return SPEC_ERR_INVALID_ARG;
+  if (r.rows == 0) return SPEC_OK;
+  if (!r.row_seq || !r.row_pos || (r.sequences > 0 && r.pages_per_seq > 0 && !r.page_table)) return SPEC_ERR_INVALID_ARG;
+  if (!on(r.row_seq, 4) || !on(r.row_pos, 4) || !on(r.page_table, 4)) return SPEC_ERR_INVALID_ARG;
+  return SPEC_OK;
+}
+
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const bool cached = dev >= 0 && dev < 64;
+  int n = cached ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (cached) known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// A launch with programmatic stream serialisation: the kernel may start while its
+// predecessor drains, and waits for it before it touches memory.
+template <typename... Args>
+cudaError_t start(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+KvParams kv_params(const spec_kv_cache& c, const spec_kv_rows& r, uint32_t* status) {
+  KvParams p;
+  memset(&p, 0, sizeof(p));
+  p.k = static_cast<uint8_t*>(c.k);
+  p.v = static_cast<uint8_t*>(c.v);
+  p.k_exp = c.k_exp;
+  p.v_exp = c.v_exp;
+  p.num_pages = c.num_pages;
+  p.page_shift = page_shift_of(c.page_size);
+  p.Hk = c.kv_heads;
+  p.rows = r.rows;
+  p.seqs = r.sequences;
+  p.pps = r.pages_per_seq;
+  p.table = r.page_table;
+  p.row_seq = r.row_seq;
+  p.row_pos = r.row_pos;
+  p.status = status;
+  return p;
+}
+
+// Blocks of the append and the read: all vectors at once up to 16 blocks an SM.
+unsigned kv_grid(const KvParams& p, int D) {
+  const long long need = cdiv((long long)p.rows * 2 * p.Hk, kKvThreads / (D / 8));
+  const long long most = 16LL * sm_count();
+  return (unsigned)(need < most ? need : most);
+}
+
+template <typename E, int D>
+cudaError_t launch_append(const KvParams& p, bool vec, cudaStream_t s) {
+  return vec ? start(kv_append_kernel<E, D, true>, dim3(kv_grid(p, D)), kKvThreads, 0, s, p)
+             : start(kv_append_kernel<E, D, false>, dim3(kv_grid(p, D)), kKvThreads, 0, s, p);
+}
+
+// ---------------------------------------------------------------------------
+// attention
+
+constexpr int kMaxGridS = 1024;  // largest grid of the 32-bit kernel (its workspace is sized for it)
+
+struct AttnLayout {
+  long long grid;      // blocks of the pass over the sequences' tokens, at most
+  long long pre_grid;  // of the prefix pass
+  size_t part, pre_o, pre_lse, total;
+};
+
+long long rows_of(const spec_attn_batch& g) { return (long long)g.total_draft + g.B; }
+
+AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, int nr, long long cap) {
+  AttnLayout L;
+  const int G = g.q_heads / c.kv_heads;
+  const long long most_tiles = cdiv((long long)g.pages_per_seq * c.page_size, kTile);
+  const long long nt = most_tiles > 1 ? most_tiles : 1;
+  const long long own = (long long)g.B * cdiv((long long)(g.gamma + 1) * G, nr) * c.kv_heads * nt;
+  const long long pre = g.prefix_len > 0 ? cdiv(rows_of(g) * G, nr) * c.kv_heads * cdiv(g.prefix_len, kTile) : 0;
+  L.grid = own < cap ? own : cap;
+  L.pre_grid = pre < cap ? pre : cap;
+  const long long slots = 2 * (L.grid > L.pre_grid ? L.grid : L.pre_grid);
+  size_t off = 0;
+  L.part = off;
+  off = up256(off + sizeof(float) * (size_t)slots * nr * (c.head_dim + 2));
+  L.pre_o = off;
+  if (g.prefix_len > 0) off = up256(off + sizeof(float) * (size_t)rows_of(g) * g.q_heads * c.head_dim);
+  L.pre_lse = off;
+  if (g.prefix_len > 0) off = up256(off + sizeof(float) * (size_t)rows_of(g) * g.q_heads);
+  L.total = off;
+  return L;
+}
+
+spec_status check_attn(const spec_attn_batch& g, const spec_kv_cache& c) {
+  const spec_status e = check_cache(c);
+  if (e != SPEC_OK) return e;
+  if (g.B < 0 || g.gamma < 0 || g.gamma > SPEC_MAX_GAMMA || g.total_draft < 0) return SPEC_ERR_INVALID_ARG;
+  if (g.cu_draft == nullptr && (long long)g.B * g.gamma != g.total_draft) return SPEC_ERR_INVALID_ARG;
+  if ((long long)g.total_draft > (long long)g.B * g.gamma) return SPEC_ERR_INVALID_ARG;
+  if (g.q_heads < 1 || g.q_heads % c.kv_heads != 0 || g.q_heads / c.kv_heads > 64) return SPEC_ERR_INVALID_ARG;
+  // flat rows (row * group + head) and row indices stay inside int
+  if (rows_of(g) * g.q_heads > (1LL << 30)) return SPEC_ERR_INVALID_ARG;
+  if (g.pages_per_seq < 0 || (long long)g.pages_per_seq * c.page_size > (1LL << 30)) return SPEC_ERR_INVALID_ARG;
+  if (g.prefix_len < 0 || g.prefix_len > (1 << 30)) return SPEC_ERR_INVALID_ARG;
+  if (!(g.scale > 0.f) || !isfinite(g.scale)) return SPEC_ERR_INVALID_ARG;
+  if (g.parent != nullptr) {
+    if (g.cu_draft != nullptr || g.gamma < 1 || g.gamma > SPEC_MAX_TREE_NODES) return SPEC_ERR_INVALID_ARG;
+    for (int j = 0; j < g.gamma; ++j)
+      if (g.parent[j] < -1 || g.parent[j] >= j) return SPEC_ERR_INVALID_ARG;
+  }
+  return SPEC_OK;
+}
+
+AttnParams attn_params(const spec_attn_batch& g, const spec_kv_cache& c, const void* q, int64_t q_row, int64_t q_head,
+                       void* o, float* lse, uint32_t* status) {
+  AttnParams p;
+  memset(&p, 0, sizeof(p));
+  p.k = static_cast<const uint8_t*>(c.k);
+  p.v = static_cast<const uint8_t*>(c.v);
+  p.k_exp = c.k_exp;
+  p.v_exp = c.v_exp;
+  p.num_pages = c.num_pages;
+  p.page_shift = page_shift_of(c.page_size);
+  p.Hk = c.kv_heads;
+  p.Hq = g.q_heads;
+  p.G = g.q_heads / c.kv_heads;
+  p.q = q;
+  p.q_row = q_row;
+  p.q_head = q_head;
+  p.B = g.B;
+  p.gamma = g.gamma;
+  p.total_draft = g.total_draft;
+  p.R = (int)rows_of(g);
+  p.cu = g.cu_draft;
+  p.table = g.page_table;
+  p.pps = g.pages_per_seq;
+  p.kv_len = g.kv_len;
+  p.mask = g.parent != nullptr ? A_TREE : A_CHAIN;
+  p.c = g.scale * 1.4426950408889634f;
+  p.o = o;
+  p.lse = lse;
+  p.status = status;
+  if (g.parent != nullptr)
+    for (int i = 0; i < g.gamma; ++i)
+      for (int j = i; j >= 0; j = g.parent[j]) p.sees[j] |= 1ull << i;
+  return p;
+}
+
+// The prefix as one sequence whose rows are all rows of the batch.
+AttnParams prefix_params(const AttnParams& own, const spec_attn_batch& g, const spec_kv_cache& c, float* pre_o,
+                         float* pre_lse) {
+  AttnParams p = own;
+  p.B = 1;
+  p.gamma = own.R - 1;
+  p.total_draft = own.R - 1;
+  p.cu = nullptr;
+  p.table = g.prefix_table;
+  p.pps = (int)cdiv(g.prefix_len, c.page_size);
+  p.kv_len = nullptr;
+  p.fixed_len = g.prefix_len;
+  p.mask = A_ALL;
+  p.dst_o = pre_o;
+  p.dst_lse = pre_lse;
+  return p;
+}
+
+template <typename E, int D, int NR>
+cudaError_t launch_merge(const AttnParams& p, int grid, cudaStream_t s) {
+  if (grid < 2) return cudaSuccess;
+  return start(attn_merge_kernel<E, D, NR>, dim3((unsigned)(grid - 1), cdiv(NR, 4)), 128, 0, s, p, grid);
+}
+
+// One wave of the 32-bit kernel on the current device.
+template <typename E, int D>
+long long f32_wave() {
+  static std::atomic<int> per_sm{0};
+  int n = per_sm.load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_f32_kernel<E, D>, 128, 0) != cudaSuccess || n < 1) return 0;
+    per_sm.store(n, std::memory_order_relaxed);
+  }
+  const long long w = (long long)n * sm_count();
+  return w < kMaxGridS ? w : kMaxGridS;
+}
+
+template <typename E, int D>
+cudaError_t pass_f32(const AttnParams& p, long long grid, cudaStream_t s) {
+  const long long wave = f32_wave<E, D>();
+  if (wave < 1) return cudaErrorInvalidConfiguration;
+  const int n = (int)(grid < wave ? grid : wave);
+  const cudaError_t e = start(attn_f32_kernel<E, D>, dim3((unsigned)n), 128, 0, s, p);
+  return e != cudaSuccess ? e : launch_merge<E, D, kRowsS>(p, n, s);
+}
+
+template <typename E>
+cudaError_t pass_f32_d(int D, const AttnParams& p, long long grid, cudaStream_t s) {
+  return D == 64 ? pass_f32<E, 64>(p, grid, s) : pass_f32<E, 128>(p, grid, s);
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" {
+
+spec_status spec_kv_append(spec_kv_cache c, spec_kv_rows r, spec_dtype dtype, const void* k, int64_t k_row_stride,
+                           int64_t k_head_stride, const void* v, int64_t v_row_stride, int64_t v_head_stride,
+                           uint32_t* device_status, spec_stream_t stream_) {
+  const KvRange range("spec_kv_append");
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
+  spec_status e = check_cache(c);
+  if (e != SPEC_OK) return e;
+  if ((e = check_rows(r)) != SPEC_OK) return e;
+  if (!device_status || !on(device_status, 4)) return SPEC_ERR_INVALID_ARG;
+  if (r.rows == 0) return SPEC_OK;
+  const size_t es = dtype == SPEC_BF16 ? 2 : 4;
+  if (!k || !v || !on(k, es) || !on(v, es)) return SPEC_ERR_INVALID_ARG;
+  if (k_row_stride < 0 || k_head_stride < 0 || v_row_stride < 0 || v_head_stride < 0) return SPEC_ERR_INVALID_ARG;
+  KvParams p = kv_params(c, r, device_status);
+  p.src_k = k;
+  p.src_v = v;
+  p.k_row = k_row_stride;
+  p.k_head = k_head_stride;
+  p.v_row = v_row_stride;
+  p.v_head = v_head_stride;
+  const long long per = 16 / (long long)es;
+  const bool vec = on(k, 16) && on(v, 16) && k_row_stride % per == 0 && k_head_stride % per == 0 &&
+                   v_row_stride % per == 0 && v_head_stride % per == 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  cudaError_t err;
+  if (dtype == SPEC_BF16)
+    err = c.head_dim == 64 ? launch_append<uint16_t, 64>(p, vec, s) : launch_append<uint16_t, 128>(p, vec, s);
+  else
+    err = c.head_dim == 64 ? launch_append<float, 64>(p, vec, s) : launch_append<float, 128>(p, vec, s);
+  return err == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+spec_status spec_kv_read(spec_kv_cache c, spec_kv_rows r, spec_dtype dtype, void* k_out, void* v_out,
+                         uint32_t* device_status, spec_stream_t stream_) {
+  const KvRange range("spec_kv_read");
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
+  spec_status e = check_cache(c);
+  if (e != SPEC_OK) return e;
+  if ((e = check_rows(r)) != SPEC_OK) return e;
+  if (!device_status || !on(device_status, 4) || !on(k_out, 16) || !on(v_out, 16)) return SPEC_ERR_INVALID_ARG;
+  if (r.rows == 0 || (!k_out && !v_out)) return SPEC_OK;
+  KvParams p = kv_params(c, r, device_status);
+  p.dst_k = k_out;
+  p.dst_v = v_out;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  const dim3 grid(kv_grid(p, c.head_dim));
+  cudaError_t err;
+  if (dtype == SPEC_BF16)
+    err = c.head_dim == 64 ? start(kv_read_kernel<uint16_t, 64>, grid, kKvThreads, 0, s, p)
+                           : start(kv_read_kernel<uint16_t, 128>, grid, kKvThreads, 0, s, p);
+  else
+    err = c.head_dim == 64 ? start(kv_read_kernel<float, 64>, grid, kKvThreads, 0, s, p)
+                           : start(kv_read_kernel<float, 128>, grid, kKvThreads, 0, s, p);
+  return err == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+size_t spec_attention_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype) {
+  if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || check_attn(g, c) != SPEC_OK) return 0;
+  return attn_layout(g, c, kRowsS, kMaxGridS).total;
+}
+
+spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,
+                           int64_t q_head_stride, void* o, float* lse, uint32_t* device_status, void* workspace,
+                           size_t workspace_bytes, spec_stream_t stream_) {
+  const KvRange range("spec_attention");
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
+  const spec_status e = check_attn(g, c);
+  if (e != SPEC_OK) return e;
+  if (!device_status || !on(device_status, 4)) return SPEC_ERR_INVALID_ARG;
+  if (g.B == 0) return SPEC_OK;
+  const size_t es = dtype == SPEC_BF16 ? 2 : 4;
+  if (!q || !o || !on(q, es) || !on(o, 16) || !on(lse, 4) || q_row_stride < 0 || q_head_stride < 0)
+    return SPEC_ERR_INVALID_ARG;
+  if (!g.kv_len || !on(g.kv_len, 4) || !on(g.cu_draft, 4)) return SPEC_ERR_INVALID_ARG;
+  if ((g.pages_per_seq > 0 && !g.page_table) || !on(g.page_table, 4)) return SPEC_ERR_INVALID_ARG;
+  if ((g.prefix_len > 0 && !g.prefix_table) || !on(g.prefix_table, 4)) return SPEC_ERR_INVALID_ARG;
+  const AttnLayout L = attn_layout(g, c, kRowsS, kMaxGridS);
+  if (!workspace || workspace_bytes < L.total || !on(workspace, 256)) return SPEC_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  AttnParams p = attn_params(g, c, q, q_row_stride, q_head_stride, o, lse, device_status);
+  p.part = reinterpret_cast<float*>(ws + L.part);
+  cudaError_t err = cudaSuccess;
+  if (g.prefix_len > 0) {
+    float* pre_o = reinterpret_cast<float*>(ws + L.pre_o);
+    float* pre_lse = reinterpret_cast<float*>(ws + L.pre_lse);
+    const AttnParams pp = prefix_params(p, g, c, pre_o, pre_lse);
+    err = dtype == SPEC_BF16 ? pass_f32_d<uint16_t>(c.head_dim, pp, L.pre_grid, s)
+                             : pass_f32_d<float>(c.head_dim, pp, L.pre_grid, s);
+    if (err != cudaSuccess) return SPEC_ERR_CUDA;
+    p.pre_o = pre_o;
+    p.pre_lse = pre_lse;
+  }
+  err = dtype == SPEC_BF16 ? pass_f32_d<uint16_t>(c.head_dim, p, L.grid, s) : pass_f32_d<float>(c.head_dim, p, L.grid, s);
+  return err == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // extern "C"
