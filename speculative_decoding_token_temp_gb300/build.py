@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libspecverify.so")
 LIB_BOUNDS = os.path.join(PKG, "libspecverify_bounds.so")
 SOURCES = ["spec_verify.cu", "spec_kv.cu"]
 HEADERS = ["kernels.cuh", "kernels_rows.cuh", "kernels_sample.cuh", "kernels_multi.cuh", "plan.h",
-           "kernels_kv.cuh", "kernels_attn.cuh"]
+           "kernels_kv.cuh", "kernels_attn.cuh", "kernels_attn_tc.cuh"]
 PUBLIC = ["spec_verify.h", "spec_kv.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

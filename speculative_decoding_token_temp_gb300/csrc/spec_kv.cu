@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "kernels_attn.cuh"
+#include "kernels_attn_tc.cuh"
 #include "kernels_kv.cuh"
 #include "spec_kv.h"
 
@@ -119,7 +120,10 @@ cudaError_t launch_append(const KvParams& p, bool vec, cudaStream_t s) {
 
 constexpr int kMaxGridS = 1024;  // largest grid of the 32-bit kernel (its workspace is sized for it)
 
+constexpr int kMaxGridT = 256;   // of the tensor-core kernel (one block an SM)
+
 struct AttnLayout {
+  int nr, pre_nr;      // rows of a row block, of the two passes
   long long grid;      // blocks of the pass over the sequences' tokens, at most
   long long pre_grid;  // of the prefix pass
   size_t part, pre_o, pre_lse, total;
@@ -127,19 +131,31 @@ struct AttnLayout {
 
 long long rows_of(const spec_attn_batch& g) { return (long long)g.total_draft + g.B; }
 
-AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, int nr, long long cap) {
+// Rows of a row block of the tensor-core kernel, for `flat` rows that share keys: as few
+// blocks of up to 64 as hold them, each as small as that allows in steps of 16 (the MMAs'
+// columns, and what a softmax thread does, are in proportion).
+int tc_rows(long long flat) {
+  const long long per = cdiv(flat, cdiv(flat, 64));
+  return (int)(cdiv(per, 16) * 16);
+}
+
+AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype) {
   AttnLayout L;
   const int G = g.q_heads / c.kv_heads;
+  const bool tc = dtype == SPEC_BF16;
+  const long long cap = tc ? kMaxGridT : kMaxGridS;
+  L.nr = tc ? tc_rows((long long)(g.gamma + 1) * G) : kRowsS;
+  L.pre_nr = tc && rows_of(g) > 0 ? tc_rows(rows_of(g) * G) : kRowsS;
   const long long most_tiles = cdiv((long long)g.pages_per_seq * c.page_size, kTile);
   const long long nt = most_tiles > 1 ? most_tiles : 1;
-  const long long own = (long long)g.B * cdiv((long long)(g.gamma + 1) * G, nr) * c.kv_heads * nt;
-  const long long pre = g.prefix_len > 0 ? cdiv(rows_of(g) * G, nr) * c.kv_heads * cdiv(g.prefix_len, kTile) : 0;
+  const long long own = (long long)g.B * cdiv((long long)(g.gamma + 1) * G, L.nr) * c.kv_heads * nt;
+  const long long pre = g.prefix_len > 0 ? cdiv(rows_of(g) * G, L.pre_nr) * c.kv_heads * cdiv(g.prefix_len, kTile) : 0;
   L.grid = own < cap ? own : cap;
   L.pre_grid = pre < cap ? pre : cap;
-  const long long slots = 2 * (L.grid > L.pre_grid ? L.grid : L.pre_grid);
+  const long long slot_rows = L.grid * L.nr > L.pre_grid * L.pre_nr ? L.grid * L.nr : L.pre_grid * L.pre_nr;
   size_t off = 0;
   L.part = off;
-  off = up256(off + sizeof(float) * (size_t)slots * nr * (c.head_dim + 2));
+  off = up256(off + sizeof(float) * (size_t)(2 * slot_rows) * (c.head_dim + 2));
   L.pre_o = off;
   if (g.prefix_len > 0) off = up256(off + sizeof(float) * (size_t)rows_of(g) * g.q_heads * c.head_dim);
   L.pre_lse = off;
@@ -249,9 +265,78 @@ cudaError_t pass_f32(const AttnParams& p, long long grid, cudaStream_t s) {
   return e != cudaSuccess ? e : launch_merge<E, D, kRowsS>(p, n, s);
 }
 
-template <typename E>
-cudaError_t pass_f32_d(int D, const AttnParams& p, long long grid, cudaStream_t s) {
-  return D == 64 ? pass_f32<E, 64>(p, grid, s) : pass_f32<E, 128>(p, grid, s);
+// The cache's codes of one operand as a tensor of pages: a TMA load takes one page's tokens
+// of one kv head (at most a tile of them), its rows swizzled as the MMAs read them.
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::atomic<EncodeFn> known{nullptr};
+  EncodeFn f = known.load(std::memory_order_acquire);
+  if (f == nullptr) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+        how != cudaDriverEntryPointSuccess)
+      return nullptr;
+    f = reinterpret_cast<EncodeFn>(ptr);
+    known.store(f, std::memory_order_release);
+  }
+  return f;
+}
+
+bool page_map(CUtensorMap* m, const void* codes, const spec_kv_cache& c) {
+  const EncodeFn f = encode_fn();
+  if (f == nullptr) return false;
+  const cuuint64_t D = (cuuint64_t)c.head_dim, S = (cuuint64_t)c.page_size, H = (cuuint64_t)c.kv_heads;
+  const cuuint64_t dims[4] = {D, S, H, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {D, S * D, H * S * D};
+  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(S < kTile ? S : kTile), 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box, ones,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+  CUtensorMap k, v;
+};
+
+template <int D, int NR>
+cudaError_t pass_tc(const AttnParams& p, long long grid, const Maps& m, cudaStream_t s) {
+  auto kern = attn_tc_kernel<D, NR>;
+  static std::atomic<unsigned long long> done{0};  // a bit a device: the kernel may use its shared memory there
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const long long sms = sm_count();
+  if (sms < 1) return cudaErrorInvalidConfiguration;
+  const int n = (int)(grid < sms ? grid : sms);
+  e = start(kern, dim3((unsigned)n), kTcThreads, TcShape<D>::kSmem, s, p, m.k, m.v);
+  return e != cudaSuccess ? e : launch_merge<uint16_t, D, NR>(p, n, s);
+}
+
+template <int D>
+cudaError_t pass_tc_nr(int nr, const AttnParams& p, long long grid, const Maps& m, cudaStream_t s) {
+  switch (nr) {
+    case 16: return pass_tc<D, 16>(p, grid, m, s);
+    case 32: return pass_tc<D, 32>(p, grid, m, s);
+    case 48: return pass_tc<D, 48>(p, grid, m, s);
+    default: return pass_tc<D, 64>(p, grid, m, s);
+  }
+}
+
+// One pass over keys: fp32 queries on the 32-bit kernel, bf16 queries on the tensor cores.
+cudaError_t attn_pass(spec_dtype dtype, int D, int nr, const AttnParams& p, long long grid, const Maps& m, cudaStream_t s) {
+  if (dtype == SPEC_F32) return D == 64 ? pass_f32<float, 64>(p, grid, s) : pass_f32<float, 128>(p, grid, s);
+  return D == 64 ? pass_tc_nr<64>(nr, p, grid, m, s) : pass_tc_nr<128>(nr, p, grid, m, s);
 }
 
 }  // namespace
@@ -319,7 +404,7 @@ spec_status spec_kv_read(spec_kv_cache c, spec_kv_rows r, spec_dtype dtype, void
 
 size_t spec_attention_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype) {
   if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || check_attn(g, c) != SPEC_OK) return 0;
-  return attn_layout(g, c, kRowsS, kMaxGridS).total;
+  return attn_layout(g, c, dtype).total;
 }
 
 spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,
@@ -337,24 +422,26 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
   if (!g.kv_len || !on(g.kv_len, 4) || !on(g.cu_draft, 4)) return SPEC_ERR_INVALID_ARG;
   if ((g.pages_per_seq > 0 && !g.page_table) || !on(g.page_table, 4)) return SPEC_ERR_INVALID_ARG;
   if ((g.prefix_len > 0 && !g.prefix_table) || !on(g.prefix_table, 4)) return SPEC_ERR_INVALID_ARG;
-  const AttnLayout L = attn_layout(g, c, kRowsS, kMaxGridS);
+  const AttnLayout L = attn_layout(g, c, dtype);
   if (!workspace || workspace_bytes < L.total || !on(workspace, 256)) return SPEC_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   AttnParams p = attn_params(g, c, q, q_row_stride, q_head_stride, o, lse, device_status);
   p.part = reinterpret_cast<float*>(ws + L.part);
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (dtype == SPEC_BF16 && (!page_map(&maps.k, c.k, c) || !page_map(&maps.v, c.v, c))) return SPEC_ERR_CUDA;
   cudaError_t err = cudaSuccess;
   if (g.prefix_len > 0) {
     float* pre_o = reinterpret_cast<float*>(ws + L.pre_o);
     float* pre_lse = reinterpret_cast<float*>(ws + L.pre_lse);
     const AttnParams pp = prefix_params(p, g, c, pre_o, pre_lse);
-    err = dtype == SPEC_BF16 ? pass_f32_d<uint16_t>(c.head_dim, pp, L.pre_grid, s)
-                             : pass_f32_d<float>(c.head_dim, pp, L.pre_grid, s);
+    err = attn_pass(dtype, c.head_dim, L.pre_nr, pp, L.pre_grid, maps, s);
     if (err != cudaSuccess) return SPEC_ERR_CUDA;
     p.pre_o = pre_o;
     p.pre_lse = pre_lse;
   }
-  err = dtype == SPEC_BF16 ? pass_f32_d<uint16_t>(c.head_dim, p, L.grid, s) : pass_f32_d<float>(c.head_dim, p, L.grid, s);
+  err = attn_pass(dtype, c.head_dim, L.nr, p, L.grid, maps, s);
   return err == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
