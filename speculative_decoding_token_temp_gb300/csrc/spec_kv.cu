@@ -120,7 +120,7 @@ cudaError_t launch_append(const KvParams& p, bool vec, cudaStream_t s) {
 
 constexpr int kMaxGridS = 1024;  // largest grid of the 32-bit kernel (its workspace is sized for it)
 
-constexpr int kMaxGridT = 256;   // of the tensor-core kernel (one block an SM)
+constexpr int kMaxGridT = 512;   // of the tensor-core kernel (two blocks an SM)
 
 struct AttnLayout {
   int nr, pre_nr;      // rows of a row block, of the two passes
@@ -132,10 +132,11 @@ struct AttnLayout {
 long long rows_of(const spec_attn_batch& g) { return (long long)g.total_draft + g.B; }
 
 // Rows of a row block of the tensor-core kernel, for `flat` rows that share keys: as few
-// blocks of up to 64 as hold them, each as small as that allows in steps of 16 (the MMAs'
-// columns, and what a softmax thread does, are in proportion).
-int tc_rows(long long flat) {
-  const long long per = cdiv(flat, cdiv(flat, 64));
+// blocks as hold them, each as small as that allows in steps of 16 (the MMAs' columns, and
+// what a softmax thread does, are in proportion). A block's accumulators take 5 columns of
+// tensor memory a row, 8 with head_dim 64, of 256 a group.
+int tc_rows(long long flat, int head_dim) {
+  const long long per = cdiv(flat, cdiv(flat, head_dim == 64 ? 32 : 48));
   return (int)(cdiv(per, 16) * 16);
 }
 
@@ -144,8 +145,8 @@ AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dt
   const int G = g.q_heads / c.kv_heads;
   const bool tc = dtype == SPEC_BF16;
   const long long cap = tc ? kMaxGridT : kMaxGridS;
-  L.nr = tc ? tc_rows((long long)(g.gamma + 1) * G) : kRowsS;
-  L.pre_nr = tc && rows_of(g) > 0 ? tc_rows(rows_of(g) * G) : kRowsS;
+  L.nr = tc ? tc_rows((long long)(g.gamma + 1) * G, c.head_dim) : kRowsS;
+  L.pre_nr = tc && rows_of(g) > 0 ? tc_rows(rows_of(g) * G, c.head_dim) : kRowsS;
   const long long most_tiles = cdiv((long long)g.pages_per_seq * c.page_size, kTile);
   const long long nt = most_tiles > 1 ? most_tiles : 1;
   const long long own = (long long)g.B * cdiv((long long)(g.gamma + 1) * G, L.nr) * c.kv_heads * nt;
@@ -312,25 +313,24 @@ cudaError_t pass_tc(const AttnParams& p, long long grid, const Maps& m, cudaStre
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (!(done.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D, NR>::kSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
   const long long sms = sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
-  const int n = (int)(grid < sms ? grid : sms);
-  e = start(kern, dim3((unsigned)n), kTcThreads, TcShape<D>::kSmem, s, p, m.k, m.v);
+  const int n = (int)(grid < 2 * sms ? grid : 2 * sms);
+  e = start(kern, dim3((unsigned)n), kTcThreads, TcShape<D, NR>::kSmem, s, p, m.k, m.v);
   return e != cudaSuccess ? e : launch_merge<uint16_t, D, NR>(p, n, s);
 }
 
 template <int D>
 cudaError_t pass_tc_nr(int nr, const AttnParams& p, long long grid, const Maps& m, cudaStream_t s) {
-  switch (nr) {
-    case 16: return pass_tc<D, 16>(p, grid, m, s);
-    case 32: return pass_tc<D, 32>(p, grid, m, s);
-    case 48: return pass_tc<D, 48>(p, grid, m, s);
-    default: return pass_tc<D, 64>(p, grid, m, s);
+  if (nr == 16) return pass_tc<D, 16>(p, grid, m, s);
+  if constexpr (D == 128) {
+    if (nr == 48) return pass_tc<D, 48>(p, grid, m, s);
   }
+  return pass_tc<D, 32>(p, grid, m, s);
 }
 
 // One pass over keys: fp32 queries on the 32-bit kernel, bf16 queries on the tensor cores.
