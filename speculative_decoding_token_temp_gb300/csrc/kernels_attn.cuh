@@ -38,6 +38,7 @@ struct AttnParams {
   const int32_t* kv_len;  // null: every sequence has fixed_len tokens
   int fixed_len;
   int mask;
+  int seg_cost;             // tiles that a segment's beginning and end count for
   float c;                  // scale * log2(e)
   float* part;              // the parts of cut segments: two slots a block
   long long part_floats;
@@ -72,10 +73,10 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
 
 __device__ __forceinline__ int seq_ntiles(const SeqInfo& s) { return s.len > 0 ? (s.len - 1) / kTile + 1 : 1; }
 
-// Tiles of sequence b over all its row blocks and kv heads.
+// Tiles on the line of a sequence, over all its row blocks and kv heads.
 template <int NR>
 __device__ __forceinline__ long long seq_tiles(const AttnParams& p, const SeqInfo& s) {
-  return (long long)((s.rows * p.G + NR - 1) / NR) * p.Hk * seq_ntiles(s);
+  return (long long)((s.rows * p.G + NR - 1) / NR) * p.Hk * (seq_ntiles(s) + p.seg_cost);
 }
 
 // A place on the line of tiles: sequence b, tile `off` of it.
@@ -162,23 +163,25 @@ struct Seg {
   bool bad;
 };
 
-// The next stretch at `at` (advanced), at most `left` tiles (reduced).
+// The next stretch at `at` (advanced), at most `left` tiles of the line (reduced). It may
+// be empty (n = 0): the block's part of the line ends among the tiles that only count.
 template <int NR>
 __device__ __forceinline__ Seg next_seg(const AttnParams& p, Place& at, long long& left) {
   Seg g;
   const SeqInfo s = seq_info(p, at.b);
   g.row0 = s.row0, g.rows = s.rows, g.len = s.len, g.bad = s.bad;
   g.nt = seq_ntiles(s);
-  const int nrb = (s.rows * p.G + NR - 1) / NR;
-  const int seg = (int)(at.off / g.nt);
-  g.t0 = (int)(at.off - (long long)seg * g.nt);
+  const int nrb = (s.rows * p.G + NR - 1) / NR, line = g.nt + p.seg_cost;
+  const int seg = (int)(at.off / line), r = (int)(at.off - (long long)seg * line);
+  const int take = (int)min((long long)(line - r), left);
+  g.t0 = max(0, r - p.seg_cost);
+  g.n = max(0, r + take - p.seg_cost - g.t0);
   g.h = seg / nrb;
   g.f0 = (seg - g.h * nrb) * NR;
-  g.n = (int)min((long long)(g.nt - g.t0), left);
   g.pages = p.table + (long long)at.b * p.pps;
-  at.off += g.n;
-  left -= g.n;
-  if (at.off >= (long long)nrb * p.Hk * g.nt) {
+  at.off += take;
+  left -= take;
+  if (at.off >= (long long)nrb * p.Hk * line) {
     at.b += 1;
     at.off = 0;
   }
@@ -282,6 +285,7 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(AttnParams p, int grid)
   Place at = sh.at[1];
   long long left = 1;
   const Seg g = next_seg<NR>(p, at, left);
+  // the segment's own tiles on the line; a cut at or before the first does not divide it
   const long long first = cut - g.t0, last = first + g.nt;
   if (g.t0 == 0 || prev > first) return;
   const int c = blockIdx.y * 4 + (threadIdx.x >> 5), f = g.f0 + c;
@@ -365,6 +369,7 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
   uint32_t bits = 0;
   while (left > 0) {
     const Seg g = next_seg<NR>(p, at, left);
+    if (g.n == 0) continue;
     if (g.bad) bits |= SPEC_DEV_OFFSETS;
     __syncthreads();
     for (int e = tid; e < NR * D; e += 128) {

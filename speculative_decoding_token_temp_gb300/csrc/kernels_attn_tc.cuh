@@ -14,16 +14,16 @@
 //            absolute 2^-18 of it);
 //   weights  a weight rounded to f16 (11 bits) is exactly the sum of three parts (each the
 //            rest of the ones before, scaled by 16 and 256 in columns of its own), down to
-//            2^-18, where the largest weights of a row stand between 2^5 and 2^8: what is
-//            dropped of a flat tail is below 2^-23 of the largest weight a token.
+//            2^-18, where the largest weights of a row stand between 2^4 and 2^8: what is
+//            dropped of a flat tail is below 2^-22 of the largest weight a token.
 //
 //   Exponents: a key's is a factor of its token's scores, one lane's constant; a value's is
 //   added to the score before the exponential (weights are 2^(x + e - m)), so that the
 //   weighted values need no further scaling and no weight over- or underflows where values
 //   differ much in size; the sum takes it out again (2^-e).
 //
-// Four warps do the softmax: a thread is a token, its weights of all rows sit in its
-// registers. The maximum over tokens, which would cross lanes, is needed only when a score
+// Eight warps do the softmax: a thread is a token and half of the rows, whose weights sit
+// in its registers. The maximum over tokens, which would cross lanes, is needed only when a score
 // exceeds the row's reference by 2^8 (the first tile of a stretch, then rarely): the
 // reference is not the maximum itself but anything that keeps the weights in range. One
 // warp keeps rings of key and value tiles filled (a TMA load a page and operand; pages
@@ -41,9 +41,10 @@
 
 namespace sv {
 
-constexpr int kTcThreads = 192;        // four softmax warps, one for copies, one for MMAs
+constexpr int kTcThreads = 320;        // eight softmax warps, one for copies, one for MMAs
+constexpr int kTcSoft = 256;
 constexpr int kTcPollLimit = 1 << 18;  // bounded waits (SPEC_DEV_TIMEOUT): about a second
-constexpr float kTop = 5.f;            // a fresh reference puts the largest weight at 2^5 ...
+constexpr float kTop = 4.f;            // a fresh reference puts the largest weight at 2^4 ...
 constexpr float kOver = 8.f;           // ... and is renewed when one would pass 2^8 (e4m3 ends at 448)
 
 template <int D, int NR>
@@ -95,19 +96,15 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(a));
+__device__ __forceinline__ void tc_ld8(uint32_t a, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(a));
 }
-__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
-      : "memory");
+__device__ __forceinline__ void tc_st8(uint32_t a, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(a)
+               : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -203,25 +200,27 @@ __device__ __forceinline__ uint32_t rest16(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Sixteen columns of the values' sums: the three parts' accumulators joined.
+// Eight columns of the values' sums: the three parts' accumulators joined.
 template <int NR>
-__device__ __forceinline__ void tc_sum_parts(uint32_t at, float (&o)[16]) {
-  uint32_t a[16], b[16], c[16];
-  tc_ld16(at, a);
-  tc_ld16(at + NR, b);
-  tc_ld16(at + 2 * NR, c);
+__device__ __forceinline__ void tc_sum_parts(uint32_t at, float (&o)[8]) {
+  uint32_t a[8], b[8], c[8];
+  tc_ld8(at, a);
+  tc_ld8(at + NR, b);
+  tc_ld8(at + 2 * NR, c);
   tc_wait_ld();
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
+  for (int j = 0; j < 8; ++j)
     o[j] = fmaf(fmaf(__uint_as_float(c[j]), 0.0625f, __uint_as_float(b[j])), 0.0625f, __uint_as_float(a[j]));
 }
 
-// Sums over a warp of 16 columns held by every lane: lane c (mod 16) gets column c's.
-__device__ __forceinline__ float column_sums(float (&v)[16], int lane) {
+// Sums over a warp of 8 columns held by every lane: lane c (mod 8) gets column c's.
+__device__ __forceinline__ float column_sums(float (&v)[8], int lane) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(kFull, v[i], 16);
+  for (int o = 16; o >= 8; o >>= 1)
 #pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) {
+    for (int i = 0; i < 8; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -240,6 +239,7 @@ struct TcShared {
   uint32_t tmem;
   int gave_up;
   uint32_t bad_pages[T::kNK];
+  uint8_t nan_code[kTile];          // of a tile with masked places: the token's values hold a NaN code
   alignas(16) float rq[NR];         // a row's factor of the scores: scale * log2(e) * its power of two
   alignas(16) int row[NR];          // query row of a flat row
   alignas(16) float neg_m[NR];      // the reference, negated
@@ -255,7 +255,7 @@ struct TcShared {
 // has them.
 template <int D, int NR>
 __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g, TcShared<D, NR>& sh, uint8_t* q, int t) {
-  constexpr int TPR = NR == 16 ? 8 : NR == 32 ? 4 : 2, E = D / TPR;
+  constexpr int TPR = NR == 48 ? 4 : 8, E = D / TPR;
   const int c = t / TPR, part = t % TPR, f = g.f0 + c;
   const float nan = __int_as_float(0x7fffffff);
   if (c < NR) {  // (whole warps)
@@ -340,22 +340,22 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) {
       mbar_init(bar(sh.k_full[i]), 1);
-      mbar_init(bar(sh.k_free[i]), 5);  // the scores' MMA, and the softmax warps (exponents)
+      mbar_init(bar(sh.k_free[i]), 9);  // the scores' MMA, and the softmax warps (exponents)
     }
     for (int i = 0; i < NV; ++i) {
       mbar_init(bar(sh.v_full[i]), 1);
       mbar_init(bar(sh.v_free[i]), 1);
     }
-    mbar_init(bar(sh.q_full), 128);
+    mbar_init(bar(sh.q_full), kTcSoft);
     mbar_init(bar(sh.drained), 1);
     mbar_init(bar(sh.s_full), 1);
-    mbar_init(bar(sh.s_free), 4);
-    mbar_init(bar(sh.p_full), 4);
+    mbar_init(bar(sh.s_free), 8);
+    mbar_init(bar(sh.p_full), 8);
     mbar_init(bar(sh.o_done), 1);
     sh.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 5) {
+  if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(
                      (uint32_t)__cvta_generic_to_shared(&sh.tmem))
                  : "memory");
@@ -375,13 +375,14 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   Place at = sh.loc.at[0];
   long long left = end - begin;
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ---- the rings of tiles ----
     int gi = 0;
     uint32_t bits = 0;
     const int psz = 1 << p.page_shift, box = min(psz, kTile), np = kTile / box;
     while (left > 0) {
       const Seg g = next_seg<NR>(p, at, left);
+      if (g.n == 0) continue;
       if (g.bad) bits |= SPEC_DEV_OFFSETS;
       auto page_of = [&](int tile) -> int {  // of this lane's part of a tile
         const int t = tile * kTile + lane * box;
@@ -426,7 +427,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     for (int i = 0; i < NV; ++i)
       for (int it = 0; gi > i && it < kTcPollLimit && !mbar_try_wait(bar(sh.v_full[i]), ((gi - 1 - i) / NV) & 1); ++it) {
       }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ---- the MMAs: scores of the next tile, then weighted values of this one ----
     // The whole warp walks the tiles, so that descriptors and addresses stay warp-uniform; one elected lane issues.
     constexpr uint32_t id_s = mma_idesc(2 * NR, false), id_o = mma_idesc(3 * NR, true);
@@ -452,6 +453,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     };
     while (left > 0) {
       const int n = __shfl_sync(kFull, next_seg<NR>(p, at, left).n, 0);
+      if (n == 0) continue;
       tc_wait(bar(sh.q_full), nseg & 1, gave_up, p.status);
       ++nseg;
       scores(gi);
@@ -485,23 +487,25 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     for (int it = 0; it < kTcPollLimit && !mbar_try_wait(bar(sh.drained), 0); ++it) {
     }
   } else {
-    // ---- softmax: thread = token (lane of S^T) and element (lane of O^T) ----
-    const int t = tid;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    const uint32_t tS = tmem + lanes, tO = tmem + lanes + T::cO + (kHalves == 2 && warp >= 2 ? T::cHalf : 0);
+    // ---- softmax: thread = token (lane of S^T) and element (lane of O^T), half of the columns ----
+    constexpr int NH = NR / 2;
+    const int t = tid & 127, wl = warp & 3, c0 = (warp >> 2) * NH;
+    const uint32_t lanes = (uint32_t)(wl * 32) << 16;
+    const uint32_t tS = tmem + lanes + c0, tO = tmem + lanes + T::cO + (kHalves == 2 && wl >= 2 ? T::cHalf : 0) + c0;
     uint8_t* const pw = mem + T::oP + t * 16;
     const float nan = __int_as_float(0x7fffffff), ninf = __int_as_float(kNegInfBits);
     int gi = 0;
-    f2 l2[NR / 2];
+    f2 l2[NH / 2];
     while (left > 0) {
       const Seg g = next_seg<NR>(p, at, left);
+      if (g.n == 0) continue;
       const int flat = g.rows * p.G;
-      stage_queries<D, NR>(p, g, sh, mem + T::oQ, t);
+      stage_queries<D, NR>(p, g, sh, mem + T::oQ, tid);
       fence_async();
       mbar_arrive(bar(sh.q_full));
-      bar_sync(1, 128);  // rq, row and the references are seen by all
+      bar_sync(1, kTcSoft);  // rq, row and the references are seen by all
 #pragma unroll
-      for (int i = 0; i < NR / 2; ++i) l2[i] = 0ull;
+      for (int i = 0; i < NH / 2; ++i) l2[i] = 0ull;
       for (int k = 0; k < g.n; ++k, ++gi) {
         const int sk = gi % NK, tile = g.t0 + k, tok = tile * kTile + t;
         const bool first = k == 0;
@@ -517,21 +521,27 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           // what no row sees of this token's values is made zero, a NaN code too: 0 * NaN must not reach other rows;
           // the token is marked for the rows that see it
           const int sv = gi % NV;
-          tc_wait(bar(sh.v_full[sv]), (gi / NV) & 1, gave_up, p.status);
-          uint8_t* src = mem + T::oV + sv * T::kTileBytes + t * D;
-          const bool zero = !live || hurt;
+          if (c0 == 0) {
+            tc_wait(bar(sh.v_full[sv]), (gi / NV) & 1, gave_up, p.status);
+            uint8_t* src = mem + T::oV + sv * T::kTileBytes + t * D;
+            const bool zero = !live || hurt;
+            bool code = false;
+#pragma unroll 1
+            for (int ch = 0; ch < D / 16; ++ch) {
+              uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ t) & (D / 16 - 1)) * 16);
+              uint32_t* q = &v.x;
 #pragma unroll
-          for (int ch = 0; ch < D / 16; ++ch) {
-            uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ t) & (D / 16 - 1)) * 16);
-            uint32_t* q = &v.x;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t mk = __vcmpeq4(q[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              if (live && mk) hurt = true;
-              q[j] = zero ? 0u : q[j] & ~mk;
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t mk = __vcmpeq4(q[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                code |= mk != 0;
+                q[j] = zero ? 0u : q[j] & ~mk;
+              }
+              *reinterpret_cast<uint4*>(src + ((ch ^ t) & (D / 16 - 1)) * 16) = v;
             }
-            *reinterpret_cast<uint4*>(src + ((ch ^ t) & (D / 16 - 1)) * 16) = v;
+            sh.nan_code[t] = code;
           }
+          bar_sync(1, kTcSoft);
+          hurt |= sh.nan_code[t] != 0;
         }
         const bool fine = live && !hurt;
         const float ks = !live ? 0.f : hurt ? nan : exp_value(kb);
@@ -541,57 +551,51 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         // scores
         tc_wait(bar(sh.s_full), gi & 1, gave_up, p.status);
         tc_after();
-        f2 x[NR / 2];
+        f2 x[NH / 2];
         float most = ninf;
-        uint32_t hi[16], lo[16];
-        tc_ld16(tS, hi);
-        tc_ld16(tS + NR, lo);
+        uint32_t hi[NH / 8][8], lo[NH / 8][8];
 #pragma unroll
-        for (int c = 0; c < NR; c += 16) {
-          f2 s2[8];
-          tc_wait_ld();
+        for (int i = 0; i < NH / 8; ++i) {
+          tc_ld8(tS + i * 8, hi[i]);
+          tc_ld8(tS + NR + i * 8, lo[i]);
+        }
+        tc_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            s2[j] = add2(pack(__uint_as_float(hi[2 * j]), __uint_as_float(hi[2 * j + 1])),
-                         pack(__uint_as_float(lo[2 * j]), __uint_as_float(lo[2 * j + 1])));
-          if (c + 16 < NR) {  // the next columns arrive while these are worked on
-            tc_ld16(tS + c + 16, hi);
-            tc_ld16(tS + NR + c + 16, lo);
+        for (int c = 0; c < NH; c += 4) {
+          const float4 rq = *reinterpret_cast<const float4*>(&sh.rq[c0 + c]);
+          const float4 nm = *reinterpret_cast<const float4*>(&sh.neg_m[c0 + c]);
+          const uint32_t *a = &hi[c / 8][c % 8], *b = &lo[c / 8][c % 8];
+          const f2 s0 = add2(pack(__uint_as_float(a[0]), __uint_as_float(a[1])), pack(__uint_as_float(b[0]), __uint_as_float(b[1])));
+          const f2 s1 = add2(pack(__uint_as_float(a[2]), __uint_as_float(a[3])), pack(__uint_as_float(b[2]), __uint_as_float(b[3])));
+          f2 y0 = add2(fma2(mul2(s0, pack(rq.x, rq.y)), ks2, ev2), pack(nm.x, nm.y));
+          f2 y1 = add2(fma2(mul2(s1, pack(rq.z, rq.w)), ks2, ev2), pack(nm.z, nm.w));
+          float z[4];
+          unpack(y0, z[0], z[1]);
+          unpack(y1, z[2], z[3]);
+          if (masked) {
+            const int4 rows = *reinterpret_cast<const int4*>(&sh.row[c0 + c]);
+            const int ri[4] = {rows.x, rows.y, rows.z, rows.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (!(live && ri[q] < g.rows && sees(p, ri[q], g.rows, g.len, tok))) z[q] = ninf;
+            y0 = pack(z[0], z[1]);
+            y1 = pack(z[2], z[3]);
           }
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 rq = *reinterpret_cast<const float4*>(&sh.rq[c + j]);
-            const float4 nm = *reinterpret_cast<const float4*>(&sh.neg_m[c + j]);
-            f2 y0 = add2(fma2(mul2(s2[j / 2], pack(rq.x, rq.y)), ks2, ev2), pack(nm.x, nm.y));
-            f2 y1 = add2(fma2(mul2(s2[j / 2 + 1], pack(rq.z, rq.w)), ks2, ev2), pack(nm.z, nm.w));
-            float z[4];
-            unpack(y0, z[0], z[1]);
-            unpack(y1, z[2], z[3]);
-            if (masked) {
-              const int4 rows = *reinterpret_cast<const int4*>(&sh.row[c + j]);
-              const int ri[4] = {rows.x, rows.y, rows.z, rows.w};
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if (!(live && ri[q] < g.rows && sees(p, ri[q], g.rows, g.len, tok))) z[q] = ninf;
-              y0 = pack(z[0], z[1]);
-              y1 = pack(z[2], z[3]);
-            }
-            most = fmaxf(most, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
-            x[(c + j) / 2] = y0;
-            x[(c + j) / 2 + 1] = y1;
-          }
+          most = fmaxf(most, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
+          x[c / 2] = y0;
+          x[c / 2 + 1] = y1;
         }
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh.s_free));
-        if (bar_or(1, 128, first || most > kOver)) {
+        if (bar_or(1, kTcSoft, first || most > kOver)) {
           // new references: the maxima, over the warps' lanes, of the columns that need one
           const float over = first ? ninf : kOver;
 #pragma unroll
-          for (int c = 0; c < NR; c += 16) {
+          for (int c = 0; c < NH; c += 8) {
             float keep = ninf;
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
+            for (int j = 0; j < 8; j += 2) {
               float a, b;
               unpack(x[(c + j) / 2], a, b);
               if (__any_sync(kFull, fmaxf(a, b) > over)) {
@@ -601,51 +605,47 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
                 if (lane == j + 1) keep = b;
               }
             }
-            if (lane < 16) sh.red[warp][c + lane] = keep;
+            if (lane < 8) sh.red[wl][c0 + c + lane] = keep;
           }
-          bar_sync(1, 128);
-          if (warp < (NR + 31) / 32) {
+          bar_sync(1, kTcSoft);
+          if (tid < NR) {
             float d = 0.f;
-            if (t < NR) {
-              const float mx = fmaxf(fmaxf(sh.red[0][t], sh.red[1][t]), fmaxf(sh.red[2][t], sh.red[3][t]));
-              if (mx != ninf && (first || mx > kTop)) d = mx - kTop;
-              sh.delta[t] = -d;
-              sh.factor[t] = ex2(-d);
-              sh.neg_m[t] -= d;
-            }
+            const float mx = fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid]));
+            if (mx != ninf && (first || mx > kTop)) d = mx - kTop;
+            sh.delta[tid] = -d;
+            sh.factor[tid] = ex2(-d);
+            sh.neg_m[tid] -= d;
           }
-          bar_sync(1, 128);
+          bar_sync(1, kTcSoft);
           if (!first) {
             tc_wait(bar(sh.o_done), (gi - 1) & 1, gave_up, p.status);  // the accumulator holds the earlier tiles
             tc_after();
           }
 #pragma unroll
-          for (int c = 0; c < NR; c += 16) {
+          for (int c = 0; c < NH; c += 8) {
             bool moved = false;
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 d = *reinterpret_cast<const float4*>(&sh.delta[c + j]);
+            for (int j = 0; j < 8; j += 4) {
+              const float4 d = *reinterpret_cast<const float4*>(&sh.delta[c0 + c + j]);
               moved |= d.x != 0.f || d.y != 0.f || d.z != 0.f || d.w != 0.f;
               x[(c + j) / 2] = add2(x[(c + j) / 2], pack(d.x, d.y));
               x[(c + j) / 2 + 1] = add2(x[(c + j) / 2 + 1], pack(d.z, d.w));
             }
-            if (!first && moved) {  // (the same for all threads)
-              uint32_t o[3][16];
+            if (!first && moved) {  // (the same for all threads of a warp)
 #pragma unroll
-              for (int k3 = 0; k3 < 3; ++k3) tc_ld16(tO + k3 * NR + c, o[k3]);
-              tc_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const float f0 = sh.factor[c + j], f1 = sh.factor[c + j + 1];
-                l2[(c + j) / 2] = mul2(l2[(c + j) / 2], pack(f0, f1));
-#pragma unroll
-                for (int k3 = 0; k3 < 3; ++k3) {
-                  o[k3][j] = __float_as_uint(__uint_as_float(o[k3][j]) * f0);
-                  o[k3][j + 1] = __float_as_uint(__uint_as_float(o[k3][j + 1]) * f1);
-                }
+              for (int j = 0; j < 8; j += 2) {
+                const float2 f = *reinterpret_cast<const float2*>(&sh.factor[c0 + c + j]);
+                l2[(c + j) / 2] = mul2(l2[(c + j) / 2], pack(f.x, f.y));
               }
+#pragma unroll 1
+              for (int part = 0; part < 3; ++part) {
+                uint32_t o[8];
+                tc_ld8(tO + part * NR + c, o);
+                tc_wait_ld();
 #pragma unroll
-              for (int k3 = 0; k3 < 3; ++k3) tc_st16(tO + k3 * NR + c, o[k3]);
+                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.factor[c0 + c + j]);
+                tc_st8(tO + part * NR + c, o);
+              }
               tc_wait_st();
             }
           }
@@ -654,10 +654,10 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         // weights (the buffer's last reader: the values' MMA of the tile before)
         if (gi > 0) tc_wait(bar(sh.o_done), (gi - 1) & 1, gave_up, p.status);
 #pragma unroll
-        for (int c = 0; c < NR; c += 16) {
-          uint32_t part[3][4];
+        for (int c = 0; c < NH; c += 8) {
+          uint32_t part[3][2];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             float a, b;
             unpack(x[c / 2 + j], a, b);
             a = ex2(a);
@@ -672,9 +672,10 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
             }
           }
 #pragma unroll
-          for (int k3 = 0; k3 < 3; ++k3)
-            *reinterpret_cast<uint4*>(pw + (k3 * NR + c) / 16 * T::kChunk) =
-                make_uint4(part[k3][0], part[k3][1], part[k3][2], part[k3][3]);
+          for (int k3 = 0; k3 < 3; ++k3) {
+            const int col = k3 * NR + c0 + c;
+            *reinterpret_cast<uint2*>(pw + (col >> 4) * T::kChunk + (col & 8)) = make_uint2(part[k3][0], part[k3][1]);
+          }
         }
         fence_async();
         __syncwarp();
@@ -682,67 +683,67 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       }
       // ---- the end of the stretch ----
 #pragma unroll
-      for (int c = 0; c < NR; c += 16) {
-        float v[16];
+      for (int c = 0; c < NH; c += 8) {
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) unpack(l2[(c + j) / 2], v[j], v[j + 1]);
+        for (int j = 0; j < 8; j += 2) unpack(l2[(c + j) / 2], v[j], v[j + 1]);
         const float s = column_sums(v, lane);
-        if (lane < 16) sh.red[warp][c + lane] = s;
+        if (lane < 8) sh.red[wl][c0 + c + lane] = s;
       }
       const bool whole = g.n == g.nt;
       float* slot = whole ? nullptr : slot_of<NR, D>(p, 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0));
-      bar_sync(1, 128);
-      if (t < NR) {
-        const int f = g.f0 + t;
-        const float l = sh.red[0][t] + sh.red[1][t] + sh.red[2][t] + sh.red[3][t], m = -sh.neg_m[t];
+      bar_sync(1, kTcSoft);
+      if (tid < NR) {
+        const int f = g.f0 + tid;
+        const float l = sh.red[0][tid] + sh.red[1][tid] + sh.red[2][tid] + sh.red[3][tid], m = -sh.neg_m[tid];
         const long long idx = (long long)(g.row0 + f / p.G) * p.Hq + g.h * p.G + f % p.G;
-        sh.idx[t] = f < flat ? idx : -1;
+        sh.idx[tid] = f < flat ? idx : -1;
         if (!whole) {
-          slot[t] = l == 0.f ? ninf : m;  // a row that saw nothing has no reference
-          slot[NR + t] = l;
+          slot[tid] = l == 0.f ? ninf : m;  // a row that saw nothing has no reference
+          slot[NR + tid] = l;
         } else if (f < flat) {
           const Coef r = row_coef(p, idx, m, l, g.bad);
-          sh.coef[t] = r;
+          sh.coef[tid] = r;
           finish_lse(p, idx, r);
         }
       }
       tc_wait(bar(sh.o_done), (gi - 1) & 1, gave_up, p.status);
       tc_after();
       const int d = t & (D - 1);
-      float* const half = reinterpret_cast<float*>(mem + T::oP);  // the weights' memory, read by now
+      float* const half = reinterpret_cast<float*>(mem + T::oP) + c0 * D;  // the weights' memory, read by now
       if (kHalves == 2 && t >= D) {
 #pragma unroll 1
-        for (int c = 0; c < NR; c += 16) {
-          float o[16];
+        for (int c = 0; c < NH; c += 8) {
+          float o[8];
           tc_sum_parts<NR>(tO + c, o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) half[(c + j) * D + d] = o[j];
+          for (int j = 0; j < 8; ++j) half[(c + j) * D + d] = o[j];
         }
       }
-      bar_sync(1, 128);
+      bar_sync(1, kTcSoft);
       if (t < D) {
 #pragma unroll 1
-        for (int c = 0; c < NR; c += 16) {
-          float o[16];
+        for (int c = 0; c < NH; c += 8) {
+          float o[8];
           tc_sum_parts<NR>(tO + c, o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const long long idx = sh.idx[c + j];
+          for (int j = 0; j < 8; ++j) {
+            const long long idx = sh.idx[c0 + c + j];
             if (kHalves == 2) o[j] += half[(c + j) * D + d];
             if (!whole)
-              slot[2 * NR + (c + j) * D + d] = o[j];
+              slot[2 * NR + (c0 + c + j) * D + d] = o[j];
             else if (idx >= 0)
-              finish<uint16_t, D>(p, idx, d, o[j], sh.coef[c + j]);
+              finish<uint16_t, D>(p, idx, d, o[j], sh.coef[c0 + c + j]);
           }
         }
       }
       tc_before();
-      bar_sync(1, 128);
+      bar_sync(1, kTcSoft);
     }
   }
   tc_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
   }

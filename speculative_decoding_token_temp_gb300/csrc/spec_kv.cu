@@ -120,6 +120,8 @@ cudaError_t launch_append(const KvParams& p, bool vec, cudaStream_t s) {
 
 constexpr int kMaxGridS = 1024;  // largest grid of the 32-bit kernel (its workspace is sized for it)
 
+// tiles that a segment's beginning and end count for on the line of tiles
+constexpr int kSegCostT = 3, kSegCostS = 1;
 constexpr int kMaxGridT = 512;   // of the tensor-core kernel (two blocks an SM)
 
 struct AttnLayout {
@@ -186,7 +188,7 @@ spec_status check_attn(const spec_attn_batch& g, const spec_kv_cache& c) {
 }
 
 AttnParams attn_params(const spec_attn_batch& g, const spec_kv_cache& c, const void* q, int64_t q_row, int64_t q_head,
-                       void* o, float* lse, uint32_t* status) {
+                       void* o, float* lse, uint32_t* status, int seg_cost) {
   AttnParams p;
   memset(&p, 0, sizeof(p));
   p.k = static_cast<const uint8_t*>(c.k);
@@ -211,6 +213,7 @@ AttnParams attn_params(const spec_attn_batch& g, const spec_kv_cache& c, const v
   p.kv_len = g.kv_len;
   p.mask = g.parent != nullptr ? A_TREE : A_CHAIN;
   p.c = g.scale * 1.4426950408889634f;
+  p.seg_cost = seg_cost;
   p.o = o;
   p.lse = lse;
   p.status = status;
@@ -426,7 +429,8 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
   if (!workspace || workspace_bytes < L.total || !on(workspace, 256)) return SPEC_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
-  AttnParams p = attn_params(g, c, q, q_row_stride, q_head_stride, o, lse, device_status);
+  AttnParams p = attn_params(g, c, q, q_row_stride, q_head_stride, o, lse, device_status,
+                             dtype == SPEC_BF16 ? kSegCostT : kSegCostS);
   p.part = reinterpret_cast<float*>(ws + L.part);
   Maps maps;
   memset(&maps, 0, sizeof(maps));
