@@ -464,6 +464,14 @@ def spec_verify_multi(target: torch.Tensor, draft: torch.Tensor, draft_tokens: t
 # ---------------------------------------------------------------------------
 # the 8-bit key/value cache and the attention over it (include/spec_kv.h)
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(device) -> int:
+    """The current stream's handle, without the Stream object where torch gives it directly (2 us a call)."""
+    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 class KVCache:
     """A paged key/value cache in 8 bits: k, v [num_pages, kv_heads, page_size, head_dim]
     (torch.float8_e4m3fn codes), k_exp, v_exp [num_pages, kv_heads, page_size] (uint8); an
@@ -556,7 +564,7 @@ def spec_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table:
     st = _status_word(o, device_status, dev)
     check("spec_kv_append", _lib.lib().spec_kv_append(cache.desc, r, dt, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row,
                                                       v_head, st.data_ptr(),
-                                                      torch.cuda.current_stream(dev).cuda_stream))
+                                                      _stream_handle(dev)))
     return o
 
 
@@ -582,7 +590,7 @@ def spec_kv_read(cache: KVCache, page_table: torch.Tensor, row_seq: torch.Tensor
     code = {torch.bfloat16: _lib.SPEC_BF16, torch.float32: _lib.SPEC_F32}.get(dtype)
     if code is None:
         raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
-    check("spec_kv_read", _lib.lib().spec_kv_read(cache.desc, r, code, _ptr(k), _ptr(v), st.data_ptr(), _stream(dev)))
+    check("spec_kv_read", _lib.lib().spec_kv_read(cache.desc, r, code, _ptr(k), _ptr(v), st.data_ptr(), _stream_handle(dev)))
     return o
 
 
@@ -661,7 +669,7 @@ def spec_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv
     st = _status_word(o, device_status, dev)
     lib = _lib.lib()
     nbytes = int(lib.spec_attention_workspace_bytes(g, cache.desc, dt))
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = _stream_handle(dev)
     if workspace is None:  # a default workspace for each stream: calls on two streams may overlap
         workspace = _DEFAULT_WS.setdefault((dev.type, dev.index, stream), Workspace())
     ws = _workspace(workspace, nbytes, dev)

@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libspecverify.so")
 LIB_BOUNDS = os.path.join(PKG, "libspecverify_bounds.so")
 SOURCES = ["spec_verify.cu", "spec_kv.cu"]
 HEADERS = ["kernels.cuh", "kernels_rows.cuh", "kernels_sample.cuh", "kernels_multi.cuh", "plan.h",
-           "kernels_kv.cuh", "kernels_attn.cuh", "kernels_attn_tc.cuh"]
+           "kernels_kv.cuh", "kernels_attn.cuh", "kernels_attn_tc.cuh",
+           "kernels_attn_prefix.cuh"]
 PUBLIC = ["spec_verify.h", "spec_kv.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -41,13 +41,21 @@ struct AttnParams {
   int seg_cost;             // tiles that a segment's beginning and end count for
   float c;                  // scale * log2(e)
   float* part;              // the parts of cut segments: two slots a block
-  long long part_floats;
+  struct CutRec* cut;       // what each block leaves for attn_merge_kernel
   const float *pre_o, *pre_lse;  // the prefix's part to join in (normalised values, log2 of the sum), or null
   float *dst_o, *dst_lse;        // the prefix pass: its part goes here instead of o and lse
   void* o;
   float* lse;
   uint32_t* status;
   uint64_t sees[SPEC_MAX_TREE_NODES];  // node j: bit i set when node i sees it (i == j or a descendant of j)
+};
+
+// The segment that begins in a block and goes on in others (parts = 0: none): blocks
+// block .. block + parts - 1 hold it, of which those whose stretch of the line (length
+// `total`) is empty hold nothing.
+struct CutRec {
+  int parts, row0, rows, h, f0, bad;
+  long long total;
 };
 
 struct SeqInfo {
@@ -88,15 +96,15 @@ struct Place {
 struct LocateShared {
   long long warp_sum[32];
   int bad;
-  Place at[2];
+  Place at;
 };
 
-// Block-wide: the line's length and the places of the tiles at fraction i0 / n and i1 / n of
-// it. Each thread sums a stretch of sequences, the block scans the sums, and the thread
-// whose stretch holds a place walks to it. Returns false when cu is no valid prefix sum
+// Block-wide: the line's length, block i's part of it (of n), and the place where that
+// begins. Each thread sums a stretch of sequences, the block scans the sums, and the thread
+// whose stretch holds the place walks to it. Returns false when cu is no valid prefix sum
 // (nothing else it says is then used).
 template <int NR, int THREADS>
-__device__ bool locate(const AttnParams& p, LocateShared& sh, int i0, int i1, int n, long long* begin, long long* end,
+__device__ bool locate(const AttnParams& p, LocateShared& sh, int i, int n, long long* begin, long long* end,
                        long long* line) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) sh.bad = 0;
@@ -130,27 +138,22 @@ __device__ bool locate(const AttnParams& p, LocateShared& sh, int i0, int i1, in
   }
   const long long excl = before + incl - sum;
   const bool ok = sh.bad == 0;
-  if (ok) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const long long pos = total * (k ? i1 : i0) / n;
-      if (pos >= excl && pos < excl + sum) {
-        long long at = excl;
-        for (int b = b0; b < b1; ++b) {
-          const long long t = seq_tiles<NR>(p, seq_info(p, b));
-          if (pos < at + t) {
-            sh.at[k].b = b;
-            sh.at[k].off = pos - at;
-            break;
-          }
-          at += t;
-        }
+  const long long pos = total * i / n;
+  if (ok && pos >= excl && pos < excl + sum) {
+    long long at = excl;
+    for (int b = b0; b < b1; ++b) {
+      const long long t = seq_tiles<NR>(p, seq_info(p, b));
+      if (pos < at + t) {
+        sh.at.b = b;
+        sh.at.off = pos - at;
+        break;
       }
+      at += t;
     }
   }
   __syncthreads();
-  *begin = total * i0 / n;
-  *end = total * i1 / n;
+  *begin = pos;
+  *end = total * (i + 1) / n;
   *line = total;
   return ok;
 }
@@ -188,12 +191,25 @@ __device__ __forceinline__ Seg next_seg(const AttnParams& p, Place& at, long lon
   return g;
 }
 
-// Whether row i of a segment sees token t (< len) of its sequence.
-__device__ __forceinline__ bool sees(const AttnParams& p, int i, int rows, int len, int t) {
+// Which of a segment's rows see one token t of its sequence: rows from `from` on, of these
+// (in a tree) the ones whose bit stands in `nodes` (bit i - 1: row i). `sees` is
+// AttnParams::sees in shared memory (lanes ask for different nodes).
+struct Sight {
+  int from;
+  uint64_t nodes;
+  __device__ __forceinline__ bool operator()(int row) const { return row >= from && ((nodes >> ((row - 1) & 63)) & 1); }
+};
+
+__device__ __forceinline__ Sight sight_of(int mask, const uint64_t* sees, int rows, int len, int t) {
   const int j = t - (len - rows);  // the round's row whose token it is
-  if (p.mask == A_ALL || j < 0) return true;
-  if (p.mask == A_CHAIN || j == 0) return i >= j;
-  return i >= j && ((p.sees[j - 1] >> (i - 1)) & 1);
+  Sight s{0, ~0ull};
+  if (t >= len)
+    s.from = 1 << 30;
+  else if (mask != A_ALL && j >= 0) {
+    s.from = j;
+    if (mask == A_TREE && j > 0) s.nodes = sees[j - 1];
+  }
+  return s;
 }
 
 // ---------------------------------------------------------------------------
@@ -210,7 +226,7 @@ __device__ __forceinline__ Coef row_coef(const AttnParams& p, long long idx, flo
   r.a = l == 0.f ? 0.f : 1.f / l;
   r.b = 0.f;
   if (p.pre_o != nullptr) {
-    const float q = __ldg(p.pre_lse + idx);
+    const float q = __ldcg(p.pre_lse + idx);
     if (l == 0.f) {
       r.b = q == ninf ? 0.f : 1.f;
       r.lse2 = q;
@@ -236,7 +252,7 @@ __device__ __forceinline__ void finish(const AttnParams& p, long long idx, int d
   const long long at = idx * D + d;
   if (!in_idx(at, (long long)p.R * p.Hq * D, p.status)) return;
   float x = v * r.a;
-  if (r.b != 0.f) x += __ldg(p.pre_o + at) * r.b;
+  if (r.b != 0.f) x += __ldcg(p.pre_o + at) * r.b;
   if (p.dst_o != nullptr)
     p.dst_o[at] = x;
   else
@@ -268,71 +284,71 @@ __device__ void fill_nan(const AttnParams& p, int block, int blocks) {
   }
 }
 
+// What block `block` of `grid` leaves for attn_merge_kernel about a stretch g that ends the
+// block's part of the line (at `end` of `total`).
+__device__ __forceinline__ CutRec cut_rec(const Seg& g, int block, int grid, long long end, long long total) {
+  CutRec r{0, g.row0, g.rows, g.h, g.f0, g.bad, total};
+  if (g.t0 == 0 && g.n < g.nt) {
+    const long long last = end + (g.nt - g.n);
+    int e = block + 1;
+    while (e < grid && total * e / grid < last) ++e;
+    r.parts = e - block;
+  }
+  return r;
+}
+
 // ---------------------------------------------------------------------------
-// Joins the parts of cut segments. Block x looks at the cut between grid blocks x and
-// x + 1; if it is the first cut inside a segment, it joins all parts of that segment, in
-// order; block y takes 4 of its rows, one a warp.
+// Joins the parts of cut segments, in order: block x takes the segment that begins in block
+// x of the attention kernel and goes on, block y 8 of its rows, one a warp.
+constexpr int kMergeThreads = 256;
+
 template <typename E, int D, int NR>
-__global__ void __launch_bounds__(128) attn_merge_kernel(AttnParams p, int grid) {
-  __shared__ LocateShared sh;
-  const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
-  long long prev, cut, total;
-  // what locate reads was there before the attention kernel began, which released this grid after its own wait
-  const bool ok = locate<NR, 128>(p, sh, i - 1, i, grid, &prev, &cut, &total);
+__global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(AttnParams p, int grid) {
   griddep_wait();
   griddep_launch();
-  if (!ok || cut >= total) return;
-  Place at = sh.at[1];
-  long long left = 1;
-  const Seg g = next_seg<NR>(p, at, left);
-  // the segment's own tiles on the line; a cut at or before the first does not divide it
-  const long long first = cut - g.t0, last = first + g.nt;
-  if (g.t0 == 0 || prev > first) return;
-  const int c = blockIdx.y * 4 + (threadIdx.x >> 5), f = g.f0 + c;
-  if (f >= g.rows * p.G) return;
-  // parts: block i - 1 (slot 2 (i - 1) + 1), then every block from i on that has tiles before `last`
-  int e = i;
-  while (e < grid && total * e / grid < last) ++e;
-  const int parts = e - i + 1;
+  const CutRec r = p.cut[blockIdx.x];
+  const int i = blockIdx.x, lane = threadIdx.x & 31, c = blockIdx.y * 8 + (threadIdx.x >> 5), f = r.f0 + c;
+  if (r.parts == 0 || c >= NR || f >= r.rows * p.G) return;
+  // part j: slot 2 i + 1 of the first block, slot 2 (i + j) of the others
+  auto part_of = [&](int j) { return slot_of<NR, D>(p, j == 0 ? 2 * i + 1 : 2 * (i + j)); };
+  auto holds = [&](int j) { return j == 0 || r.total * (i + j) / grid != r.total * (i + j + 1) / grid; };
   float m = __int_as_float(kNegInfBits);
-  for (int j = lane; j < parts; j += 32) {
-    const int blk = i - 1 + j;
-    if (j > 0 && total * blk / grid == total * (blk + 1) / grid) continue;
-    m = fmaxf(m, slot_of<NR, D>(p, j == 0 ? 2 * blk + 1 : 2 * blk)[c]);
-  }
+  for (int j = lane; j < r.parts; j += 32)
+    if (holds(j)) m = fmaxf(m, part_of(j)[c]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
   const float mu = m == __int_as_float(kNegInfBits) ? 0.f : m;
   float l = 0.f, acc[D / 32];
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
-  for (int j0 = 0; j0 < parts; j0 += 32) {
-    const int j = j0 + lane, blk = i - 1 + j;
-    float w = 0.f, lj = 0.f;
-    if (j < parts && (j == 0 || total * blk / grid != total * (blk + 1) / grid)) {
-      const float* s = slot_of<NR, D>(p, j == 0 ? 2 * blk + 1 : 2 * blk);
-      w = exp2f(s[c] - mu);
-      lj = s[NR + c];
-      if (!(lj == 0.f)) l += w * lj;
-      if (lj == 0.f) w = 0.f;
+  for (int j0 = 0; j0 < r.parts; j0 += 32) {
+    const int j = j0 + lane;
+    float w = 0.f;
+    if (j < r.parts && holds(j)) {
+      const float* s = part_of(j);
+      const float lj = s[NR + c];
+      if (lj != 0.f) {
+        w = exp2f(s[c] - mu);
+        l += w * lj;
+      }
     }
-    const int cnt = min(32, parts - j0);
+    const int cnt = min(32, r.parts - j0);
+#pragma unroll 4
     for (int t = 0; t < cnt; ++t) {
       const float wt = __shfl_sync(kFull, w, t);
       if (wt == 0.f) continue;
-      const int jt = j0 + t, bt = i - 1 + jt;
-      const float* s = slot_of<NR, D>(p, jt == 0 ? 2 * bt + 1 : 2 * bt) + 2 * NR + c * D + lane * (D / 32);
+      const float* s = part_of(j0 + t) + 2 * NR + c * D + lane * (D / 32);
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) acc[k] += wt * s[k];
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-  const long long idx = (long long)(g.row0 + f / p.G) * p.Hq + g.h * p.G + f % p.G;
-  const Coef r = row_coef(p, idx, mu, l, g.bad);
+  const long long idx = (long long)(r.row0 + f / p.G) * p.Hq + r.h * p.G + f % p.G;
+  const Coef co = row_coef(p, idx, mu, l, r.bad != 0);
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) finish<E, D>(p, idx, lane * (D / 32) + k, acc[k], r);
-  if (lane == 0) finish_lse(p, idx, r);
+  for (int k = 0; k < D / 32; ++k) finish<E, D>(p, idx, lane * (D / 32) + k, acc[k], co);
+  if (lane == 0) finish_lse(p, idx, co);
 }
 
 // ---------------------------------------------------------------------------
@@ -352,24 +368,28 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
   __shared__ float sx[kTile];
   __shared__ int sbad[kTile];
   __shared__ float sm[NR], sl[NR], sf[NR];
+  __shared__ uint64_t s_sees[SPEC_MAX_TREE_NODES];
   static_assert(sizeof(float) * NG * NR * D <= sizeof(skv), "the sums of the token groups fit where the tile was");
   uint8_t* sk = skv;
   uint8_t* svv = skv + kTile * KS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float ninf = __int_as_float(kNegInfBits), nan = __int_as_float(0x7fffffff);
+  if (p.mask == A_TREE && tid < SPEC_MAX_TREE_NODES) s_sees[tid] = p.sees[tid];
   griddep_wait();
   griddep_launch();
   long long begin, end, total;
-  if (!locate<NR, 128>(p, sh, blockIdx.x, blockIdx.x + 1, gridDim.x, &begin, &end, &total)) {
+  if (!locate<NR, 128>(p, sh, blockIdx.x, gridDim.x, &begin, &end, &total)) {
     fill_nan<E, D>(p, blockIdx.x, gridDim.x);
-    return;
+    begin = end = 0;
   }
-  Place at = sh.at[0];
+  Place at = sh.at;
   long long left = end - begin;
   uint32_t bits = 0;
+  if (tid == 0) p.cut[blockIdx.x].parts = 0;
   while (left > 0) {
     const Seg g = next_seg<NR>(p, at, left);
     if (g.n == 0) continue;
+    if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, end, total);
     if (g.bad) bits |= SPEC_DEV_OFFSETS;
     __syncthreads();
     for (int e = tid; e < NR * D; e += 128) {
@@ -444,9 +464,9 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
             s[c] = fmaf(x[0], y.x, fmaf(x[1], y.y, fmaf(x[2], y.z, fmaf(x[3], y.w, s[c]))));
           }
         }
+        const Sight sight = sight_of(p.mask, s_sees, g.rows, g.len, t);
 #pragma unroll
-        for (int c = 0; c < NR; ++c)
-          ss[c][tid] = t < g.len && sees(p, (g.f0 + c) / p.G, g.rows, g.len, t) ? s[c] * ke : ninf;
+        for (int c = 0; c < NR; ++c) ss[c][tid] = sight((g.f0 + c) / p.G) ? s[c] * ke : ninf;
         sx[tid] = ve;
       }
       __syncthreads();

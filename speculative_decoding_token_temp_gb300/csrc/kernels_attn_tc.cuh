@@ -239,6 +239,7 @@ struct TcShared {
   uint32_t tmem;
   int gave_up;
   uint32_t bad_pages[T::kNK];
+  uint64_t sees[SPEC_MAX_TREE_NODES];
   uint8_t nan_code[kTile];          // of a tile with masked places: the token's values hold a NaN code
   alignas(16) float rq[NR];         // a row's factor of the scores: scale * log2(e) * its power of two
   alignas(16) int row[NR];          // query row of a flat row
@@ -355,6 +356,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     sh.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (p.mask == A_TREE && tid < SPEC_MAX_TREE_NODES) sh.sees[tid] = p.sees[tid];
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(
                      (uint32_t)__cvta_generic_to_shared(&sh.tmem))
@@ -365,14 +367,14 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   griddep_wait();
   griddep_launch();
   long long begin, end, total;
-  const bool ok = locate<NR, kTcThreads>(p, sh.loc, blockIdx.x, blockIdx.x + 1, gridDim.x, &begin, &end, &total);
+  const bool ok = locate<NR, kTcThreads>(p, sh.loc, blockIdx.x, gridDim.x, &begin, &end, &total);
   tc_after();
   const uint32_t tmem = sh.tmem;
   if (!ok) {
     fill_nan<uint16_t, D>(p, blockIdx.x, gridDim.x);
     begin = end = 0;
   }
-  Place at = sh.loc.at[0];
+  Place at = sh.loc.at;
   long long left = end - begin;
 
   if (warp == 8) {
@@ -496,9 +498,11 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     const float nan = __int_as_float(0x7fffffff), ninf = __int_as_float(kNegInfBits);
     int gi = 0;
     f2 l2[NH / 2];
+    if (tid == 0) p.cut[blockIdx.x].parts = 0;
     while (left > 0) {
       const Seg g = next_seg<NR>(p, at, left);
       if (g.n == 0) continue;
+      if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, end, total);
       const int flat = g.rows * p.G;
       stage_queries<D, NR>(p, g, sh, mem + T::oQ, tid);
       fence_async();
@@ -548,6 +552,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         const float ev = fine ? (float)((int)vb - kExpBias) : 0.f;
         const float isv = fine ? __int_as_float((2 * kExpBias - (int)vb) << 23) : 1.f;
         const f2 ks2 = pack(ks, ks), ev2 = pack(ev, ev), isv2 = pack(isv, isv);
+        const Sight sight = sight_of(masked ? p.mask : A_ALL, sh.sees, g.rows, g.len, tok);
         // scores
         tc_wait(bar(sh.s_full), gi & 1, gave_up, p.status);
         tc_after();
@@ -577,7 +582,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
             const int ri[4] = {rows.x, rows.y, rows.z, rows.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              if (!(live && ri[q] < g.rows && sees(p, ri[q], g.rows, g.len, tok))) z[q] = ninf;
+              if (!sight(ri[q])) z[q] = ninf;
             y0 = pack(z[0], z[1]);
             y1 = pack(z[2], z[3]);
           }

@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "kernels_attn.cuh"
+#include "kernels_attn_prefix.cuh"
 #include "kernels_attn_tc.cuh"
 #include "kernels_kv.cuh"
 #include "spec_kv.h"
@@ -121,14 +122,19 @@ cudaError_t launch_append(const KvParams& p, bool vec, cudaStream_t s) {
 constexpr int kMaxGridS = 1024;  // largest grid of the 32-bit kernel (its workspace is sized for it)
 
 // tiles that a segment's beginning and end count for on the line of tiles
-constexpr int kSegCostT = 3, kSegCostS = 1;
+constexpr int kSegCostT = 4, kSegCostS = 1, kSegCostP = 2;
+constexpr int kMaxGridP = 160;   // of attn_prefix_kernel (one block an SM)
+// rows that share the prefix's keys from which on it is widened and computed in 128-row tiles
+constexpr int kWideRows = 96;
 constexpr int kMaxGridT = 512;   // of the tensor-core kernel (two blocks an SM)
 
 struct AttnLayout {
   int nr, pre_nr;      // rows of a row block, of the two passes
   long long grid;      // blocks of the pass over the sequences' tokens, at most
   long long pre_grid;  // of the prefix pass
-  size_t part, pre_o, pre_lse, total;
+  bool wide;           // the prefix widened and computed by attn_prefix_kernel
+  long long tiles;     // of the prefix
+  size_t part, cut, pre_o, pre_lse, k16, v16, exp, total;
 };
 
 long long rows_of(const spec_attn_batch& g) { return (long long)g.total_draft + g.B; }
@@ -148,21 +154,35 @@ AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dt
   const bool tc = dtype == SPEC_BF16;
   const long long cap = tc ? kMaxGridT : kMaxGridS;
   L.nr = tc ? tc_rows((long long)(g.gamma + 1) * G, c.head_dim) : kRowsS;
-  L.pre_nr = tc && rows_of(g) > 0 ? tc_rows(rows_of(g) * G, c.head_dim) : kRowsS;
+  const long long flat = rows_of(g) * G;
+  L.wide = tc && g.prefix_len > 0 && flat >= kWideRows;
+  L.tiles = cdiv(g.prefix_len, kTile);
+  L.pre_nr = L.wide ? kRowsP : tc && flat > 0 ? tc_rows(flat, c.head_dim) : kRowsS;
   const long long most_tiles = cdiv((long long)g.pages_per_seq * c.page_size, kTile);
   const long long nt = most_tiles > 1 ? most_tiles : 1;
-  const long long own = (long long)g.B * cdiv((long long)(g.gamma + 1) * G, L.nr) * c.kv_heads * nt;
-  const long long pre = g.prefix_len > 0 ? cdiv(rows_of(g) * G, L.pre_nr) * c.kv_heads * cdiv(g.prefix_len, kTile) : 0;
+  const int more = tc ? kSegCostT : kSegCostS;  // a block for every tile of the line at most
+  const long long own = (long long)g.B * cdiv((long long)(g.gamma + 1) * G, L.nr) * c.kv_heads * (nt + more);
+  const long long pre = g.prefix_len > 0 ? cdiv(rows_of(g) * G, L.pre_nr) * c.kv_heads * (cdiv(g.prefix_len, kTile) + more) : 0;
   L.grid = own < cap ? own : cap;
-  L.pre_grid = pre < cap ? pre : cap;
+  const long long pre_cap = L.wide ? kMaxGridP : cap;
+  L.pre_grid = pre < pre_cap ? pre : pre_cap;
   const long long slot_rows = L.grid * L.nr > L.pre_grid * L.pre_nr ? L.grid * L.nr : L.pre_grid * L.pre_nr;
   size_t off = 0;
   L.part = off;
   off = up256(off + sizeof(float) * (size_t)(2 * slot_rows) * (c.head_dim + 2));
+  L.cut = off;
+  off = up256(off + sizeof(CutRec) * (size_t)(L.grid > L.pre_grid ? L.grid : L.pre_grid));
   L.pre_o = off;
   if (g.prefix_len > 0) off = up256(off + sizeof(float) * (size_t)rows_of(g) * g.q_heads * c.head_dim);
   L.pre_lse = off;
   if (g.prefix_len > 0) off = up256(off + sizeof(float) * (size_t)rows_of(g) * g.q_heads);
+  const size_t wide_bytes = L.wide ? (size_t)2 * c.kv_heads * L.tiles * kTile * c.head_dim : 0;
+  L.k16 = off;
+  off = up256(off + wide_bytes);
+  L.v16 = off;
+  off = up256(off + wide_bytes);
+  L.exp = off;
+  if (L.wide) off = up256(off + sizeof(float) * (size_t)c.kv_heads * L.tiles);
   L.total = off;
   return L;
 }
@@ -244,7 +264,7 @@ AttnParams prefix_params(const AttnParams& own, const spec_attn_batch& g, const 
 template <typename E, int D, int NR>
 cudaError_t launch_merge(const AttnParams& p, int grid, cudaStream_t s) {
   if (grid < 2) return cudaSuccess;
-  return start(attn_merge_kernel<E, D, NR>, dim3((unsigned)(grid - 1), cdiv(NR, 4)), 128, 0, s, p, grid);
+  return start(attn_merge_kernel<E, D, NR>, dim3((unsigned)grid, cdiv(NR, 8)), kMergeThreads, 0, s, p, grid);
 }
 
 // One wave of the 32-bit kernel on the current device.
@@ -307,19 +327,25 @@ struct Maps {
   CUtensorMap k, v;
 };
 
-template <int D, int NR>
-cudaError_t pass_tc(const AttnParams& p, long long grid, const Maps& m, cudaStream_t s) {
-  auto kern = attn_tc_kernel<D, NR>;
-  static std::atomic<unsigned long long> done{0};  // a bit a device: the kernel may use its shared memory there
+// Lets a kernel use `bytes` of shared memory on the current device, once (`done`: a bit a device).
+template <typename K>
+cudaError_t allow_smem(K kern, std::atomic<unsigned long long>& done, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (!(done.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D, NR>::kSmem);
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_relaxed);
-  }
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <int D, int NR>
+cudaError_t pass_tc(const AttnParams& p, long long grid, const Maps& m, cudaStream_t s) {
+  auto kern = attn_tc_kernel<D, NR>;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(kern, done, TcShape<D, NR>::kSmem);
+  if (e != cudaSuccess) return e;
   const long long sms = sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
   const int n = (int)(grid < 2 * sms ? grid : 2 * sms);
@@ -334,6 +360,42 @@ cudaError_t pass_tc_nr(int nr, const AttnParams& p, long long grid, const Maps& 
     if (nr == 48) return pass_tc<D, 48>(p, grid, m, s);
   }
   return pass_tc<D, 32>(p, grid, m, s);
+}
+
+// The widened prefix: 16-bit rows of head_dim elements, loaded 64 elements by a tile of tokens.
+bool wide_map(CUtensorMap* m, void* base, const spec_kv_cache& c, long long rows, CUtensorMapDataType type) {
+  const EncodeFn f = encode_fn();
+  if (f == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)c.head_dim * 2};
+  const cuuint32_t box[2] = {64, kTile};
+  const cuuint32_t ones[2] = {1, 1};
+  return f(m, type, 2, base, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t pass_prefix(const AttnParams& p, const spec_kv_cache& c, const AttnLayout& L, char* ws, cudaStream_t s) {
+  WideParams w;
+  w.k16 = reinterpret_cast<uint16_t*>(ws + L.k16);
+  w.v16 = reinterpret_cast<uint16_t*>(ws + L.v16);
+  w.exp = reinterpret_cast<float*>(ws + L.exp);
+  w.tiles = (int)L.tiles;
+  Maps m;
+  const long long rows = L.tiles * kTile * c.kv_heads;
+  if (!wide_map(&m.k, w.k16, c, rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) ||
+      !wide_map(&m.v, w.v16, c, rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
+    return cudaErrorInvalidValue;
+  cudaError_t e = start(widen_kernel<D>, dim3((unsigned)L.tiles, (unsigned)c.kv_heads), 256, 0, s, p, w);
+  if (e != cudaSuccess) return e;
+  auto kern = attn_prefix_kernel<D>;
+  static std::atomic<unsigned long long> done{0};
+  if ((e = allow_smem(kern, done, PreShape<D>::kSmem)) != cudaSuccess) return e;
+  const long long sms = sm_count();
+  if (sms < 1) return cudaErrorInvalidConfiguration;
+  const int n = (int)(L.pre_grid < sms ? L.pre_grid : sms);
+  e = start(kern, dim3((unsigned)n), kPreThreads, PreShape<D>::kSmem, s, p, w, m.k, m.v);
+  return e != cudaSuccess ? e : launch_merge<uint16_t, D, kRowsP>(p, n, s);
 }
 
 // One pass over keys: fp32 queries on the 32-bit kernel, bf16 queries on the tensor cores.
@@ -432,6 +494,7 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
   AttnParams p = attn_params(g, c, q, q_row_stride, q_head_stride, o, lse, device_status,
                              dtype == SPEC_BF16 ? kSegCostT : kSegCostS);
   p.part = reinterpret_cast<float*>(ws + L.part);
+  p.cut = reinterpret_cast<CutRec*>(ws + L.cut);
   Maps maps;
   memset(&maps, 0, sizeof(maps));
   if (dtype == SPEC_BF16 && (!page_map(&maps.k, c.k, c) || !page_map(&maps.v, c.v, c))) return SPEC_ERR_CUDA;
@@ -439,8 +502,12 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
   if (g.prefix_len > 0) {
     float* pre_o = reinterpret_cast<float*>(ws + L.pre_o);
     float* pre_lse = reinterpret_cast<float*>(ws + L.pre_lse);
-    const AttnParams pp = prefix_params(p, g, c, pre_o, pre_lse);
-    err = attn_pass(dtype, c.head_dim, L.pre_nr, pp, L.pre_grid, maps, s);
+    AttnParams pp = prefix_params(p, g, c, pre_o, pre_lse);
+    if (L.wide) pp.seg_cost = kSegCostP;
+    if (L.wide)
+      err = c.head_dim == 64 ? pass_prefix<64>(pp, c, L, ws, s) : pass_prefix<128>(pp, c, L, ws, s);
+    else
+      err = attn_pass(dtype, c.head_dim, L.pre_nr, pp, L.pre_grid, maps, s);
     if (err != cudaSuccess) return SPEC_ERR_CUDA;
     p.pre_o = pre_o;
     p.pre_lse = pre_lse;
