@@ -51,11 +51,9 @@ struct AttnParams {
 };
 
 // The segment that begins in a block and goes on in others (parts = 0: none): blocks
-// block .. block + parts - 1 hold it, of which those whose stretch of the line (length
-// `total`) is empty hold nothing.
+// block .. block + parts - 1 hold it (`total`: the line's length).
 struct CutRec {
-  int parts, row0, rows, h, f0, bad;
-  long long total;
+  int parts, row0, rows, h, f0, bad, total;
 };
 
 struct SeqInfo {
@@ -83,35 +81,38 @@ __device__ __forceinline__ int seq_ntiles(const SeqInfo& s) { return s.len > 0 ?
 
 // Tiles on the line of a sequence, over all its row blocks and kv heads.
 template <int NR>
-__device__ __forceinline__ long long seq_tiles(const AttnParams& p, const SeqInfo& s) {
-  return (long long)((s.rows * p.G + NR - 1) / NR) * p.Hk * (seq_ntiles(s) + p.seg_cost);
+__device__ __forceinline__ int seq_tiles(const AttnParams& p, const SeqInfo& s) {
+  return (s.rows * p.G + NR - 1) / NR * p.Hk * (seq_ntiles(s) + p.seg_cost);
 }
 
 // A place on the line of tiles: sequence b, tile `off` of it.
 struct Place {
-  int b;
-  long long off;
+  int b, off;
 };
 
 struct LocateShared {
-  long long warp_sum[32];
+  int warp_sum[32];
   int bad;
   Place at;
 };
+
+// Where block i's part of a line of `total` tiles begins, of n blocks (the first total % n
+// have one tile more). The host has seen to it that a line's length fits an int.
+__device__ __forceinline__ int line_at(int total, int i, int n) { return total / n * i + min(i, total % n); }
 
 // Block-wide: the line's length, block i's part of it (of n), and the place where that
 // begins. Each thread sums a stretch of sequences, the block scans the sums, and the thread
 // whose stretch holds the place walks to it. Returns false when cu is no valid prefix sum
 // (nothing else it says is then used).
 template <int NR, int THREADS>
-__device__ bool locate(const AttnParams& p, LocateShared& sh, int i, int n, long long* begin, long long* end,
-                       long long* line) {
+__device__ __noinline__ bool locate(const AttnParams& p, LocateShared& sh, int i, int n, int* begin, int* end, int* line) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) sh.bad = 0;
   __syncthreads();
   const int per = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  long long sum = 0;
+  int sum = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     if (p.cu != nullptr) {
       const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1);
@@ -123,38 +124,39 @@ __device__ bool locate(const AttnParams& p, LocateShared& sh, int i, int n, long
     }
     sum += seq_tiles<NR>(p, seq_info(p, b));
   }
-  long long incl = sum;
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(kFull, incl, o);
+    const int y = __shfl_up_sync(kFull, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) sh.warp_sum[warp] = incl;
   __syncthreads();
-  long long before = 0, total = 0;
+  int before = 0, total = 0;
+#pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += sh.warp_sum[w];
     total += sh.warp_sum[w];
   }
-  const long long excl = before + incl - sum;
+  const int excl = before + incl - sum;
   const bool ok = sh.bad == 0;
-  const long long pos = total * i / n;
-  if (ok && pos >= excl && pos < excl + sum) {
-    long long at = excl;
+  *begin = line_at(total, i, n);
+  *end = line_at(total, i + 1, n);
+  *line = total;
+  if (ok && *begin >= excl && *begin < excl + sum) {
+    int at = excl;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const long long t = seq_tiles<NR>(p, seq_info(p, b));
-      if (pos < at + t) {
+      const int t = seq_tiles<NR>(p, seq_info(p, b));
+      if (*begin < at + t) {
         sh.at.b = b;
-        sh.at.off = pos - at;
+        sh.at.off = *begin - at;
         break;
       }
       at += t;
     }
   }
   __syncthreads();
-  *begin = pos;
-  *end = total * (i + 1) / n;
-  *line = total;
   return ok;
 }
 
@@ -169,14 +171,14 @@ struct Seg {
 // The next stretch at `at` (advanced), at most `left` tiles of the line (reduced). It may
 // be empty (n = 0): the block's part of the line ends among the tiles that only count.
 template <int NR>
-__device__ __forceinline__ Seg next_seg(const AttnParams& p, Place& at, long long& left) {
+__device__ __noinline__ Seg next_seg(const AttnParams& p, Place& at, int& left) {
   Seg g;
   const SeqInfo s = seq_info(p, at.b);
   g.row0 = s.row0, g.rows = s.rows, g.len = s.len, g.bad = s.bad;
   g.nt = seq_ntiles(s);
   const int nrb = (s.rows * p.G + NR - 1) / NR, line = g.nt + p.seg_cost;
-  const int seg = (int)(at.off / line), r = (int)(at.off - (long long)seg * line);
-  const int take = (int)min((long long)(line - r), left);
+  const int seg = at.off / line, r = at.off - seg * line;
+  const int take = min(line - r, left);
   g.t0 = max(0, r - p.seg_cost);
   g.n = max(0, r + take - p.seg_cost - g.t0);
   g.h = seg / nrb;
@@ -184,7 +186,7 @@ __device__ __forceinline__ Seg next_seg(const AttnParams& p, Place& at, long lon
   g.pages = p.table + (long long)at.b * p.pps;
   at.off += take;
   left -= take;
-  if (at.off >= (long long)nrb * p.Hk * line) {
+  if (at.off >= nrb * p.Hk * line) {
     at.b += 1;
     at.off = 0;
   }
@@ -218,7 +220,7 @@ struct Coef {
   float a, b, lse2;
 };
 
-__device__ __forceinline__ Coef row_coef(const AttnParams& p, long long idx, float m, float l, bool bad) {
+__device__ __noinline__ Coef row_coef(const AttnParams& p, long long idx, float m, float l, bool bad) {
   Coef r;
   const float nan = __int_as_float(0x7fffffff), ninf = __int_as_float(kNegInfBits);
   if (bad) return Coef{nan, 0.f, nan};
@@ -246,17 +248,23 @@ __device__ __forceinline__ void put(uint16_t* o, float x) {
 }
 __device__ __forceinline__ void put(float* o, float x) { *o = x; }
 
-// Element d of row `idx` (row * Hq + head): the values' sum v under the row's weights.
+// Element d of row `idx` (row * Hq + head) of the output, or of the prefix pass's part.
 template <typename E, int D>
-__device__ __forceinline__ void finish(const AttnParams& p, long long idx, int d, float v, const Coef& r) {
+__device__ __forceinline__ void store_out(const AttnParams& p, long long idx, int d, float x) {
   const long long at = idx * D + d;
   if (!in_idx(at, (long long)p.R * p.Hq * D, p.status)) return;
-  float x = v * r.a;
-  if (r.b != 0.f) x += __ldcg(p.pre_o + at) * r.b;
   if (p.dst_o != nullptr)
     p.dst_o[at] = x;
   else
     put(static_cast<E*>(p.o) + at, x);
+}
+
+// The same from the values' sum v under the row's weights.
+template <typename E, int D>
+__device__ __forceinline__ void finish(const AttnParams& p, long long idx, int d, float v, const Coef& r) {
+  float x = v * r.a;
+  if (r.b != 0.f) x += __ldcg(p.pre_o + idx * D + d) * r.b;
+  store_out<E, D>(p, idx, d, x);
 }
 
 __device__ __forceinline__ void finish_lse(const AttnParams& p, long long idx, const Coef& r) {
@@ -274,7 +282,7 @@ __device__ __forceinline__ float* slot_of(const AttnParams& p, int s) {
 
 // A cu that is no prefix sum of the batch: every row is NaN.
 template <typename E, int D>
-__device__ void fill_nan(const AttnParams& p, int block, int blocks) {
+__device__ __noinline__ void fill_nan(const AttnParams& p, int block, int blocks) {
   if (block == 0 && threadIdx.x == 0) atomicOr(p.status, SPEC_DEV_OFFSETS);
   const long long n = (long long)p.R * p.Hq * D;
   const float nan = __int_as_float(0x7fffffff);
@@ -286,12 +294,13 @@ __device__ void fill_nan(const AttnParams& p, int block, int blocks) {
 
 // What block `block` of `grid` leaves for attn_merge_kernel about a stretch g that ends the
 // block's part of the line (at `end` of `total`).
-__device__ __forceinline__ CutRec cut_rec(const Seg& g, int block, int grid, long long end, long long total) {
+__device__ __noinline__ CutRec cut_rec(const Seg& g, int block, int grid, int end, int total) {
   CutRec r{0, g.row0, g.rows, g.h, g.f0, g.bad, total};
   if (g.t0 == 0 && g.n < g.nt) {
-    const long long last = end + (g.nt - g.n);
+    const int last = end + (g.nt - g.n);
     int e = block + 1;
-    while (e < grid && total * e / grid < last) ++e;
+#pragma unroll 1
+    while (e < grid && line_at(total, e, grid) < last) ++e;
     r.parts = e - block;
   }
   return r;
@@ -311,7 +320,8 @@ __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(AttnParams p,
   if (r.parts == 0 || c >= NR || f >= r.rows * p.G) return;
   // part j: slot 2 i + 1 of the first block, slot 2 (i + j) of the others
   auto part_of = [&](int j) { return slot_of<NR, D>(p, j == 0 ? 2 * i + 1 : 2 * (i + j)); };
-  auto holds = [&](int j) { return j == 0 || r.total * (i + j) / grid != r.total * (i + j + 1) / grid; };
+  const int some = r.total >= grid ? grid : r.total;  // blocks that have a part of the line
+  auto holds = [&](int j) { return i + j < some; };
   float m = __int_as_float(kNegInfBits);
   for (int j = lane; j < r.parts; j += 32)
     if (holds(j)) m = fmaxf(m, part_of(j)[c]);
@@ -377,13 +387,13 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
   if (p.mask == A_TREE && tid < SPEC_MAX_TREE_NODES) s_sees[tid] = p.sees[tid];
   griddep_wait();
   griddep_launch();
-  long long begin, end, total;
+  int begin, end, total;
   if (!locate<NR, 128>(p, sh, blockIdx.x, gridDim.x, &begin, &end, &total)) {
     fill_nan<E, D>(p, blockIdx.x, gridDim.x);
     begin = end = 0;
   }
   Place at = sh.at;
-  long long left = end - begin;
+  int left = end - begin;
   uint32_t bits = 0;
   if (tid == 0) p.cut[blockIdx.x].parts = 0;
   while (left > 0) {

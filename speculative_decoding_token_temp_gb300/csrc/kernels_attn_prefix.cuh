@@ -208,12 +208,12 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   }
   griddep_wait();
   griddep_launch();
-  long long begin, end, total;
+  int begin, end, total;
   locate<NR, kPreThreads>(p, sh.loc, blockIdx.x, gridDim.x, &begin, &end, &total);  // (one dense sequence: no cu)
   tc_after();
   const uint32_t tmem = sh.tmem;
   Place at = sh.loc.at;
-  long long left = end - begin;
+  int left = end - begin;
 
   if (warp == 8) {
     // ---- the rings of tiles ----

@@ -136,8 +136,7 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
 // A bounded wait. Once one gives up, the block's later waits return at once: the loops run
 // to their end (every address they form is in range whatever the data), and the status
 // word says that the call's results are not to be used.
-__device__ __forceinline__ void tc_wait(uint32_t bar, unsigned parity, volatile int* gave_up, uint32_t* status) {
-  if (mbar_try_wait(bar, parity)) return;
+__device__ __noinline__ void tc_wait_long(uint32_t bar, unsigned parity, volatile int* gave_up, uint32_t* status) {
   for (int it = 0; !mbar_try_wait(bar, parity); ++it) {
     if (*gave_up) return;
     if (it == kTcPollLimit) {
@@ -146,6 +145,9 @@ __device__ __forceinline__ void tc_wait(uint32_t bar, unsigned parity, volatile 
       return;
     }
   }
+}
+__device__ __forceinline__ void tc_wait(uint32_t bar, unsigned parity, volatile int* gave_up, uint32_t* status) {
+  if (!mbar_try_wait(bar, parity)) tc_wait_long(bar, parity, gave_up, status);
 }
 
 // ---- arithmetic on pairs of floats ------------------------------------------
@@ -200,16 +202,21 @@ __device__ __forceinline__ uint32_t rest16(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Eight columns of the values' sums: the three parts' accumulators joined.
+__device__ __forceinline__ void tc_ld4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+// Four columns of the values' sums: the three parts' accumulators joined.
 template <int NR>
-__device__ __forceinline__ void tc_sum_parts(uint32_t at, float (&o)[8]) {
-  uint32_t a[8], b[8], c[8];
-  tc_ld8(at, a);
-  tc_ld8(at + NR, b);
-  tc_ld8(at + 2 * NR, c);
+__device__ __forceinline__ void tc_sum_parts(uint32_t at, float (&o)[4]) {
+  uint32_t a[4], b[4], c[4];
+  tc_ld4(at, a);
+  tc_ld4(at + NR, b);
+  tc_ld4(at + 2 * NR, c);
   tc_wait_ld();
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 4; ++j)
     o[j] = fmaf(fmaf(__uint_as_float(c[j]), 0.0625f, __uint_as_float(b[j])), 0.0625f, __uint_as_float(a[j]));
 }
 
@@ -247,74 +254,71 @@ struct TcShared {
   alignas(16) float delta[NR];      // its last change, and 2^that
   alignas(16) float factor[NR];
   float red[4][NR];                 // of the four warps: maxima, then sums
-  Coef coef[NR];
-  long long idx[NR];
+  float2 coef[NR];                  // weights of a row's values and of the prefix's part
+  alignas(16) int idx[NR];          // row * query heads + head, -1 past the last
 };
 
 // Queries of a stretch staged for the scores' MMA: TPR threads a row find its power of two
 // and write its two parts, rows of D bytes whose 16-byte chunks are exchanged as the swizzle
-// has them.
+// has them. (Loops kept short: what runs once a stretch should not push the tiles' loop out
+// of the instruction caches.)
 template <int D, int NR>
 __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g, TcShared<D, NR>& sh, uint8_t* q, int t) {
   constexpr int TPR = NR == 48 ? 4 : 8, E = D / TPR;
   const int c = t / TPR, part = t % TPR, f = g.f0 + c;
-  const float nan = __int_as_float(0x7fffffff);
   if (c < NR) {  // (whole warps)
-    float x[E];
-    if (f < g.rows * p.G) {
-      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(g.row0 + f / p.G) * p.q_row +
-                            (long long)(g.h * p.G + f % p.G) * p.q_head + part * E;
-      if (((uintptr_t)src & 15) == 0 && E % 8 == 0) {
+    const int i = f / p.G, hq = g.h * p.G + f - i * p.G;
+    const bool here = f < g.rows * p.G;
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(g.row0 + i) * p.q_row + (long long)hq * p.q_head + part * E;
+    const bool vec = ((uintptr_t)src & 15) == 0;
+    uint32_t x[E / 2];
 #pragma unroll
-        for (int i = 0; i < E / 8; ++i) {
-          float y[8];
-          load8<true>(src + i * 8, y);
+    for (int k = 0; k < E / 2; ++k) x[k] = 0;
+    if (here && vec) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[i * 8 + j] = y[j];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = __uint_as_float((uint32_t)__ldg(src + i) << 16);
+      for (int k = 0; k < E / 8; ++k) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + k);
+        x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
       }
-    } else {
+    } else if (here) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = 0.f;
+      for (int k = 0; k < E / 2; ++k) x[k] = (uint32_t)__ldg(src + 2 * k) | (uint32_t)__ldg(src + 2 * k + 1) << 16;
     }
-    float m = 0.f;
-    bool bad = false;
+    // the largest magnitude, by its bits (a NaN or an infinity is above every finite one)
+    uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      m = fmaxf(m, fabsf(x[i]));
-      bad |= !(fabsf(x[i]) <= 3.402823466e38f);
-    }
-    if (bad) m = __int_as_float(0x7f800000);
+    for (int k = 0; k < E / 2; ++k) top = __vmaxu2(top, x[k] & 0x7fff7fffu);
+    top = max(top & 0xffffu, top >> 16);
 #pragma unroll
-    for (int o = 1; o < TPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    bad = m == __int_as_float(0x7f800000);
-    const int e = max((__float_as_int(m) >> 23) - 127, -100) - 7;  // the largest element comes to [128, 256)
-    const float inv = __int_as_float((127 - e) << 23);
+    for (int o = 1; o < TPR; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+    const bool bad = top >= 0x7f80u;
+    const int e = max((int)(top >> 7) - 127, -100) - 7;  // the largest element comes to [128, 256)
+    const float inv = bad ? 0.f : __int_as_float((127 - e) << 23);
     if (part == 0) {
-      sh.rq[c] = bad ? nan : p.c * __int_as_float((e + 127) << 23);
-      sh.row[c] = f / p.G;
+      sh.rq[c] = bad ? __int_as_float(0x7fffffff) : p.c * __int_as_float((e + 127) << 23);
+      sh.row[c] = i;
+      sh.idx[c] = here ? (g.row0 + i) * p.Hq + hq : -1;
       sh.neg_m[c] = 0.f;
     }
+    const int rl = NR + c;
 #pragma unroll
-    for (int i = 0; i < E / 8; ++i) {
+    for (int k = 0; k < E / 8; ++k) {
       uint32_t hi[2], lo[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float y[4], b[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = bad ? 0.f : x[i * 8 + j * 4 + k] * inv;
-        const uint32_t h0 = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t h1 = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
-        hi[j] = h0 | h1 << 16;
+        for (int u = 0; u < 2; ++u) {
+          y[2 * u] = bad ? 0.f : __uint_as_float(x[4 * k + 2 * j + u] << 16) * inv;
+          y[2 * u + 1] = bad ? 0.f : __uint_as_float(x[4 * k + 2 * j + u] & 0xffff0000u) * inv;
+        }
+        hi[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3) |
+                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3) << 16;
         codes4(hi[j], b);
-        const uint32_t l0 = __nv_cvt_float2_to_fp8x2(make_float2(y[0] - b[0], y[1] - b[1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t l1 = __nv_cvt_float2_to_fp8x2(make_float2(y[2] - b[2], y[3] - b[3]), __NV_SATFINITE, __NV_E4M3);
-        lo[j] = l0 | l1 << 16;
+        lo[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[0] - b[0], y[1] - b[1]), __NV_SATFINITE, __NV_E4M3) |
+                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[2] - b[2], y[3] - b[3]), __NV_SATFINITE, __NV_E4M3) << 16;
       }
-      const int at = part * E + i * 8, chunk = at >> 4, rl = NR + c;
+      const int at = part * E + k * 8, chunk = at >> 4;
       const int ch_h = D == 128 ? chunk ^ (c & 7) : chunk ^ ((c >> 1) & 3);
       const int ch_l = D == 128 ? chunk ^ (rl & 7) : chunk ^ ((rl >> 1) & 3);
       *reinterpret_cast<uint2*>(q + c * D + ch_h * 16 + (at & 15)) = make_uint2(hi[0], hi[1]);
@@ -366,7 +370,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   }
   griddep_wait();
   griddep_launch();
-  long long begin, end, total;
+  int begin, end, total;
   const bool ok = locate<NR, kTcThreads>(p, sh.loc, blockIdx.x, gridDim.x, &begin, &end, &total);
   tc_after();
   const uint32_t tmem = sh.tmem;
@@ -375,7 +379,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     begin = end = 0;
   }
   Place at = sh.loc.at;
-  long long left = end - begin;
+  int left = end - begin;
 
   if (warp == 8) {
     // ---- the rings of tiles ----
@@ -438,32 +442,32 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     constexpr uint64_t hi_p = mma_desc_hi(T::kChunk, 0) | (uint64_t)(128 >> 4) << 16;  // weights: 8 tokens, then 16 columns on
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
     int gi = 0, nseg = 0;
-    auto scores = [&](int i) {
-      const int st = i % NK;
-      if (i > 0) tc_wait(bar(sh.s_free), (i - 1) & 1, gave_up, p.status);
-      tc_wait(bar(sh.k_full[st]), (i / NK) & 1, gave_up, p.status);
-      __syncwarp();
-      tc_after();
-      if (elect()) {
-        const uint32_t a = (base + T::oK + st * T::kTileBytes) >> 4, b = (base + T::oQ) >> 4;
-#pragma unroll
-        for (int s = 0; s < D / 32; ++s) mma_f8(tm, hi_d | (a + s * 2), hi_d | (b + s * 2), id_s, s > 0);
-        mma_commit(bar(sh.s_full));
-        mma_commit(bar(sh.k_free[st]));
-      }
-      __syncwarp();
-    };
     while (left > 0) {
       const int n = __shfl_sync(kFull, next_seg<NR>(p, at, left).n, 0);
       if (n == 0) continue;
       tc_wait(bar(sh.q_full), nseg & 1, gave_up, p.status);
       ++nseg;
-      scores(gi);
-      for (int k = 0; k < n; ++k, ++gi) {
-        if (k + 1 < n) scores(gi + 1);
-        const int st = gi % NV;
-        tc_wait(bar(sh.v_full[st]), (gi / NV) & 1, gave_up, p.status);
-        tc_wait(bar(sh.p_full), gi & 1, gave_up, p.status);
+#pragma unroll 1
+      for (int k = -1; k < n; ++k) {
+        if (k + 1 < n) {
+          const int i = gi + k + 1, st = i % NK;
+          if (i > 0) tc_wait(bar(sh.s_free), (i - 1) & 1, gave_up, p.status);
+          tc_wait(bar(sh.k_full[st]), (i / NK) & 1, gave_up, p.status);
+          __syncwarp();
+          tc_after();
+          if (elect()) {
+            const uint32_t a = (base + T::oK + st * T::kTileBytes) >> 4, b = (base + T::oQ) >> 4;
+#pragma unroll
+            for (int s = 0; s < D / 32; ++s) mma_f8(tm, hi_d | (a + s * 2), hi_d | (b + s * 2), id_s, s > 0);
+            mma_commit(bar(sh.s_full));
+            mma_commit(bar(sh.k_free[st]));
+          }
+          __syncwarp();
+        }
+        if (k < 0) continue;
+        const int i = gi + k, st = i % NV;
+        tc_wait(bar(sh.v_full[st]), (i / NV) & 1, gave_up, p.status);
+        tc_wait(bar(sh.p_full), i & 1, gave_up, p.status);
         __syncwarp();
         tc_after();
         if (elect()) {
@@ -482,6 +486,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         }
         __syncwarp();
       }
+      gi += n;
     }
     // no MMA is left in flight when the block ends, even after a wait that gave up
     if (elect()) mma_commit(bar(sh.drained));
@@ -503,7 +508,6 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       const Seg g = next_seg<NR>(p, at, left);
       if (g.n == 0) continue;
       if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, end, total);
-      const int flat = g.rows * p.G;
       stage_queries<D, NR>(p, g, sh, mem + T::oQ, tid);
       fence_async();
       mbar_arrive(bar(sh.q_full));
@@ -552,7 +556,13 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         const float ev = fine ? (float)((int)vb - kExpBias) : 0.f;
         const float isv = fine ? __int_as_float((2 * kExpBias - (int)vb) << 23) : 1.f;
         const f2 ks2 = pack(ks, ks), ev2 = pack(ev, ev), isv2 = pack(isv, isv);
-        const Sight sight = sight_of(masked ? p.mask : A_ALL, sh.sees, g.rows, g.len, tok);
+        uint32_t sight = ~0u;  // bit c: the row of column c0 + c sees this token
+        if (masked) {
+          const Sight sees = sight_of(p.mask, sh.sees, g.rows, g.len, tok);
+          sight = 0;
+#pragma unroll 1
+          for (int c = 0; c < NH; ++c) sight |= (uint32_t)sees(sh.row[c0 + c]) << c;
+        }
         // scores
         tc_wait(bar(sh.s_full), gi & 1, gave_up, p.status);
         tc_after();
@@ -578,11 +588,8 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           unpack(y0, z[0], z[1]);
           unpack(y1, z[2], z[3]);
           if (masked) {
-            const int4 rows = *reinterpret_cast<const int4*>(&sh.row[c0 + c]);
-            const int ri[4] = {rows.x, rows.y, rows.z, rows.w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (!sight(ri[q])) z[q] = ninf;
+            for (int q = 0; q < 4; ++q) z[q] = sight >> (c + q) & 1 ? z[q] : ninf;
             y0 = pack(z[0], z[1]);
             y1 = pack(z[2], z[3]);
           }
@@ -699,16 +706,14 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       float* slot = whole ? nullptr : slot_of<NR, D>(p, 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0));
       bar_sync(1, kTcSoft);
       if (tid < NR) {
-        const int f = g.f0 + tid;
         const float l = sh.red[0][tid] + sh.red[1][tid] + sh.red[2][tid] + sh.red[3][tid], m = -sh.neg_m[tid];
-        const long long idx = (long long)(g.row0 + f / p.G) * p.Hq + g.h * p.G + f % p.G;
-        sh.idx[tid] = f < flat ? idx : -1;
+        const int idx = sh.idx[tid];
         if (!whole) {
           slot[tid] = l == 0.f ? ninf : m;  // a row that saw nothing has no reference
           slot[NR + tid] = l;
-        } else if (f < flat) {
+        } else if (idx >= 0) {
           const Coef r = row_coef(p, idx, m, l, g.bad);
-          sh.coef[tid] = r;
+          sh.coef[tid] = make_float2(r.a, r.b);
           finish_lse(p, idx, r);
         }
       }
@@ -718,27 +723,40 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       float* const half = reinterpret_cast<float*>(mem + T::oP) + c0 * D;  // the weights' memory, read by now
       if (kHalves == 2 && t >= D) {
 #pragma unroll 1
-        for (int c = 0; c < NH; c += 8) {
-          float o[8];
+        for (int c = 0; c < NH; c += 4) {
+          float o[4];
           tc_sum_parts<NR>(tO + c, o);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) half[(c + j) * D + d] = o[j];
+          for (int j = 0; j < 4; ++j) half[(c + j) * D + d] = o[j];
         }
       }
       bar_sync(1, kTcSoft);
-      if (t < D) {
+      if (t < D && !whole) {
+        slot += 2 * NR + c0 * D + d;
 #pragma unroll 1
-        for (int c = 0; c < NH; c += 8) {
-          float o[8];
+        for (int c = 0; c < NH; c += 4, slot += 4 * D) {
+          float o[4];
           tc_sum_parts<NR>(tO + c, o);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const long long idx = sh.idx[c0 + c + j];
+          for (int j = 0; j < 4; ++j) slot[j * D] = kHalves == 2 ? o[j] + half[(c + j) * D + d] : o[j];
+        }
+      } else if (t < D) {
+        const bool join = p.pre_o != nullptr;
+#pragma unroll 1
+        for (int c = 0; c < NH; c += 4) {
+          const int4 idx = *reinterpret_cast<const int4*>(&sh.idx[c0 + c]);
+          const int row[4] = {idx.x, idx.y, idx.z, idx.w};
+          float o[4], pre[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) pre[j] = join && row[j] >= 0 ? __ldcg(p.pre_o + (long long)row[j] * D + d) : 0.f;
+          tc_sum_parts<NR>(tO + c, o);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
             if (kHalves == 2) o[j] += half[(c + j) * D + d];
-            if (!whole)
-              slot[2 * NR + (c0 + c + j) * D + d] = o[j];
-            else if (idx >= 0)
-              finish<uint16_t, D>(p, idx, d, o[j], sh.coef[c0 + c + j]);
+            const float2 r = sh.coef[c0 + c + j];
+            float y = o[j] * r.x;
+            if (r.y != 0.f) y = fmaf(pre[j], r.y, y);
+            if (row[j] >= 0) store_out<uint16_t, D>(p, row[j], d, y);
           }
         }
       }

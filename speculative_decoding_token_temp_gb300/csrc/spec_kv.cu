@@ -123,6 +123,7 @@ constexpr int kMaxGridS = 1024;  // largest grid of the 32-bit kernel (its works
 
 // tiles that a segment's beginning and end count for on the line of tiles
 constexpr int kSegCostT = 4, kSegCostS = 1, kSegCostP = 2;
+constexpr long long kMaxLine = 1LL << 30;  // a line of tiles is counted in ints
 constexpr int kMaxGridP = 160;   // of attn_prefix_kernel (one block an SM)
 // rows that share the prefix's keys from which on it is widened and computed in 128-row tiles
 constexpr int kWideRows = 96;
@@ -132,6 +133,7 @@ struct AttnLayout {
   int nr, pre_nr;      // rows of a row block, of the two passes
   long long grid;      // blocks of the pass over the sequences' tokens, at most
   long long pre_grid;  // of the prefix pass
+  long long line;      // the longer pass's line of tiles, at most
   bool wide;           // the prefix widened and computed by attn_prefix_kernel
   long long tiles;     // of the prefix
   size_t part, cut, pre_o, pre_lse, k16, v16, exp, total;
@@ -163,6 +165,7 @@ AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dt
   const int more = tc ? kSegCostT : kSegCostS;  // a block for every tile of the line at most
   const long long own = (long long)g.B * cdiv((long long)(g.gamma + 1) * G, L.nr) * c.kv_heads * (nt + more);
   const long long pre = g.prefix_len > 0 ? cdiv(rows_of(g) * G, L.pre_nr) * c.kv_heads * (cdiv(g.prefix_len, kTile) + more) : 0;
+  L.line = own > pre ? own : pre;
   L.grid = own < cap ? own : cap;
   const long long pre_cap = L.wide ? kMaxGridP : cap;
   L.pre_grid = pre < pre_cap ? pre : pre_cap;
@@ -469,7 +472,8 @@ spec_status spec_kv_read(spec_kv_cache c, spec_kv_rows r, spec_dtype dtype, void
 
 size_t spec_attention_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype) {
   if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || check_attn(g, c) != SPEC_OK) return 0;
-  return attn_layout(g, c, dtype).total;
+  const AttnLayout L = attn_layout(g, c, dtype);
+  return L.line <= kMaxLine ? L.total : 0;
 }
 
 spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,
@@ -488,6 +492,7 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
   if ((g.pages_per_seq > 0 && !g.page_table) || !on(g.page_table, 4)) return SPEC_ERR_INVALID_ARG;
   if ((g.prefix_len > 0 && !g.prefix_table) || !on(g.prefix_table, 4)) return SPEC_ERR_INVALID_ARG;
   const AttnLayout L = attn_layout(g, c, dtype);
+  if (L.line > kMaxLine) return SPEC_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < L.total || !on(workspace, 256)) return SPEC_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
