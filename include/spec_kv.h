@@ -56,7 +56,7 @@ typedef struct {
  * the verification of a tree, the nodes of the accepted path are appended at their
  * positions and the others left out.) */
 typedef struct {
-  int32_t rows;
+  int32_t rows; /* 0..2^22 */
   int32_t sequences;
   int32_t pages_per_seq;
   const int32_t* page_table; /* device [sequences][pages_per_seq] */

@@ -670,8 +670,11 @@ def spec_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv
     lib = _lib.lib()
     nbytes = int(lib.spec_attention_workspace_bytes(g, cache.desc, dt))
     stream = _stream_handle(dev)
-    if workspace is None:  # a default workspace for each stream: calls on two streams may overlap
-        workspace = _DEFAULT_WS.setdefault((dev.type, dev.index, stream), Workspace())
+    if workspace is None:
+        if torch.cuda.is_current_stream_capturing():  # a graph's own, from its memory pool
+            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        else:  # a default workspace for each stream: calls on two streams may overlap
+            workspace = _DEFAULT_WS.setdefault((dev.type, dev.index, stream), Workspace())
     ws = _workspace(workspace, nbytes, dev)
     check("spec_attention", lib.spec_attention(g, cache.desc, dt, q.data_ptr(), q_row, q_head, y.data_ptr(), _ptr(lse),
                                                st.data_ptr(), ws.data_ptr(), ws.numel(), stream))

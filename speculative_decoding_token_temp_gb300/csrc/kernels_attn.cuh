@@ -171,7 +171,7 @@ struct Seg {
 // The next stretch at `at` (advanced), at most `left` tiles of the line (reduced). It may
 // be empty (n = 0): the block's part of the line ends among the tiles that only count.
 template <int NR>
-__device__ __noinline__ Seg next_seg(const AttnParams& p, Place& at, int& left) {
+__device__ __forceinline__ Seg next_seg(const AttnParams& p, Place& at, int& left) {
   Seg g;
   const SeqInfo s = seq_info(p, at.b);
   g.row0 = s.row0, g.rows = s.rows, g.len = s.len, g.bad = s.bad;
@@ -220,25 +220,29 @@ struct Coef {
   float a, b, lse2;
 };
 
-__device__ __noinline__ Coef row_coef(const AttnParams& p, long long idx, float m, float l, bool bad) {
-  Coef r;
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// m, l: the row's reference and sum; pre: the log-sum of the prefix's part (-inf: none). The
+// approximate functions are off by at most 2^-22 of their results.
+__device__ __forceinline__ Coef row_coef(float pre, float m, float l, bool bad) {
   const float nan = __int_as_float(0x7fffffff), ninf = __int_as_float(kNegInfBits);
-  if (bad) return Coef{nan, 0.f, nan};
-  r.lse2 = l == 0.f ? ninf : m + log2f(l);
-  r.a = l == 0.f ? 0.f : 1.f / l;
-  r.b = 0.f;
-  if (p.pre_o != nullptr) {
-    const float q = __ldcg(p.pre_lse + idx);
-    if (l == 0.f) {
-      r.b = q == ninf ? 0.f : 1.f;
-      r.lse2 = q;
-    } else if (q != ninf) {
-      const float mx = fmaxf(r.lse2, q), e1 = exp2f(r.lse2 - mx), e2 = exp2f(q - mx), s = e1 + e2;
-      r.a *= e1 / s;
-      r.b = e2 / s;
-      r.lse2 = mx + log2f(s);
-    }
+  Coef r{0.f, pre == ninf ? 0.f : 1.f, pre};
+  if (l != 0.f) {
+    const float own = m + lg2(l), mx = fmaxf(own, pre), e1 = ex2(own - mx), e2 = ex2(pre - mx), s = e1 + e2, is = rcp(s);
+    r.a = e1 * is * rcp(l);
+    r.b = pre == ninf ? 0.f : e2 * is;  // (never a NaN where there is no prefix: its part is then not there to be read)
+    r.lse2 = mx + lg2(s);
   }
+  if (bad) r.a = r.lse2 = nan;
   return r;
 }
 
@@ -263,7 +267,7 @@ __device__ __forceinline__ void store_out(const AttnParams& p, long long idx, in
 template <typename E, int D>
 __device__ __forceinline__ void finish(const AttnParams& p, long long idx, int d, float v, const Coef& r) {
   float x = v * r.a;
-  if (r.b != 0.f) x += __ldcg(p.pre_o + idx * D + d) * r.b;
+  if (p.pre_o != nullptr && r.b != 0.f) x += __ldcg(p.pre_o + idx * D + d) * r.b;
   store_out<E, D>(p, idx, d, x);
 }
 
@@ -294,7 +298,7 @@ __device__ __noinline__ void fill_nan(const AttnParams& p, int block, int blocks
 
 // What block `block` of `grid` leaves for attn_merge_kernel about a stretch g that ends the
 // block's part of the line (at `end` of `total`).
-__device__ __noinline__ CutRec cut_rec(const Seg& g, int block, int grid, int end, int total) {
+__device__ __forceinline__ CutRec cut_rec(const Seg& g, int block, int grid, int end, int total) {
   CutRec r{0, g.row0, g.rows, g.h, g.f0, g.bad, total};
   if (g.t0 == 0 && g.n < g.nt) {
     const int last = end + (g.nt - g.n);
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(AttnParams p,
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
   const long long idx = (long long)(r.row0 + f / p.G) * p.Hq + r.h * p.G + f % p.G;
-  const Coef co = row_coef(p, idx, mu, l, r.bad != 0);
+  const Coef co = row_coef(p.pre_o != nullptr ? __ldcg(p.pre_lse + idx) : __int_as_float(kNegInfBits), mu, l, r.bad != 0);
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) finish<E, D>(p, idx, lane * (D / 32) + k, acc[k], co);
   if (lane == 0) finish_lse(p, idx, co);
@@ -545,7 +549,7 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
         slot[2 * NR + e] = v;
       } else if (f < g.rows * p.G) {
         const long long idx = (long long)(g.row0 + f / p.G) * p.Hq + g.h * p.G + f % p.G;
-        const Coef r = row_coef(p, idx, sm[c] == ninf ? 0.f : sm[c], sl[c], g.bad);
+        const Coef r = row_coef(p.pre_o != nullptr ? __ldcg(p.pre_lse + idx) : ninf, sm[c] == ninf ? 0.f : sm[c], sl[c], g.bad);
         finish<E, D>(p, idx, d, v, r);
         if (d == 0) finish_lse(p, idx, r);
       }

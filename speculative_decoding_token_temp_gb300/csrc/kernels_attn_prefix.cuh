@@ -225,12 +225,12 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         for (int k = 0; k < g.n; ++k, ++gi) {
           const int st = gi % NST, row = (g.h * wide.tiles + g.t0 + k) * kTile;
           const uint32_t bk = bar(sh.k_full[st]), bv = bar(sh.v_full[st]);
-          if (gi >= NST) tc_wait(bar(sh.k_free[st]), (gi / NST - 1) & 1, gave_up, p.status);
+          if (gi >= NST) tc_wait_one(bar(sh.k_free[st]), (gi / NST - 1) & 1, gave_up, p.status);
           mbar_expect_arrive(bk, T::kTileBytes);
 #pragma unroll
           for (int a = 0; a < T::kAtoms; ++a)
             tma_rows(base + T::oK + st * T::kTileBytes + a * 16384, &map_k, a * 64, row, bk);
-          if (gi >= NST) tc_wait(bar(sh.v_free[st]), (gi / NST - 1) & 1, gave_up, p.status);
+          if (gi >= NST) tc_wait_one(bar(sh.v_free[st]), (gi / NST - 1) & 1, gave_up, p.status);
           mbar_expect_arrive(bv, T::kTileBytes);
 #pragma unroll
           for (int a = 0; a < T::kAtoms; ++a)
@@ -423,7 +423,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           slot[c] = m;
           slot[NR + c] = l;
         } else if (f < flat) {
-          r = row_coef(p, idx, m, l, false);
+          r = row_coef(ninf, m, l, false);
           finish_lse(p, idx, r);
         }
         float* dst = whole ? p.dst_o + idx * D : slot + 2 * NR + c * D;

@@ -43,6 +43,7 @@ namespace sv {
 
 constexpr int kTcThreads = 320;        // eight softmax warps, one for copies, one for MMAs
 constexpr int kTcSoft = 256;
+constexpr int kSegRing = 8;            // more stretches than tiles can be in the rings
 constexpr int kTcPollLimit = 1 << 18;  // bounded waits (SPEC_DEV_TIMEOUT): about a second
 constexpr float kTop = 4.f;            // a fresh reference puts the largest weight at 2^4 ...
 constexpr float kOver = 8.f;           // ... and is renewed when one would pass 2^8 (e4m3 ends at 448)
@@ -101,11 +102,6 @@ __device__ __forceinline__ void tc_ld8(uint32_t a, uint32_t (&r)[8]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(a));
 }
-__device__ __forceinline__ void tc_st8(uint32_t a, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(a)
-               : "memory");
-}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -146,8 +142,13 @@ __device__ __noinline__ void tc_wait_long(uint32_t bar, unsigned parity, volatil
     }
   }
 }
-__device__ __forceinline__ void tc_wait(uint32_t bar, unsigned parity, volatile int* gave_up, uint32_t* status) {
+__device__ __forceinline__ void tc_wait_one(uint32_t bar, unsigned parity, volatile int* gave_up, uint32_t* status) {
   if (!mbar_try_wait(bar, parity)) tc_wait_long(bar, parity, gave_up, status);
+}
+// The same by a whole warp, which goes on together (tensor-memory accesses and elections want it converged).
+__device__ __forceinline__ void tc_wait(uint32_t bar, unsigned parity, volatile int* gave_up, uint32_t* status) {
+  tc_wait_one(bar, parity, gave_up, status);
+  __syncwarp();
 }
 
 // ---- arithmetic on pairs of floats ------------------------------------------
@@ -207,6 +208,10 @@ __device__ __forceinline__ void tc_ld4(uint32_t a, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a));
 }
+__device__ __forceinline__ void tc_st4(uint32_t a, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0,%1,%2,%3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(a)
+               : "memory");
+}
 // Four columns of the values' sums: the three parts' accumulators joined.
 template <int NR>
 __device__ __forceinline__ void tc_sum_parts(uint32_t at, float (&o)[4]) {
@@ -220,29 +225,13 @@ __device__ __forceinline__ void tc_sum_parts(uint32_t at, float (&o)[4]) {
     o[j] = fmaf(fmaf(__uint_as_float(c[j]), 0.0625f, __uint_as_float(b[j])), 0.0625f, __uint_as_float(a[j]));
 }
 
-// Sums over a warp of 8 columns held by every lane: lane c (mod 8) gets column c's.
-__device__ __forceinline__ float column_sums(float (&v)[8], int lane) {
-#pragma unroll
-  for (int o = 16; o >= 8; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
-#pragma unroll
-  for (int o = 4; o >= 1; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(kFull, send, o);
-    }
-  }
-  return v[0];
-}
-
 template <int D, int NR>
 struct TcShared {
   using T = TcShape<D, NR>;
   LocateShared loc;
   uint64_t k_full[T::kNK], k_free[T::kNK], v_full[T::kNV], v_free[T::kNV], q_full, drained, s_full, s_free, p_full, o_done;
+  uint64_t seg_full[kSegRing];
+  Seg seg[kSegRing];                // the block's stretches, as the copying warp comes to them; n = 0: no more
   uint32_t tmem;
   int gave_up;
   uint32_t bad_pages[T::kNK];
@@ -253,7 +242,8 @@ struct TcShared {
   alignas(16) float neg_m[NR];      // the reference, negated
   alignas(16) float delta[NR];      // its last change, and 2^that
   alignas(16) float factor[NR];
-  float red[4][NR];                 // of the four warps: maxima, then sums
+  float red[4][NR];                 // of the warps of a token each: maxima of the columns
+  float pre[NR];                    // log-sum of the prefix's part
   float2 coef[NR];                  // weights of a row's values and of the prefix's part
   alignas(16) int idx[NR];          // row * query heads + head, -1 past the last
 };
@@ -267,27 +257,32 @@ __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g,
   constexpr int TPR = NR == 48 ? 4 : 8, E = D / TPR;
   const int c = t / TPR, part = t % TPR, f = g.f0 + c;
   if (c < NR) {  // (whole warps)
-    const int i = f / p.G, hq = g.h * p.G + f - i * p.G;
+    const int i = f / p.G, hq = g.h * p.G + f - i * p.G, idx = (g.row0 + i) * p.Hq + hq;
     const bool here = f < g.rows * p.G;
     const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(g.row0 + i) * p.q_row + (long long)hq * p.q_head + part * E;
     const bool vec = ((uintptr_t)src & 15) == 0;
-    uint32_t x[E / 2];
+    float pre = __int_as_float(kNegInfBits);
+    if (part == 0 && here && p.pre_o != nullptr) pre = __ldcg(p.pre_lse + idx);
+    uint4 x[E / 8];
 #pragma unroll
-    for (int k = 0; k < E / 2; ++k) x[k] = 0;
+    for (int k = 0; k < E / 8; ++k) x[k] = make_uint4(0, 0, 0, 0);
     if (here && vec) {
 #pragma unroll
-      for (int k = 0; k < E / 8; ++k) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + k);
-        x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
-      }
+      for (int k = 0; k < E / 8; ++k) x[k] = __ldg(reinterpret_cast<const uint4*>(src) + k);
     } else if (here) {
 #pragma unroll
-      for (int k = 0; k < E / 2; ++k) x[k] = (uint32_t)__ldg(src + 2 * k) | (uint32_t)__ldg(src + 2 * k + 1) << 16;
+      for (int k = 0; k < E / 8; ++k) {
+        uint32_t* w = &x[k].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = (uint32_t)__ldg(src + 8 * k + 2 * j) | (uint32_t)__ldg(src + 8 * k + 2 * j + 1) << 16;
+      }
     }
     // the largest magnitude, by its bits (a NaN or an infinity is above every finite one)
     uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < E / 2; ++k) top = __vmaxu2(top, x[k] & 0x7fff7fffu);
+    for (int k = 0; k < E / 8; ++k)
+      top = __vmaxu2(__vmaxu2(top, __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu)),
+                     __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu));
     top = max(top & 0xffffu, top >> 16);
 #pragma unroll
     for (int o = 1; o < TPR; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
@@ -297,32 +292,29 @@ __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g,
     if (part == 0) {
       sh.rq[c] = bad ? __int_as_float(0x7fffffff) : p.c * __int_as_float((e + 127) << 23);
       sh.row[c] = i;
-      sh.idx[c] = here ? (g.row0 + i) * p.Hq + hq : -1;
+      sh.idx[c] = here ? idx : -1;
+      sh.pre[c] = pre;
       sh.neg_m[c] = 0.f;
     }
     const int rl = NR + c;
 #pragma unroll
     for (int k = 0; k < E / 8; ++k) {
-      uint32_t hi[2], lo[2];
+      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float y[4], b[4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          y[2 * u] = bad ? 0.f : __uint_as_float(x[4 * k + 2 * j + u] << 16) * inv;
-          y[2 * u + 1] = bad ? 0.f : __uint_as_float(x[4 * k + 2 * j + u] & 0xffff0000u) * inv;
-        }
-        hi[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3) |
-                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3) << 16;
-        codes4(hi[j], b);
-        lo[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[0] - b[0], y[1] - b[1]), __NV_SATFINITE, __NV_E4M3) |
-                (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[2] - b[2], y[3] - b[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+      for (int j = 0; j < 4; ++j) {
+        // scaled to [0, 256) an element is exact in f16 (8 bits) down to 2^-17 of it
+        const uint32_t h = bad ? 0u : half2_of(__uint_as_float(w[j] << 16) * inv, __uint_as_float(w[j] & 0xffff0000u) * inv);
+        hi[j] = narrow2(h);
+        uint32_t r;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(widen2(hi[j])));
+        lo[j] = narrow2(r);
       }
       const int at = part * E + k * 8, chunk = at >> 4;
       const int ch_h = D == 128 ? chunk ^ (c & 7) : chunk ^ ((c >> 1) & 3);
       const int ch_l = D == 128 ? chunk ^ (rl & 7) : chunk ^ ((rl >> 1) & 3);
-      *reinterpret_cast<uint2*>(q + c * D + ch_h * 16 + (at & 15)) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(q + rl * D + ch_l * 16 + (at & 15)) = make_uint2(lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(q + c * D + ch_h * 16 + (at & 15)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+      *reinterpret_cast<uint2*>(q + rl * D + ch_l * 16 + (at & 15)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
     }
   }
 }
@@ -351,6 +343,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       mbar_init(bar(sh.v_full[i]), 1);
       mbar_init(bar(sh.v_free[i]), 1);
     }
+    for (int i = 0; i < kSegRing; ++i) mbar_init(bar(sh.seg_full[i]), 1);
     mbar_init(bar(sh.q_full), kTcSoft);
     mbar_init(bar(sh.drained), 1);
     mbar_init(bar(sh.s_full), 1);
@@ -383,13 +376,21 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
 
   if (warp == 8) {
     // ---- the rings of tiles ----
-    int gi = 0;
+    int gi = 0, ns = 0;
     uint32_t bits = 0;
     const int psz = 1 << p.page_shift, box = min(psz, kTile), np = kTile / box;
+    if (lane == 0) p.cut[blockIdx.x].parts = 0;
     while (left > 0) {
       const Seg g = next_seg<NR>(p, at, left);
       if (g.n == 0) continue;
       if (g.bad) bits |= SPEC_DEV_OFFSETS;
+      if (lane == 0) {
+        if (left == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, end, total);
+        // the stretch that had this place is read: its tiles left the rings before the ones in front of this one's came in
+        sh.seg[ns % kSegRing] = g;
+        mbar_arrive(bar(sh.seg_full[ns % kSegRing]));
+      }
+      ++ns;
       auto page_of = [&](int tile) -> int {  // of this lane's part of a tile
         const int t = tile * kTile + lane * box;
         return lane < np && t < g.len ? __ldg(g.pages + (t >> p.page_shift)) : -2;
@@ -425,6 +426,10 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         page = next;
       }
     }
+    if (lane == 0) {
+      sh.seg[ns % kSegRing].n = 0;
+      mbar_arrive(bar(sh.seg_full[ns % kSegRing]));
+    }
     if (bits) atomicOr(p.status, bits);
     // no copy is left in flight when the block ends, even after a wait that gave up
     for (int i = 0; i < NK; ++i)
@@ -441,12 +446,12 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     constexpr uint64_t lbo_v = (uint64_t)(kTile / 2 * 64 >> 4) << 16;           // head_dim 64: to the second 64 tokens
     constexpr uint64_t hi_p = mma_desc_hi(T::kChunk, 0) | (uint64_t)(128 >> 4) << 16;  // weights: 8 tokens, then 16 columns on
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-    int gi = 0, nseg = 0;
-    while (left > 0) {
-      const int n = __shfl_sync(kFull, next_seg<NR>(p, at, left).n, 0);
-      if (n == 0) continue;
-      tc_wait(bar(sh.q_full), nseg & 1, gave_up, p.status);
-      ++nseg;
+    int gi = 0;
+    for (int ns = 0;; ++ns) {
+      tc_wait(bar(sh.seg_full[ns % kSegRing]), (ns / kSegRing) & 1, gave_up, p.status);
+      const int n = __shfl_sync(kFull, *gave_up ? 0 : sh.seg[ns % kSegRing].n, 0);
+      if (n == 0) break;
+      tc_wait(bar(sh.q_full), ns & 1, gave_up, p.status);
 #pragma unroll 1
       for (int k = -1; k < n; ++k) {
         if (k + 1 < n) {
@@ -503,11 +508,10 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     const float nan = __int_as_float(0x7fffffff), ninf = __int_as_float(kNegInfBits);
     int gi = 0;
     f2 l2[NH / 2];
-    if (tid == 0) p.cut[blockIdx.x].parts = 0;
-    while (left > 0) {
-      const Seg g = next_seg<NR>(p, at, left);
-      if (g.n == 0) continue;
-      if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, end, total);
+    for (int ns = 0;; ++ns) {
+      tc_wait(bar(sh.seg_full[ns % kSegRing]), (ns / kSegRing) & 1, gave_up, p.status);
+      const Seg g = sh.seg[ns % kSegRing];
+      if (bar_or(1, kTcSoft, g.n == 0 || *gave_up)) break;  // (all threads alike, also after a wait that gave up)
       stage_queries<D, NR>(p, g, sh, mem + T::oQ, tid);
       fence_async();
       mbar_arrive(bar(sh.q_full));
@@ -531,22 +535,20 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           const int sv = gi % NV;
           if (c0 == 0) {
             tc_wait(bar(sh.v_full[sv]), (gi / NV) & 1, gave_up, p.status);
-            uint8_t* src = mem + T::oV + sv * T::kTileBytes + t * D;
-            const bool zero = !live || hurt;
-            bool code = false;
-#pragma unroll 1
-            for (int ch = 0; ch < D / 16; ++ch) {
-              uint4 v = *reinterpret_cast<const uint4*>(src + ((ch ^ t) & (D / 16 - 1)) * 16);
-              uint32_t* q = &v.x;
+            uint4* src = reinterpret_cast<uint4*>(mem + T::oV + sv * T::kTileBytes + t * D);
+            uint32_t code = 0;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t mk = __vcmpeq4(q[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                code |= mk != 0;
-                q[j] = zero ? 0u : q[j] & ~mk;
-              }
-              *reinterpret_cast<uint4*>(src + ((ch ^ t) & (D / 16 - 1)) * 16) = v;
+            for (int ch = 0; ch < D / 16; ++ch) {
+              const uint4 v = src[(ch ^ t) & (D / 16 - 1)];
+              code |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
+                      ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
             }
-            sh.nan_code[t] = code;
+            const bool nan_here = code & 0x80808080u;
+            if (!live || hurt || nan_here) {
+#pragma unroll 1
+              for (int ch = 0; ch < D / 16; ++ch) src[(ch ^ t) & (D / 16 - 1)] = make_uint4(0, 0, 0, 0);
+            }
+            sh.nan_code[t] = nan_here;
           }
           bar_sync(1, kTcSoft);
           hurt |= sh.nan_code[t] != 0;
@@ -559,9 +561,14 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         uint32_t sight = ~0u;  // bit c: the row of column c0 + c sees this token
         if (masked) {
           const Sight sees = sight_of(p.mask, sh.sees, g.rows, g.len, tok);
-          sight = 0;
+          // rows come in order, G columns each: the first column that sees the token
+          const int from = min(max((long long)sees.from * p.G - g.f0 - c0, 0ll), 32ll);
+          sight = from >= 32 ? 0u : ~0u << from;
+          if (p.mask == A_TREE && sees.nodes != ~0ull) {
 #pragma unroll 1
-          for (int c = 0; c < NH; ++c) sight |= (uint32_t)sees(sh.row[c0 + c]) << c;
+            for (int c = 0; c < NH; ++c)
+              if (!sees(sh.row[c0 + c])) sight &= ~(1u << c);
+          }
         }
         // scores
         tc_wait(bar(sh.s_full), gi & 1, gave_up, p.status);
@@ -625,7 +632,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
             const float mx = fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid]));
             if (mx != ninf && (first || mx > kTop)) d = mx - kTop;
             sh.delta[tid] = -d;
-            sh.factor[tid] = ex2(-d);
+sh.factor[tid] = first ? 1.f : ex2(-d);  // (nothing is summed yet: 0 times an infinity is no 0)
             sh.neg_m[tid] -= d;
           }
           bar_sync(1, kTcSoft);
@@ -634,32 +641,31 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
             tc_after();
           }
 #pragma unroll
-          for (int c = 0; c < NH; c += 8) {
-            bool moved = false;
-#pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              const float4 d = *reinterpret_cast<const float4*>(&sh.delta[c0 + c + j]);
-              moved |= d.x != 0.f || d.y != 0.f || d.z != 0.f || d.w != 0.f;
-              x[(c + j) / 2] = add2(x[(c + j) / 2], pack(d.x, d.y));
-              x[(c + j) / 2 + 1] = add2(x[(c + j) / 2 + 1], pack(d.z, d.w));
-            }
-            if (!first && moved) {  // (the same for all threads of a warp)
-#pragma unroll
-              for (int j = 0; j < 8; j += 2) {
-                const float2 f = *reinterpret_cast<const float2*>(&sh.factor[c0 + c + j]);
-                l2[(c + j) / 2] = mul2(l2[(c + j) / 2], pack(f.x, f.y));
-              }
+          for (int c = 0; c < NH; c += 4) {
+            const float4 d = *reinterpret_cast<const float4*>(&sh.delta[c0 + c]), f = *reinterpret_cast<const float4*>(&sh.factor[c0 + c]);
+            x[c / 2] = add2(x[c / 2], pack(d.x, d.y));
+            x[c / 2 + 1] = add2(x[c / 2 + 1], pack(d.z, d.w));
+            l2[c / 2] = mul2(l2[c / 2], pack(f.x, f.y));
+            l2[c / 2 + 1] = mul2(l2[c / 2 + 1], pack(f.z, f.w));
+          }
+          if (!first) {
 #pragma unroll 1
-              for (int part = 0; part < 3; ++part) {
-                uint32_t o[8];
-                tc_ld8(tO + part * NR + c, o);
-                tc_wait_ld();
+            for (int c = 0; c < NH; c += 4) {
+              const float4 f4 = *reinterpret_cast<const float4*>(&sh.factor[c0 + c]);
+              const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+              if (f[0] == 1.f && f[1] == 1.f && f[2] == 1.f && f[3] == 1.f) continue;  // (the same for all threads of a warp)
+              uint32_t o[3][4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.factor[c0 + c + j]);
-                tc_st8(tO + part * NR + c, o);
+              for (int part = 0; part < 3; ++part) tc_ld4(tO + part * NR + c, o[part]);
+              tc_wait_ld();
+#pragma unroll
+              for (int part = 0; part < 3; ++part) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[part][j] = __float_as_uint(__uint_as_float(o[part][j]) * f[j]);
+                tc_st4(tO + part * NR + c, o[part]);
               }
-              tc_wait_st();
             }
+            tc_wait_st();
           }
           tc_before();
         }
@@ -694,25 +700,37 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         if (lane == 0) mbar_arrive(bar(sh.p_full));
       }
       // ---- the end of the stretch ----
+      // sums over the tokens: first over the lanes that share a place in the queries' memory (their scores are done)
+      constexpr int kPer = D / 2;  // partial sums of a column that fit there
+      float* const part = reinterpret_cast<float*>(mem + T::oQ);
 #pragma unroll
-      for (int c = 0; c < NH; c += 8) {
-        float v[8];
+      for (int c = 0; c < NH; c += 2) {
+        float a, b;
+        unpack(l2[c / 2], a, b);
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) unpack(l2[(c + j) / 2], v[j], v[j + 1]);
-        const float s = column_sums(v, lane);
-        if (lane < 8) sh.red[wl][c0 + c + lane] = s;
+        for (int o = 16; o >= kPer / 4; o >>= 1) {
+          a += __shfl_xor_sync(kFull, a, o);
+          b += __shfl_xor_sync(kFull, b, o);
+        }
+        if (lane < kPer / 4) {
+          part[(c0 + c) * kPer + wl * (kPer / 4) + lane] = a;
+          part[(c0 + c + 1) * kPer + wl * (kPer / 4) + lane] = b;
+        }
       }
       const bool whole = g.n == g.nt;
       float* slot = whole ? nullptr : slot_of<NR, D>(p, 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0));
       bar_sync(1, kTcSoft);
       if (tid < NR) {
-        const float l = sh.red[0][tid] + sh.red[1][tid] + sh.red[2][tid] + sh.red[3][tid], m = -sh.neg_m[tid];
+        float l = 0.f;
+        const float m = -sh.neg_m[tid];
+#pragma unroll 4
+        for (int i = 0; i < kPer; ++i) l += part[tid * kPer + ((i + tid) & (kPer - 1))];
         const int idx = sh.idx[tid];
         if (!whole) {
           slot[tid] = l == 0.f ? ninf : m;  // a row that saw nothing has no reference
           slot[NR + tid] = l;
         } else if (idx >= 0) {
-          const Coef r = row_coef(p, idx, m, l, g.bad);
+          const Coef r = row_coef(sh.pre[tid], m, l, g.bad);
           sh.coef[tid] = make_float2(r.a, r.b);
           finish_lse(p, idx, r);
         }
@@ -743,20 +761,25 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       } else if (t < D) {
         const bool join = p.pre_o != nullptr;
 #pragma unroll 1
-        for (int c = 0; c < NH; c += 4) {
-          const int4 idx = *reinterpret_cast<const int4*>(&sh.idx[c0 + c]);
-          const int row[4] = {idx.x, idx.y, idx.z, idx.w};
-          float o[4], pre[4];
+        for (int c = 0; c < NH; c += 8) {
+          int row[8];
+          float pre[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) pre[j] = join && row[j] >= 0 ? __ldcg(p.pre_o + (long long)row[j] * D + d) : 0.f;
-          tc_sum_parts<NR>(tO + c, o);
+          for (int j = 0; j < 8; ++j) row[j] = sh.idx[c0 + c + j];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (kHalves == 2) o[j] += half[(c + j) * D + d];
-            const float2 r = sh.coef[c0 + c + j];
-            float y = o[j] * r.x;
-            if (r.y != 0.f) y = fmaf(pre[j], r.y, y);
-            if (row[j] >= 0) store_out<uint16_t, D>(p, row[j], d, y);
+          for (int j = 0; j < 8; ++j) pre[j] = join && row[j] >= 0 ? __ldcg(p.pre_o + (long long)row[j] * D + d) : 0.f;
+#pragma unroll
+          for (int q = 0; q < 8; q += 4) {
+            float o[4];
+            tc_sum_parts<NR>(tO + c + q, o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (kHalves == 2) o[j] += half[(c + q + j) * D + d];
+              const float2 r = sh.coef[c0 + c + q + j];
+              float y = o[j] * r.x;
+              if (r.y != 0.f) y = fmaf(pre[q + j], r.y, y);
+              if (row[q + j] >= 0) store_out<uint16_t, D>(p, row[q + j], d, y);
+            }
           }
         }
       }

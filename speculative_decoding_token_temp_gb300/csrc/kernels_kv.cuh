@@ -25,42 +25,78 @@ __device__ __forceinline__ float exp_value(unsigned byte) {
   return byte == (unsigned)kNanExp ? __int_as_float(0x7fffffff) : __int_as_float((int)byte << 23);
 }
 
-// The smallest e with m <= 448 * 2^e for a finite m > 0, at least SPEC_KV_MIN_EXP. With
+// The smallest e with m <= 448 * 2^e for a finite m > 0 (by its bits), at least SPEC_KV_MIN_EXP. With
 // m = f * 2^k, f in [1, 2): 448 = 1.75 * 2^8, so e = k - 8, one more when f > 1.75. A
 // subnormal m has k below the minimum whatever it is read as.
-__device__ __forceinline__ int vector_exp(float m) {
-  const int b = __float_as_int(m);
+__device__ __forceinline__ int vector_exp(uint32_t bits) {
+  const int b = (int)bits;
   const int e = (b >> 23) - 127 - 8 + ((b & 0x7fffff) > 0x600000 ? 1 : 0);
   return max(e, SPEC_KV_MIN_EXP);
 }
 
-// 8 consecutive elements as floats; VEC: their address is 16-byte aligned.
-template <bool VEC>
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-  uint32_t w[4];
-  if constexpr (VEC) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else {
+// 8 consecutive elements, as they are in memory; VEC: their address is 16-byte aligned.
+template <typename E>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  uint4 w;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    if constexpr (VEC) {
+      w = __ldg(reinterpret_cast<const uint4*>(p));
+    } else {
+      uint32_t x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
+      for (int i = 0; i < 4; ++i) x[i] = (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
+      w = make_uint4(x[0], x[1], x[2], x[3]);
+    }
   }
+  // the largest magnitude among the lanes of a vector, by its bits as fp32's (a NaN or an
+  // infinity is above every finite one)
+  template <int L>
+  __device__ __forceinline__ uint32_t top() const {
+    constexpr uint32_t m = 0x7fff7fffu;
+    uint32_t t = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int o = L / 2; o > 0; o >>= 1) t = __vmaxu2(t, __shfl_xor_sync(kFull, t, o));
+    return max(t & 0xffff0000u, t << 16);
   }
-}
-template <bool VEC>
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  if constexpr (VEC) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(v[i] << 16);
+      x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const float* p) {
+    if constexpr (VEC) {
+      a = __ldg(reinterpret_cast<const float4*>(p));
+      b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    } else {
+      a = make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+      b = make_float4(__ldg(p + 4), __ldg(p + 5), __ldg(p + 6), __ldg(p + 7));
+    }
+  }
+  template <int L>
+  __device__ __forceinline__ uint32_t top() const {
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(kFull, t, o));
+    return t;
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __ldg(p + i);
   }
-}
+};
 
 __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
   uint32_t w[4];
@@ -115,96 +151,126 @@ __device__ __forceinline__ long long kv_place(const KvParams& p, int n, uint32_t
 }
 
 constexpr int kKvThreads = 256;
+// vectors a lane group has on the way at once (64 bytes a lane of the append's source)
+template <typename E>
+constexpr int kKvUnroll = 16 / (int)sizeof(E) / 2;
 
-// Append: vector j of the call is (row, k or v, head) with the head innermost, so that the
-// lanes of a warp read neighbouring heads of one row (contiguous in a projection) and write
-// whole vectors of D codes.
-template <typename E, int D, bool VEC>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(KvParams p) {
-  constexpr int L = D / 8;  // lanes of a vector
+// Both kernels: an item is `heads` heads of the key or the value side of a row (`split`
+// items a side). A warp takes `per` (1..32) items in a row: its lanes look the places up,
+// one item each (three dependent loads, once for all of them), then the warp moves the items
+// one after the other, groups of D / 8 lanes a head each, so that neighbouring heads are
+// read and written side by side.
+struct KvSplit {
+  int per, heads, split;
+};
+__device__ __forceinline__ long long kv_lookup(const KvParams& p, const KvSplit& k, int item, bool wanted, uint32_t* bits) {
+  const int side = item / k.split;
+  return side < p.rows * 2 && wanted ? kv_place(p, side >> 1, bits) : -1;
+}
+
+template <typename E, int D, bool VEC, int U>
+__global__ void __launch_bounds__(kKvThreads, U == 1 ? 6 : 5) kv_append_kernel(KvParams p, KvSplit k) {
+  constexpr int L = D / 8, GRP = 32 / L;  // lanes of a vector, vectors a warp holds at once
   griddep_wait();
-  const int lane = threadIdx.x % L;
-  const long long total = (long long)p.rows * 2 * p.Hk;
-  const long long step = (long long)gridDim.x * (kKvThreads / L);
+  griddep_launch();
+  const int lane = threadIdx.x & 31, sub = lane % L, grp = lane / L;
+  const int items = p.rows * 2 * k.split, first = (blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5)) * k.per;
   uint32_t bits = 0;
-  for (long long j0 = (long long)blockIdx.x * (kKvThreads / L); j0 < total; j0 += step) {
-    const long long j = j0 + threadIdx.x / L;
-    const bool in = j < total;
-    const int h = in ? (int)(j % p.Hk) : 0;
-    const long long r2 = in ? j / p.Hk : 0;
-    const bool is_v = r2 & 1;
-    const int n = (int)(r2 >> 1);
-    const long long at = in ? kv_place(p, n, &bits) : -1;
-    float x[8];
+  const long long mine = lane < k.per ? kv_lookup(p, k, first + lane, true, &bits) : -1;
+  const int n_items = min(k.per, items - first);
+  for (int it = 0; it < n_items; ++it) {
+    const int item = first + it, side = item / k.split, n = side >> 1, from = (item - side * k.split) * k.heads;
+    const int to = min(p.Hk, from + k.heads);
+    const bool is_v = side & 1;
+    long long at = 0;
+    if (U > 1 && (at = __shfl_sync(kFull, mine, it)) < 0) continue;
+    const E* src = static_cast<const E*>(is_v ? p.src_v : p.src_k) + (long long)n * (is_v ? p.v_row : p.k_row) + sub * 8;
+    const long long head = is_v ? p.v_head : p.k_head;
+    for (int h0 = from + grp; h0 - grp < to; h0 += GRP * U) {
+      Raw8<E> raw[U]{};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (at >= 0) {
-      const E* src = static_cast<const E*>(is_v ? p.src_v : p.src_k);
-      load8<VEC>(src + (long long)n * (is_v ? p.v_row : p.k_row) + (long long)h * (is_v ? p.v_head : p.k_head) + lane * 8, x);
+      for (int u = 0; u < U; ++u)
+        if (h0 + u * GRP < to) raw[u].template load<VEC>(src + (h0 + u * GRP) * head);
+      // few rows: the source is on its way before the place is known (a row left out is read for nothing)
+      if (U == 1 && (at = __shfl_sync(kFull, mine, it)) < 0) break;
+      uint8_t* codes = (is_v ? p.v : p.k) + at * D + sub * 8;
+      uint8_t* exps = (is_v ? p.v_exp : p.k_exp) + at;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * GRP;
+        if (h - grp >= to) break;  // (the whole warp)
+        const uint32_t top = raw[u].template top<L>();
+        if (h >= to) continue;
+        const bool bad = top >= 0x7f800000u;
+        const int e = top == 0 ? SPEC_KV_ZERO_EXP : vector_exp(top);
+        const float inv = bad ? 0.f : __int_as_float((kExpBias - e) << 23);  // 2^-e: e in [-100, 120]
+        float x[8];
+        raw[u].floats(x);
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+          w[i] = bad ? 0u : a | b << 16;
+        }
+        const long long vec = (long long)h << p.page_shift;
+        if (!in_idx(at + vec, ((long long)p.num_pages * p.Hk) << p.page_shift, p.status)) continue;
+        *reinterpret_cast<uint2*>(codes + vec * D) = make_uint2(w[0], w[1]);
+        if (sub == 0) exps[vec] = (uint8_t)(bad ? kNanExp : e + kExpBias);
+        if (bad) bits |= SPEC_DEV_NONFINITE;
+      }
     }
-    float m = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m = fmaxf(m, fabsf(x[i]));
-      bad |= !(fabsf(x[i]) <= 3.402823466e38f);
-    }
-    if (bad) m = __int_as_float(0x7f800000);
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    if (at < 0) continue;
-    bad = m == __int_as_float(0x7f800000);
-    const int e = m == 0.f ? SPEC_KV_ZERO_EXP : vector_exp(m);
-    const float inv = __int_as_float((kExpBias - e) << 23);  // 2^-e: e in [-100, 120]
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-      w[i] = bad ? 0u : a | b << 16;
-    }
-    const long long vec = at + ((long long)h << p.page_shift);
-    if (!in_idx(vec, ((long long)p.num_pages * p.Hk) << p.page_shift, p.status)) continue;
-    *reinterpret_cast<uint2*>((is_v ? p.v : p.k) + vec * D + lane * 8) = make_uint2(w[0], w[1]);
-    if (lane == 0) (is_v ? p.v_exp : p.k_exp)[vec] = (uint8_t)(bad ? kNanExp : e + kExpBias);
-    if (bad) bits |= SPEC_DEV_NONFINITE;
   }
   if (bits) atomicOr(p.status, bits);
 }
 
-// Read-back: the same split; a lane reads 8 codes and writes 8 numbers.
-template <typename E, int D>
-__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(KvParams p) {
-  constexpr int L = D / 8;
+template <typename E, int D, int U>
+__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(KvParams p, KvSplit k) {
+  constexpr int L = D / 8, GRP = 32 / L;
   griddep_wait();
-  const int lane = threadIdx.x % L;
-  const long long total = (long long)p.rows * 2 * p.Hk;
-  const long long step = (long long)gridDim.x * (kKvThreads / L);
+  griddep_launch();
+  const int lane = threadIdx.x & 31, sub = lane % L, grp = lane / L;
+  const int items = p.rows * 2 * k.split, first = (blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5)) * k.per;
   uint32_t bits = 0;
-  for (long long j = (long long)blockIdx.x * (kKvThreads / L) + threadIdx.x / L; j < total; j += step) {
-    const int h = (int)(j % p.Hk);
-    const long long r2 = j / p.Hk;
-    const bool is_v = r2 & 1;
-    const int n = (int)(r2 >> 1);
+  const bool wanted = ((first + lane) / k.split & 1 ? p.dst_v : p.dst_k) != nullptr;
+  const long long mine = lane < k.per ? kv_lookup(p, k, first + lane, wanted, &bits) : -1;
+  const int n_items = min(k.per, items - first);
+  for (int it = 0; it < n_items; ++it) {
+    const int item = first + it, side = item / k.split, n = side >> 1, from = (item - side * k.split) * k.heads;
+    const int to = min(p.Hk, from + k.heads);
+    const bool is_v = side & 1;
+    const long long at = __shfl_sync(kFull, mine, it);
     E* dst = static_cast<E*>(is_v ? p.dst_v : p.dst_k);
     if (dst == nullptr) continue;
-    const long long at = kv_place(p, n, &bits);
-    float x[8];
-    if (at >= 0) {
-      const long long vec = at + ((long long)h << p.page_shift);
-      if (!in_idx(vec, ((long long)p.num_pages * p.Hk) << p.page_shift, p.status)) continue;
-      const uint2 w = *reinterpret_cast<const uint2*>((is_v ? p.v : p.k) + vec * D + lane * 8);
-      const float s = exp_value((is_v ? p.v_exp : p.k_exp)[vec]);
-      codes4(w.x, x);
-      codes4(w.y, x + 4);
+    dst += (long long)n * p.Hk * D + sub * 8;
+    const uint8_t* codes = (is_v ? p.v : p.k) + at * D + sub * 8;
+    const uint8_t* exps = (is_v ? p.v_exp : p.k_exp) + at;
+    for (int h0 = from + grp; h0 < to; h0 += GRP * U) {
+      uint2 w[U];
+      float s[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= s;
-    } else {
-      const float fill = at == -1 ? 0.f : __int_as_float(0x7fffffff);
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * GRP;
+        const long long vec = (long long)h << p.page_shift;
+        w[u] = make_uint2(0, 0);
+        s[u] = at == -2 ? __int_as_float(0x7fffffff) : 0.f;
+        if (at >= 0 && h < to && in_idx(at + vec, ((long long)p.num_pages * p.Hk) << p.page_shift, p.status)) {
+          w[u] = *reinterpret_cast<const uint2*>(codes + vec * D);
+          s[u] = exp_value(exps[vec]);
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fill;
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * GRP;
+        if (h >= to) continue;
+        float x[8];
+        codes4(w[u].x, x);
+        codes4(w[u].y, x + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= s[u];
+        store8(dst + (long long)h * D, x);
+      }
     }
-    store8(dst + ((long long)n * p.Hk + h) * D + lane * 8, x);
   }
   if (bits) atomicOr(p.status, bits);
 }
