@@ -49,73 +49,79 @@ struct WideParams {
   int tiles;
 };
 
-// One block a tile and kv head; two threads a token.
+// One block a tile and kv head. Its first 128 threads look the tokens up; then D / 8 lanes
+// take a token, 8 codes and one 16-byte store of each operand a lane.
 template <int D>
 __global__ void __launch_bounds__(256) widen_kernel(AttnParams p, WideParams w) {
-  __shared__ float s_max[8];
+  constexpr int L = D / 8, ROWS = 256 / L, STEPS = kTile / ROWS;
+  __shared__ float s_max[4], s_ks[kTile], s_ev[kTile];
+  __shared__ long long s_vec[kTile];
   griddep_wait();
   griddep_launch();
-  const int tile = blockIdx.x, h = blockIdx.y, u = threadIdx.x >> 1, part = threadIdx.x & 1, t = tile * kTile + u;
+  const int tile = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   const float nan = __int_as_float(0x7fffffff);
-  uint4 kw[D / 32], vw[D / 32];
-  float ks = 0.f, ev = -1e30f;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
-  if (t < p.fixed_len) {
-    const int page = __ldg(p.table + (t >> p.page_shift));
-    if ((unsigned)page < (unsigned)p.num_pages) {
-      const long long vec = (((long long)page * p.Hk + h) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
-      if (in_idx(vec, ((long long)p.num_pages * p.Hk) << p.page_shift, p.status)) {
-        const uint4* sk = reinterpret_cast<const uint4*>(p.k + vec * D + part * (D / 2));
-        const uint4* sv = reinterpret_cast<const uint4*>(p.v + vec * D + part * (D / 2));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) kw[i] = __ldg(sk + i), vw[i] = __ldg(sv + i);
-        const unsigned kb = __ldg(p.k_exp + vec), vb = __ldg(p.v_exp + vec);
-        bad = kb == kNanExp || vb == kNanExp;
-        ks = exp_value(kb);
-        ev = bad ? ev : (float)((int)vb - kExpBias);
+  if (tid < kTile) {
+    const int t = tile * kTile + tid;
+    long long vec = -1;
+    float ks = 0.f, ev = -1e30f;
+    if (t < p.fixed_len) {
+      const int page = __ldg(p.table + (t >> p.page_shift));
+      ks = nan;
+      if ((unsigned)page < (unsigned)p.num_pages) {
+        vec = (((long long)page * p.Hk + h) << p.page_shift) + (t & ((1 << p.page_shift) - 1));
+        if (!in_idx(vec, ((long long)p.num_pages * p.Hk) << p.page_shift, p.status)) vec = -1;
+      } else {
+        atomicOr(p.status, SPEC_DEV_PAGE);
       }
-    } else {
-      bad = true;
-      atomicOr(p.status, SPEC_DEV_PAGE);
+      if (vec >= 0) {
+        const unsigned kb = __ldg(p.k_exp + vec), vb = __ldg(p.v_exp + vec);
+        if (kb != kNanExp && vb != kNanExp) {
+          ks = exp_value(kb);
+          ev = (float)((int)vb - kExpBias);
+        }
+      }
+    }
+    s_vec[tid] = vec;
+    s_ks[tid] = ks;  // NaN: of a token that is not to be read as numbers
+    s_ev[tid] = ev;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ev = fmaxf(ev, __shfl_xor_sync(kFull, ev, o));
+    if ((tid & 31) == 0) s_max[tid >> 5] = ev;
+  }
+  __syncthreads();
+  float e = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  if (e < -200.f) e = 0.f;  // no token with values
+  if (tid == 0) w.exp[(long long)h * w.tiles + tile] = e;
+  const int sub = tid % L, u0 = tid / L;
+  uint2 kw[STEPS], vw[STEPS];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const long long vec = s_vec[u0 + i * ROWS];
+    kw[i] = vw[i] = make_uint2(0, 0);
+    if (vec >= 0) {
+      kw[i] = __ldg(reinterpret_cast<const uint2*>(p.k + vec * D) + sub);
+      vw[i] = __ldg(reinterpret_cast<const uint2*>(p.v + vec * D) + sub);
     }
   }
-  float e = ev;
+  const long long row0 = ((long long)h * w.tiles + tile) * kTile;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) e = fmaxf(e, __shfl_xor_sync(kFull, e, o));
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = e;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) e = fmaxf(e, s_max[i]);
-  if (e < -200.f) e = 0.f;  // no token with values
-  if (threadIdx.x == 0) w.exp[(long long)h * w.tiles + tile] = e;
-  const float vs = ev < -200.f ? 0.f : ex2(ev - e + (float)kValueShift);
-  const long long row = ((long long)h * w.tiles + tile) * kTile + u;
-  uint4* dk = reinterpret_cast<uint4*>(w.k16 + row * D + part * (D / 2));
-  uint4* dv = reinterpret_cast<uint4*>(w.v16 + row * D + part * (D / 2));
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const uint32_t ck[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w}, cv[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
-    uint32_t ok[8], ov[8];
+  for (int i = 0; i < STEPS; ++i) {
+    const int u = u0 + i * ROWS;
+    const float ks = s_ks[u], ev = s_ev[u], vs = ks != ks ? nan : ev < -200.f ? 0.f : ex2(ev - e + (float)kValueShift);
+    float x[8], y[8];
+    codes4(kw[i].x, x);
+    codes4(kw[i].y, x + 4);
+    codes4(vw[i].x, y);
+    codes4(vw[i].y, y + 4);
+    uint32_t ok[4], ov[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float x[4], y[4];
-      codes4(ck[j], x);
-      codes4(cv[j], y);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = bad ? nan : x[k] * ks, y[k] = bad ? nan : y[k] * vs;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-        ok[2 * j + k] = *reinterpret_cast<const uint32_t*>(&b);
-        ov[2 * j + k] = half2_of(y[2 * k], y[2 * k + 1]);
-      }
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j] * ks, x[2 * j + 1] * ks);
+      ok[j] = *reinterpret_cast<const uint32_t*>(&b);
+      ov[j] = half2_of(y[2 * j] * vs, y[2 * j + 1] * vs);
     }
-    dk[2 * i] = make_uint4(ok[0], ok[1], ok[2], ok[3]);
-    dk[2 * i + 1] = make_uint4(ok[4], ok[5], ok[6], ok[7]);
-    dv[2 * i] = make_uint4(ov[0], ov[1], ov[2], ov[3]);
-    dv[2 * i + 1] = make_uint4(ov[4], ov[5], ov[6], ov[7]);
+    *reinterpret_cast<uint4*>(w.k16 + (row0 + u) * D + sub * 8) = make_uint4(ok[0], ok[1], ok[2], ok[3]);
+    *reinterpret_cast<uint4*>(w.v16 + (row0 + u) * D + sub * 8) = make_uint4(ov[0], ov[1], ov[2], ov[3]);
   }
 }
 

@@ -14,8 +14,8 @@
 //            absolute 2^-18 of it);
 //   weights  a weight rounded to f16 (11 bits) is exactly the sum of three parts (each the
 //            rest of the ones before, scaled by 16 and 256 in columns of its own), down to
-//            2^-18, where the largest weights of a row stand between 2^4 and 2^8: what is
-//            dropped of a flat tail is below 2^-22 of the largest weight a token.
+//            2^-18, where the largest weights of a row stand between 2^3 and 2^8: what is
+//            dropped of a flat tail is below 2^-21 of the largest weight a token.
 //
 //   Exponents: a key's is a factor of its token's scores, one lane's constant; a value's is
 //   added to the score before the exponential (weights are 2^(x + e - m)), so that the
@@ -45,7 +45,7 @@ constexpr int kTcThreads = 320;        // eight softmax warps, one for copies, o
 constexpr int kTcSoft = 256;
 constexpr int kSegRing = 8;            // more stretches than tiles can be in the rings
 constexpr int kTcPollLimit = 1 << 18;  // bounded waits (SPEC_DEV_TIMEOUT): about a second
-constexpr float kTop = 4.f;            // a fresh reference puts the largest weight at 2^4 ...
+constexpr float kTop = 3.f;            // a fresh reference puts the largest weight at 2^3 ...
 constexpr float kOver = 8.f;           // ... and is renewed when one would pass 2^8 (e4m3 ends at 448)
 
 template <int D, int NR>
@@ -391,6 +391,13 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         mbar_arrive(bar(sh.seg_full[ns % kSegRing]));
       }
       ++ns;
+      // the stretch's queries on their way to the L2 cache while the ones before are worked on
+      for (int c = lane; c < NR && g.f0 + c < g.rows * p.G; c += 32) {
+        const int f = g.f0 + c, i = f / p.G;
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(g.row0 + i) * p.q_row + (long long)(g.h * p.G + f - i * p.G) * p.q_head;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+        if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+      }
       auto page_of = [&](int tile) -> int {  // of this lane's part of a tile
         const int t = tile * kTile + lane * box;
         return lane < np && t < g.len ? __ldg(g.pages + (t >> p.page_shift)) : -2;
@@ -502,6 +509,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     // ---- softmax: thread = token (lane of S^T) and element (lane of O^T), half of the columns ----
     constexpr int NH = NR / 2;
     const int t = tid & 127, wl = warp & 3, c0 = (warp >> 2) * NH;
+    const int half_bar = 2 + (warp >> 2);  // the columns' halves have references of their own and run on their own
     const uint32_t lanes = (uint32_t)(wl * 32) << 16;
     const uint32_t tS = tmem + lanes + c0, tO = tmem + lanes + T::cO + (kHalves == 2 && wl >= 2 ? T::cHalf : 0) + c0;
     uint8_t* const pw = mem + T::oP + t * 16;
@@ -607,35 +615,43 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh.s_free));
-        if (bar_or(1, kTcSoft, first || most > kOver)) {
+        if (bar_or(half_bar, 128, first || most > kOver)) {
           // new references: the maxima, over the warps' lanes, of the columns that need one
-          const float over = first ? ninf : kOver;
+          uint32_t need = ~0u;
+          if (!first) {
+            need = 0;
 #pragma unroll
-          for (int c = 0; c < NH; c += 8) {
-            float keep = ninf;
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
+            for (int c = 0; c < NH; c += 2) {
               float a, b;
-              unpack(x[(c + j) / 2], a, b);
-              if (__any_sync(kFull, fmaxf(a, b) > over)) {
-                a = warp_max(a);
-                b = warp_max(b);
-                if (lane == j) keep = a;
-                if (lane == j + 1) keep = b;
-              }
+              unpack(x[c / 2], a, b);
+              need |= (a > kOver ? 1u << c : 0u) | (b > kOver ? 2u << c : 0u);
             }
-            if (lane < 8) sh.red[wl][c0 + c + lane] = keep;
+            need = __reduce_or_sync(kFull, need);
           }
-          bar_sync(1, kTcSoft);
-          if (tid < NR) {
+          float keep = ninf;
+#pragma unroll
+          for (int c = 0; c < NH; c += 2) {
+            if (need >> c & 3u) {
+              float a, b;
+              unpack(x[c / 2], a, b);
+              a = warp_max(a);
+              b = warp_max(b);
+              if (lane == c) keep = a;
+              if (lane == c + 1) keep = b;
+            }
+          }
+          if (lane < NH) sh.red[wl][c0 + lane] = keep;
+          bar_sync(half_bar, 128);
+          if (t < NH) {
+            const int c = c0 + t;
             float d = 0.f;
-            const float mx = fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid]));
+            const float mx = fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c]));
             if (mx != ninf && (first || mx > kTop)) d = mx - kTop;
-            sh.delta[tid] = -d;
-sh.factor[tid] = first ? 1.f : ex2(-d);  // (nothing is summed yet: 0 times an infinity is no 0)
-            sh.neg_m[tid] -= d;
+            sh.delta[c] = -d;
+            sh.factor[c] = first ? 1.f : ex2(-d);  // (nothing is summed yet: 0 times an infinity is no 0)
+            sh.neg_m[c] -= d;
           }
-          bar_sync(1, kTcSoft);
+          bar_sync(half_bar, 128);
           if (!first) {
             tc_wait(bar(sh.o_done), (gi - 1) & 1, gave_up, p.status);  // the accumulator holds the earlier tiles
             tc_after();
@@ -700,6 +716,14 @@ sh.factor[tid] = first ? 1.f : ex2(-d);  // (nothing is summed yet: 0 times an i
         if (lane == 0) mbar_arrive(bar(sh.p_full));
       }
       // ---- the end of the stretch ----
+      const bool whole = g.n == g.nt, join = whole && p.pre_o != nullptr && t < D;
+      const int d = t & (D - 1);
+      float pre[NH];  // this element of the prefix's part, on its way while the sums are joined
+#pragma unroll
+      for (int c = 0; c < NH; ++c) {
+        const int idx = sh.idx[c0 + c];
+        pre[c] = join && idx >= 0 ? __ldcg(p.pre_o + (long long)idx * D + d) : 0.f;
+      }
       // sums over the tokens: first over the lanes that share a place in the queries' memory (their scores are done)
       constexpr int kPer = D / 2;  // partial sums of a column that fit there
       float* const part = reinterpret_cast<float*>(mem + T::oQ);
@@ -717,27 +741,29 @@ sh.factor[tid] = first ? 1.f : ex2(-d);  // (nothing is summed yet: 0 times an i
           part[(c0 + c + 1) * kPer + wl * (kPer / 4) + lane] = b;
         }
       }
-      const bool whole = g.n == g.nt;
       float* slot = whole ? nullptr : slot_of<NR, D>(p, 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0));
       bar_sync(1, kTcSoft);
-      if (tid < NR) {
+      if (tid < 4 * NR) {  // (whole warps) four threads a column
+        const int col = tid >> 2;
         float l = 0.f;
-        const float m = -sh.neg_m[tid];
-#pragma unroll 4
-        for (int i = 0; i < kPer; ++i) l += part[tid * kPer + ((i + tid) & (kPer - 1))];
-        const int idx = sh.idx[tid];
-        if (!whole) {
-          slot[tid] = l == 0.f ? ninf : m;  // a row that saw nothing has no reference
-          slot[NR + tid] = l;
+        const float m = -sh.neg_m[col];
+#pragma unroll
+        for (int i = 0; i < kPer / 4; ++i) l += part[col * kPer + ((i + col) * 4 & (kPer - 1)) + (tid & 3)];
+        l += __shfl_xor_sync(kFull, l, 1);
+        l += __shfl_xor_sync(kFull, l, 2);
+        const int idx = sh.idx[col];
+        if ((tid & 3) != 0) {
+        } else if (!whole) {
+          slot[col] = l == 0.f ? ninf : m;  // a row that saw nothing has no reference
+          slot[NR + col] = l;
         } else if (idx >= 0) {
-          const Coef r = row_coef(sh.pre[tid], m, l, g.bad);
-          sh.coef[tid] = make_float2(r.a, r.b);
+          const Coef r = row_coef(sh.pre[col], m, l, g.bad);
+          sh.coef[col] = make_float2(r.a, r.b);
           finish_lse(p, idx, r);
         }
       }
       tc_wait(bar(sh.o_done), (gi - 1) & 1, gave_up, p.status);
       tc_after();
-      const int d = t & (D - 1);
       float* const half = reinterpret_cast<float*>(mem + T::oP) + c0 * D;  // the weights' memory, read by now
       if (kHalves == 2 && t >= D) {
 #pragma unroll 1
@@ -759,27 +785,18 @@ sh.factor[tid] = first ? 1.f : ex2(-d);  // (nothing is summed yet: 0 times an i
           for (int j = 0; j < 4; ++j) slot[j * D] = kHalves == 2 ? o[j] + half[(c + j) * D + d] : o[j];
         }
       } else if (t < D) {
-        const bool join = p.pre_o != nullptr;
-#pragma unroll 1
-        for (int c = 0; c < NH; c += 8) {
-          int row[8];
-          float pre[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) row[j] = sh.idx[c0 + c + j];
+        for (int c = 0; c < NH; c += 4) {
+          float o[4];
+          tc_sum_parts<NR>(tO + c, o);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) pre[j] = join && row[j] >= 0 ? __ldcg(p.pre_o + (long long)row[j] * D + d) : 0.f;
-#pragma unroll
-          for (int q = 0; q < 8; q += 4) {
-            float o[4];
-            tc_sum_parts<NR>(tO + c + q, o);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (kHalves == 2) o[j] += half[(c + q + j) * D + d];
-              const float2 r = sh.coef[c0 + c + q + j];
-              float y = o[j] * r.x;
-              if (r.y != 0.f) y = fmaf(pre[q + j], r.y, y);
-              if (row[q + j] >= 0) store_out<uint16_t, D>(p, row[q + j], d, y);
-            }
+          for (int j = 0; j < 4; ++j) {
+            const int idx = sh.idx[c0 + c + j];
+            if (kHalves == 2) o[j] += half[(c + j) * D + d];
+            const float2 r = sh.coef[c0 + c + j];
+            float y = o[j] * r.x;
+            if (r.y != 0.f) y = fmaf(pre[c + j], r.y, y);
+            if (idx >= 0) store_out<uint16_t, D>(p, idx, d, y);
           }
         }
       }
