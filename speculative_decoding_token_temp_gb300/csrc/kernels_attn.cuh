@@ -38,6 +38,7 @@ struct AttnParams {
   const int32_t* kv_len;  // null: every sequence has fixed_len tokens
   int fixed_len;
   int mask;
+  int late_wait;            // the pass over the sequences' own tokens behind a prefix pass: see attn_tc_kernel
   int seg_cost;             // tiles that a segment's beginning and end count for
   float c;                  // scale * log2(e)
   float* part;              // the parts of cut segments: two slots a block
@@ -317,8 +318,8 @@ constexpr int kMergeThreads = 256;
 
 template <typename E, int D, int NR>
 __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(AttnParams p, int grid) {
+  griddep_launch();  // (before the wait: the pass over the sequences' own tokens may begin beside the prefix pass)
   griddep_wait();
-  griddep_launch();
   const CutRec r = p.cut[blockIdx.x];
   const int i = blockIdx.x, lane = threadIdx.x & 31, c = blockIdx.y * 8 + (threadIdx.x >> 5), f = r.f0 + c;
   if (r.parts == 0 || c >= NR || f >= r.rows * p.G) return;

@@ -13,9 +13,9 @@
 //   weights f16 (11 bits), kept in tensor memory where the scores were.
 //
 // A block holds 256 rows as two tiles of 128 and walks the keys in tiles of 128 tokens:
-// S = Q K^T and O += P V, lanes = rows. A thread of the two softmax groups has a row, so
-// maxima and sums need no other lane; the reference is renewed when a row's largest score
-// passes it by 2^15. While one group makes weights, the tensor pipe sums the other's
+// S = Q K^T and O += P V, lanes = rows. Two threads share a row, half of a tile's tokens
+// each, so maxima and sums need one other thread, and that only when the reference is
+// renewed (a row's largest score passes it by 2^15). While one group makes weights, the tensor pipe sums the other's
 // values and then computes its next scores: MMAs of one block run in the order they are
 // issued, so a group's next scores may overwrite its weights without a wait.
 #pragma once
@@ -25,7 +25,8 @@
 namespace sv {
 
 constexpr int kRowsP = 256;         // rows of a block
-constexpr int kPreThreads = 320;    // two softmax groups, one warp for copies, one for MMAs
+constexpr int kPreThreads = 576;    // two softmax groups of eight warps, one warp for copies, one for MMAs
+constexpr int kPreSoft = 512;
 constexpr float kTopP = 8.f;        // a fresh reference puts a row's largest weight at 2^8 ...
 constexpr float kOverP = 15.f;      // ... and is renewed when one would pass 2^15
 constexpr int kValueShift = 6;      // the largest value of a tile comes to at most 448 * 2^6
@@ -171,6 +172,7 @@ struct PreShared {
   uint64_t q_full, drained, s_full[2], p_full[2], o_done[2];
   uint32_t tmem;
   int gave_up;
+  float top[2][2][128];  // of the halves of a row: the largest score, then the sum
 };
 
 template <int D>
@@ -195,17 +197,17 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       mbar_init(bar(sh.v_full[i]), 1);
       mbar_init(bar(sh.v_free[i]), 1);
     }
-    mbar_init(bar(sh.q_full), 256);
+    mbar_init(bar(sh.q_full), kPreSoft);
     mbar_init(bar(sh.drained), 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(sh.s_full[w]), 1);
-      mbar_init(bar(sh.p_full[w]), 4);
+      mbar_init(bar(sh.p_full[w]), 8);
       mbar_init(bar(sh.o_done[w]), 1);
     }
     sh.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) {
+  if (warp == 17) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      (uint32_t)__cvta_generic_to_shared(&sh.tmem))
                  : "memory");
@@ -221,7 +223,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   Place at = sh.loc.at;
   int left = end - begin;
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ---- the rings of tiles ----
     if (lane == 0) {
       asm volatile("fence.proxy.async.global;" ::: "memory");  // the widened prefix was written with ordinary stores
@@ -250,7 +252,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ---- the MMAs: of one group the values' sum of a tile and the next scores, then of the other ----
     constexpr uint32_t id_s = 1u << 4 | 1u << 7 | 1u << 10 | (128u >> 3) << 17 | 8u << 24;  // bf16 x bf16, K-major
     constexpr uint32_t id_o = 1u << 4 | 1u << 16 | (uint32_t)(D >> 3) << 17 | 8u << 24;      // f16 x f16, values token by token
@@ -317,8 +319,9 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     for (int it = 0; it < kTcPollLimit && !mbar_try_wait(bar(sh.drained), 0); ++it) {
     }
   } else {
-    // ---- softmax: group w, thread = row ----
-    const int w = warp >> 2, c = tid, t = tid & 127;
+    // ---- softmax: group w, a row and half of a tile's tokens a thread ----
+    const int w = warp >> 3, half = (warp >> 2) & 1, t = tid & 127, c = w * 128 + t;
+    const int pair_bar = 1 + w * 4 + (warp & 3);  // the two warps that share 32 rows
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + T::cS + w * 128, tO = tmem + lanes + T::cO + w * 128;
     const float nan = __int_as_float(0x7fffffff), ninf = __int_as_float(kNegInfBits);
@@ -329,7 +332,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       if (g.n == 0) continue;
       if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, end, total);
       const int flat = g.rows * p.G, f = g.f0 + c;
-      // this thread's query row into shared memory, swizzled
+      // half of this thread's query row into shared memory, swizzled
       bool bad = false;
       {
         uint8_t* const q = mem + T::oQ + w * 128 * D * 2;
@@ -337,7 +340,8 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
                               (long long)(g.h * p.G + f % p.G) * p.q_head;
         const bool vec = ((uintptr_t)src & 15) == 0;
 #pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch) {
+        for (int i8 = 0; i8 < D / 16; ++i8) {
+          const int ch = half * (D / 16) + i8;
           uint32_t x[4] = {0, 0, 0, 0};
           if (f < flat) {
             if (vec) {
@@ -360,33 +364,38 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       float m = 0.f, l = 0.f;
       if (have) {
         for (int k = 0; k < g.n; ++k, ++tiles_done) {
-          const int tile = g.t0 + k, valid = g.len - tile * kTile;
+          const int tile = g.t0 + k, valid = g.len - tile * kTile - half * 64;
           const float E = __ldcg(wide.exp + (long long)g.h * wide.tiles + tile);
           tc_wait(bar(sh.s_full[w]), tiles_done & 1, gave_up, p.status);
           tc_after();
-          float s[128];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tc_ld32(tS + i * 32, s + i * 32);
+          float s[64];
+          tc_ld32(tS + half * 64, s);
+          tc_ld32(tS + half * 64 + 32, s + 32);
           tc_wait_ld();
-          if (valid < kTile) {
+          if (valid < 64) {
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
+            for (int i = 0; i < 64; ++i)
               if (i >= valid) s[i] = ninf;
           }
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 4; i < 128; i += 4)
+          for (int i = 4; i < 64; i += 4)
 #pragma unroll
             for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[i + j]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), x = fmaf(top, p.c, E - m);
-          const bool renew = top != ninf && (k == 0 || x > kOverP);
-          if (__any_sync(kFull, renew)) {
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // (the barrier also stands between both halves' loads and the weights that overwrite scores)
+          if (bar_or(pair_bar, 64, k == 0 || fmaf(top, p.c, E - m) > kOverP)) {
+            sh.top[w][half][t] = top;
+            bar_sync(pair_bar, 64);
+            top = fmaxf(top, sh.top[w][half ^ 1][t]);
+            const float x = fmaf(top, p.c, E - m);
+            const bool renew = top != ninf && (k == 0 || x > kOverP);
             const float d = renew ? x - kTopP : 0.f, fac = ex2(-d);
             m += d;
             if (k > 0) {  // the tiles before are summed: the scores' barrier stands behind their MMAs
               l *= fac;
 #pragma unroll 1
-              for (int i = 0; i < D; i += 16) {
+              for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 16) {
                 uint32_t o[16];
                 tc_ld8(tO + i, *reinterpret_cast<uint32_t(*)[8]>(o));
                 tc_ld8(tO + i + 8, *reinterpret_cast<uint32_t(*)[8]>(o + 8));
@@ -400,7 +409,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           const float off = E - m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 128; i += 32) {
+          for (int i = 0; i < 64; i += 32) {
             uint32_t h[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
@@ -408,7 +417,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
               sum[(j >> 1) & 3] += a + b;
               h[j / 2] = half2_of(a, b);
             }
-            tc_st16(tS + i / 2, h);
+            tc_st16(tS + half * 32 + i / 2, h);
           }
           tc_wait_st();
           tc_before();
@@ -417,25 +426,31 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * ex2(-E);
         }
         // ---- the end of the stretch ----
+        if (bad) l = nan;
+        bar_sync(pair_bar, 64);  // the last maxima are read
+        sh.top[w][half][t] = l;
+        bar_sync(pair_bar, 64);
+        l += sh.top[w][half ^ 1][t];
         tc_wait(bar(sh.o_done[w]), ends & 1, gave_up, p.status);
         ++ends;
         tc_after();
-        if (bad) l = nan;
         const bool whole = g.n == g.nt;
         float* slot = whole ? nullptr : slot_of<NR, D>(p, 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0));
         const long long idx = (long long)(f / p.G) * p.Hq + g.h * p.G + f % p.G;
         Coef r{};
         if (!whole) {
-          slot[c] = m;
-          slot[NR + c] = l;
+          if (half == 0) {
+            slot[c] = m;
+            slot[NR + c] = l;
+          }
         } else if (f < flat) {
           r = row_coef(ninf, m, l, false);
-          finish_lse(p, idx, r);
+          if (half == 0) finish_lse(p, idx, r);
         }
         float* dst = whole ? p.dst_o + idx * D : slot + 2 * NR + c * D;
         const float scale = (whole ? r.a : 1.f) * (1.f / (1 << kValueShift));
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
+        for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
           float o[32];
           tc_ld32(tO + i, o);
           tc_wait_ld();
@@ -447,12 +462,12 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
         tc_before();
       }
-      bar_sync(1, 256);  // both groups are done with the queries' memory
+      bar_sync(9, kPreSoft);  // both groups are done with the queries' memory
     }
   }
   tc_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }

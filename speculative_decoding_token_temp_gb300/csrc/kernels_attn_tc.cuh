@@ -243,7 +243,6 @@ struct TcShared {
   alignas(16) float delta[NR];      // its last change, and 2^that
   alignas(16) float factor[NR];
   float red[4][NR];                 // of the warps of a token each: maxima of the columns
-  float pre[NR];                    // log-sum of the prefix's part
   float2 coef[NR];                  // weights of a row's values and of the prefix's part
   alignas(16) int idx[NR];          // row * query heads + head, -1 past the last
 };
@@ -261,8 +260,6 @@ __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g,
     const bool here = f < g.rows * p.G;
     const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(g.row0 + i) * p.q_row + (long long)hq * p.q_head + part * E;
     const bool vec = ((uintptr_t)src & 15) == 0;
-    float pre = __int_as_float(kNegInfBits);
-    if (part == 0 && here && p.pre_o != nullptr) pre = __ldcg(p.pre_lse + idx);
     uint4 x[E / 8];
 #pragma unroll
     for (int k = 0; k < E / 8; ++k) x[k] = make_uint4(0, 0, 0, 0);
@@ -293,7 +290,6 @@ __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g,
       sh.rq[c] = bad ? __int_as_float(0x7fffffff) : p.c * __int_as_float((e + 127) << 23);
       sh.row[c] = i;
       sh.idx[c] = here ? idx : -1;
-      sh.pre[c] = pre;
       sh.neg_m[c] = 0.f;
     }
     const int rl = NR + c;
@@ -361,13 +357,17 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_before();
   }
-  griddep_wait();
+  // Behind a prefix pass this one needs what that left only where rows are joined. It may begin
+  // once the kernel before it has begun, and that one only after the prefix pass had waited for
+  // everything before the call; so the wait for the prefix's part comes before the first join.
+  if (!p.late_wait) griddep_wait();
   griddep_launch();
   int begin, end, total;
   const bool ok = locate<NR, kTcThreads>(p, sh.loc, blockIdx.x, gridDim.x, &begin, &end, &total);
   tc_after();
   const uint32_t tmem = sh.tmem;
   if (!ok) {
+    if (p.late_wait) griddep_wait();
     fill_nan<uint16_t, D>(p, blockIdx.x, gridDim.x);
     begin = end = 0;
   }
@@ -718,6 +718,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       // ---- the end of the stretch ----
       const bool whole = g.n == g.nt, join = whole && p.pre_o != nullptr && t < D;
       const int d = t & (D - 1);
+      if (p.late_wait) griddep_wait();
       float pre[NH];  // this element of the prefix's part, on its way while the sums are joined
 #pragma unroll
       for (int c = 0; c < NH; ++c) {
@@ -744,20 +745,20 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       float* slot = whole ? nullptr : slot_of<NR, D>(p, 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0));
       bar_sync(1, kTcSoft);
       if (tid < 4 * NR) {  // (whole warps) four threads a column
-        const int col = tid >> 2;
+        const int col = tid >> 2, idx = sh.idx[col];
+        const float lse = whole && idx >= 0 && p.pre_o != nullptr ? __ldcg(p.pre_lse + idx) : ninf;
         float l = 0.f;
         const float m = -sh.neg_m[col];
 #pragma unroll
         for (int i = 0; i < kPer / 4; ++i) l += part[col * kPer + ((i + col) * 4 & (kPer - 1)) + (tid & 3)];
         l += __shfl_xor_sync(kFull, l, 1);
         l += __shfl_xor_sync(kFull, l, 2);
-        const int idx = sh.idx[col];
         if ((tid & 3) != 0) {
         } else if (!whole) {
           slot[col] = l == 0.f ? ninf : m;  // a row that saw nothing has no reference
           slot[NR + col] = l;
         } else if (idx >= 0) {
-          const Coef r = row_coef(sh.pre[col], m, l, g.bad);
+          const Coef r = row_coef(lse, m, l, g.bad);
           sh.coef[col] = make_float2(r.a, r.b);
           finish_lse(p, idx, r);
         }
@@ -804,6 +805,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       bar_sync(1, kTcSoft);
     }
   }
+  if (p.late_wait) griddep_wait();  // (also of a block that joined nothing: no kernel of a call ends before the ones in front of it)
   tc_before();
   __syncthreads();
   if (warp == 9) {

@@ -151,8 +151,12 @@ constexpr int kMaxGridS = 1024;  // largest grid of the 32-bit kernel (its works
 constexpr int kSegCostT = 4, kSegCostS = 1, kSegCostP = 2;
 constexpr long long kMaxLine = 1LL << 30;  // a line of tiles is counted in ints
 constexpr int kMaxGridP = 160;   // of attn_prefix_kernel (one block an SM)
-// rows that share the prefix's keys from which on it is widened and computed in 128-row tiles
-constexpr int kWideRows = 96;
+// The prefix is widened and computed in 128-row tiles where that pays for the widening: from
+// this many row-tiles of keys on (rows that share keys x tiles x kv heads). Below, the 48- or
+// 32-row blocks of attn_tc_kernel do it: head_dim 128, 8 kv heads, 288 rows x 2000 tokens 36 us
+// against 44, 576 x 8192 even, 9216 x 16384 1.5 ms against 0.57; head_dim 64, 576 rows: 2000
+// tokens even, 8192 tokens 66 us against 49.
+constexpr long long kWideWork128 = 300000, kWideWork64 = 75000;
 constexpr int kMaxGridT = 512;   // of the tensor-core kernel (two blocks an SM)
 
 struct AttnLayout {
@@ -162,7 +166,7 @@ struct AttnLayout {
   long long line;      // the longer pass's line of tiles, at most
   bool wide;           // the prefix widened and computed by attn_prefix_kernel
   long long tiles;     // of the prefix
-  size_t part, cut, pre_o, pre_lse, k16, v16, exp, total;
+  size_t part, cut, pre_part, pre_cut, pre_o, pre_lse, k16, v16, exp, total;
 };
 
 long long rows_of(const spec_attn_batch& g) { return (long long)g.total_draft + g.B; }
@@ -183,8 +187,8 @@ AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dt
   const long long cap = tc ? kMaxGridT : kMaxGridS;
   L.nr = tc ? tc_rows((long long)(g.gamma + 1) * G, c.head_dim) : kRowsS;
   const long long flat = rows_of(g) * G;
-  L.wide = tc && g.prefix_len > 0 && flat >= kWideRows;
   L.tiles = cdiv(g.prefix_len, kTile);
+  L.wide = tc && flat >= 128 && flat * L.tiles * c.kv_heads >= (c.head_dim == 64 ? kWideWork64 : kWideWork128);
   L.pre_nr = L.wide ? kRowsP : tc && flat > 0 ? tc_rows(flat, c.head_dim) : kRowsS;
   const long long most_tiles = cdiv((long long)g.pages_per_seq * c.page_size, kTile);
   const long long nt = most_tiles > 1 ? most_tiles : 1;
@@ -195,12 +199,16 @@ AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dt
   L.grid = own < cap ? own : cap;
   const long long pre_cap = L.wide ? kMaxGridP : cap;
   L.pre_grid = pre < pre_cap ? pre : pre_cap;
-  const long long slot_rows = L.grid * L.nr > L.pre_grid * L.pre_nr ? L.grid * L.nr : L.pre_grid * L.pre_nr;
+  // each pass has parts and records of its own: the second may begin before the first has ended
   size_t off = 0;
   L.part = off;
-  off = up256(off + sizeof(float) * (size_t)(2 * slot_rows) * (c.head_dim + 2));
+  off = up256(off + sizeof(float) * (size_t)(2 * L.grid * L.nr) * (c.head_dim + 2));
   L.cut = off;
-  off = up256(off + sizeof(CutRec) * (size_t)(L.grid > L.pre_grid ? L.grid : L.pre_grid));
+  off = up256(off + sizeof(CutRec) * (size_t)L.grid);
+  L.pre_part = off;
+  off = up256(off + sizeof(float) * (size_t)(2 * L.pre_grid * L.pre_nr) * (c.head_dim + 2));
+  L.pre_cut = off;
+  off = up256(off + sizeof(CutRec) * (size_t)L.pre_grid);
   L.pre_o = off;
   if (g.prefix_len > 0) off = up256(off + sizeof(float) * (size_t)rows_of(g) * g.q_heads * c.head_dim);
   L.pre_lse = off;
@@ -285,6 +293,7 @@ AttnParams prefix_params(const AttnParams& own, const spec_attn_batch& g, const 
   p.kv_len = nullptr;
   p.fixed_len = g.prefix_len;
   p.mask = A_ALL;
+  p.late_wait = 0;
   p.dst_o = pre_o;
   p.dst_lse = pre_lse;
   return p;
@@ -531,6 +540,8 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
     float* pre_o = reinterpret_cast<float*>(ws + L.pre_o);
     float* pre_lse = reinterpret_cast<float*>(ws + L.pre_lse);
     AttnParams pp = prefix_params(p, g, c, pre_o, pre_lse);
+    pp.part = reinterpret_cast<float*>(ws + L.pre_part);
+    pp.cut = reinterpret_cast<CutRec*>(ws + L.pre_cut);
     if (L.wide) pp.seg_cost = kSegCostP;
     if (L.wide)
       err = c.head_dim == 64 ? pass_prefix<64>(pp, c, L, ws, s) : pass_prefix<128>(pp, c, L, ws, s);
@@ -539,6 +550,7 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
     if (err != cudaSuccess) return SPEC_ERR_CUDA;
     p.pre_o = pre_o;
     p.pre_lse = pre_lse;
+    p.late_wait = 1;
   }
   err = attn_pass(dtype, c.head_dim, L.nr, p, L.grid, maps, s);
   return err == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;

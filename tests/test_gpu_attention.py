@@ -390,3 +390,64 @@ def test_argument_checks(dev):
         api.spec_attention(q, cache, tb, n, gamma=1, workspace=torch.empty(16, dtype=torch.uint8, device=dev))
     with pytest.raises(ValueError):
         api.spec_attention(q, cache, tb, n, gamma=1, out={"o": torch.empty(1, dtype=c.dtype, device=dev)})
+
+
+# rows that share keys x tiles of the prefix x kv heads decide how the prefix is computed (in 128-row tiles of the widened
+# prefix from 300000 on with head_dim 128, 75000 with 64); the cases below stand on both sides, with one and two row tiles
+@pytest.mark.parametrize("dim,heads,kv_heads,batch,rows,prefix", [
+    (64, 64, 1, 2, 1, 76_000), (64, 64, 1, 2, 9, 9001), (64, 64, 1, 4, 5, 7700), (64, 8, 8, 17, 8, 8913),
+    (128, 64, 1, 2, 17, 17_700), (128, 64, 2, 33, 1, 18_200), (128, 8, 8, 32, 9, 16_777), (128, 5, 5, 60, 10, 13_000)])
+def test_long_prefix_for_many_rows(dev, dim, heads, kv_heads, batch, rows, prefix):
+    c = Case(dev, [rows + 3] * batch, [rows] * batch, heads=heads, kv_heads=kv_heads, dim=dim, page=256, prefix=prefix, size=0.7)
+    flat, tiles = batch * rows * heads // kv_heads, -(-prefix // 128)
+    assert flat >= 128 and flat * tiles * kv_heads >= (75_000 if dim == 64 else 300_000)
+    out = c.call()
+    assert int(out["device_status"][0]) == 0
+    # the first, a middle and the last rows of some heads (the whole restatement would take minutes)
+    pick = sorted({0, 1, batch * rows // 2, 127 % (batch * rows), 128 % (batch * rows), batch * rows - 1})
+    o, lse, spread, dx = sampled(c, pick)
+    bo, bl = U.bounds(o, spread, dx, c.dtype, prefix + rows + 3)
+    got = out["o"].double().cpu().numpy()[pick]
+    assert (np.abs(got - o) <= bo).all(), (np.abs(got - o) / bo).max()
+    d = np.abs(out["lse"].double().cpu().numpy()[pick] - lse)
+    assert (d <= bl + 2.0 ** -23 * np.abs(lse)).all()
+
+
+def sampled(c, pick):
+    """U.attention for some rows of a case of equally long rounds."""
+    T, keep = c.rows[0], (c.lens, c.rows, c.table, c.q)
+    parts = []
+    for r in pick:
+        b, i = divmod(r, T)
+        # row i of the round alone: what it sees are the first lens - T + i + 1 tokens
+        parts.append(U.attention(keep[3][r:r + 1].double().numpy(), c.cache(), keep[2][b:b + 1], [keep[0][b] - T + i + 1], [1],
+                                 prefix_table=c.prefix_table, prefix_len=c.prefix))
+    return [np.concatenate(x, axis=1 if k == 3 else 0) for k, x in enumerate(zip(*parts))]
+
+
+def test_long_prefix_with_bad_rows_pages_and_values_of_every_size(dev):
+    """The widened prefix: a NaN query row, queries off the 16-byte grid, tokens of zero value, exponents that differ much
+    within a tile, a NaN token, a page outside the cache."""
+    c = Case(dev, [4] * 32, [4] * 32, heads=16, kv_heads=1, dim=64, page=128, prefix=128 * 40 + 5, size=0.7)
+    rng = np.random.default_rng(3)
+    c.exps[1][c.prefix_table[3]] = rng.integers(127 - 20, 127, c.exps[1][c.prefix_table[3]].shape)
+    c.exps[1][c.prefix_table[4], 0, ::2] = 127 + U.ZERO_EXP
+    c.codes[1][c.prefix_table[4], 0, ::2] = 0
+    c.q[5, 3, 7] = math.nan
+    wide = torch.empty(32 * 4 * 16 * 65 + 1, dtype=c.dtype, device=dev)[1:].view(32 * 4, 16, 65)[:, :, :64]
+    wide.copy_(c.q)
+    out = c.call(q=wide)
+    pick = [0, 5, 6, 127]
+    ref = sampled(c, pick)
+    bo, _ = U.bounds(np.nan_to_num(ref[0]), ref[2], ref[3], c.dtype, c.prefix)
+    got = out["o"].double().cpu().numpy()
+    assert np.array_equal(np.isnan(got[pick]), np.isnan(ref[0])) and np.isnan(got[5, 3]).all() and np.isnan(got).sum() == 64
+    ok = ~np.isnan(ref[0])
+    assert (np.abs(got[pick] - ref[0])[ok] <= bo[ok]).all()
+    keep = c.prefix_table.copy()
+    c.prefix_table[7] = -1
+    out = c.call()
+    assert int(out["device_status"][0]) == _lib.SPEC_DEV_PAGE and torch.isnan(out["o"]).all()
+    c.prefix_table[7] = keep[7]
+    c.cache().k_exp[int(c.prefix_table[9]), 0, 11] = 255
+    assert torch.isnan(c.call()["o"]).all()
