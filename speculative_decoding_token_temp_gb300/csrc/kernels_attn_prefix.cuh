@@ -407,14 +407,18 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             }
           }
           const float off = E - m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const f2 c2 = pack(p.c, p.c), off2 = pack(off, off);
+          f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
           for (int i = 0; i < 64; i += 32) {
             uint32_t h[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-              const float a = ex2(fmaf(s[i + j], p.c, off)), b = ex2(fmaf(s[i + j + 1], p.c, off));
-              sum[(j >> 1) & 3] += a + b;
+              float a, b;
+              unpack(fma2(pack(s[i + j], s[i + j + 1]), c2, off2), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              sum[(j >> 1) & 3] = add2(sum[(j >> 1) & 3], pack(a, b));
               h[j / 2] = half2_of(a, b);
             }
             tc_st16(tS + half * 32 + i / 2, h);
@@ -423,7 +427,9 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           tc_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(sh.p_full[w]));
-          l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * ex2(-E);
+          float a, b;
+          unpack(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+          l += (a + b) * ex2(-E);
         }
         // ---- the end of the stretch ----
         if (bad) l = nan;
