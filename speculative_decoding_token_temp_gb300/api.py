@@ -465,11 +465,21 @@ def spec_verify_multi(target: torch.Tensor, draft: torch.Tensor, draft_tokens: t
 # the 8-bit key/value cache and the attention over it (include/spec_kv.h)
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_I32, _U8, _E4M3 = torch.int32, torch.uint8, torch.float8_e4m3fn
+_KV_DTYPES = {torch.bfloat16: _lib.SPEC_BF16, torch.float32: _lib.SPEC_F32}
+
+# The calls below may be a few microseconds of GPU work, so their checks are written for the
+# host's time: one look at a tensor's type, device and layout, and _need for what to say when
+# it is not as it should be.
 
 
-def _stream_handle(device) -> int:
+def _stream_handle(index: int) -> int:
     """The current stream's handle, without the Stream object where torch gives it directly (2 us a call)."""
-    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _is(t, dtype, index) -> bool:
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
 
 
 class KVCache:
@@ -479,70 +489,88 @@ class KVCache:
     descriptor that the calls take; `KVCache.empty` allocates them. Pages need no
     initialisation: places that nothing was appended to are never looked at."""
 
-    __slots__ = ("k", "v", "k_exp", "v_exp", "num_pages", "kv_heads", "page_size", "head_dim", "device", "desc")
+    __slots__ = ("k", "v", "k_exp", "v_exp", "num_pages", "kv_heads", "page_size", "head_dim", "index", "desc")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor):
-        _need(k, "k", torch.float8_e4m3fn)
-        if k.dim() != 4:
-            raise ValueError(f"k must be [num_pages, kv_heads, page_size, head_dim], got {tuple(k.shape)}")
-        dev = k.device
-        _need(v, "v", torch.float8_e4m3fn, k.numel(), dev)
-        P, H, S, D = k.shape
-        _need(k_exp, "k_exp", torch.uint8, P * H * S, dev)
-        _need(v_exp, "v_exp", torch.uint8, P * H * S, dev)
+        index = k.get_device() if isinstance(k, torch.Tensor) else -1
+        shape = k.shape if isinstance(k, torch.Tensor) else ()
+        if not (index >= 0 and len(shape) == 4 and _is(k, _E4M3, index) and _is(v, _E4M3, index) and v.shape == shape
+                and _is(k_exp, _U8, index) and _is(v_exp, _U8, index) and k_exp.shape == v_exp.shape == shape[:3]):
+            _need(k, "k", _E4M3)
+            if k.dim() != 4:
+                raise ValueError(f"k must be [num_pages, kv_heads, page_size, head_dim], got {tuple(k.shape)}")
+            _need(v, "v", _E4M3, device=k.device)
+            _need(k_exp, "k_exp", _U8, device=k.device)
+            _need(v_exp, "v_exp", _U8, device=k.device)
+            raise ValueError(f"v must be {tuple(shape)}, k_exp and v_exp {tuple(shape[:3])}; "
+                             f"got {tuple(v.shape)}, {tuple(k_exp.shape)}, {tuple(v_exp.shape)}")
+        P, H, S, D = shape
         if S not in (16, 32, 64, 128, 256):
             raise ValueError(f"page_size must be 16, 32, 64, 128 or 256, got {S}")
-        if D not in (64, 128):
+        if D != 128 and D != 64:
             raise ValueError(f"head_dim must be 64 or 128, got {D}")
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
-        self.num_pages, self.kv_heads, self.page_size, self.head_dim, self.device = P, H, S, D, dev
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim, self.index = P, H, S, D, index
         self.desc = _lib.SpecKvCache(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), P, S, H, D)
+
+    @property
+    def device(self) -> torch.device:
+        return self.k.device
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, device) -> "KVCache":
         shape = (int(num_pages), int(kv_heads), int(page_size))
-        k, v = (torch.empty(*shape, int(head_dim), dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
-        k_exp, v_exp = (torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2))
+        k, v = (torch.empty(*shape, int(head_dim), dtype=_E4M3, device=device) for _ in range(2))
+        k_exp, v_exp = (torch.empty(shape, dtype=_U8, device=device) for _ in range(2))
         return cls(k, v, k_exp, v_exp)
 
 
-def _status_word(o: dict, device_status, dev) -> torch.Tensor:
+def _status_word(o: dict, device_status, cache) -> int:
+    """The address of the call's status word (in o, made when there is none)."""
     if device_status is None:
-        device_status = _out(o, "device_status", lambda: torch.zeros(1, dtype=torch.int32, device=dev))
+        device_status = o.get("device_status")
+        if device_status is None:
+            device_status = o["device_status"] = torch.zeros(1, dtype=_I32, device=cache.k.device)
+            return device_status.data_ptr()
     else:
-        _need(device_status, "device_status", torch.int32, 1, dev)
         o["device_status"] = device_status
-    return device_status
+    if not _is(device_status, _I32, cache.index) or device_status.numel() != 1:
+        _need(device_status, "device_status", _I32, 1, cache.k.device)
+    return device_status.data_ptr()
 
 
-def _strides(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dev):
-    """(row, head) strides of a [rows, heads, dim] view whose vectors are contiguous; the
-    view may be a slice of a wider buffer."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}, got {t.device}")
-    if t.dim() == 4 and t.shape[0] * t.shape[1] == rows:
-        if t.shape[0] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
+def _rows_view(t: torch.Tensor, name: str, rows: int, heads: int, cache: KVCache):
+    """(address, row stride, head stride) of a [rows, heads, head_dim] view whose vectors are
+    contiguous; the view may be a slice of a wider buffer."""
+    shape = t.shape
+    if t.get_device() != cache.index:
+        raise ValueError(f"{name} must be a CUDA tensor on {cache.k.device}, got {t.device}")
+    if len(shape) == 4 and shape[0] * shape[1] == rows:
+        if shape[0] > 1 and t.stride(0) != shape[1] * t.stride(1):
             raise ValueError(f"{name}: the rows of a [B, rows, heads, dim] view must be evenly spaced")
         t = t.flatten(0, 1)
-    if t.dim() != 3 or tuple(t.shape) != (rows, heads, dim):
-        raise ValueError(f"{name} must be [{rows}, {heads}, {dim}], got {tuple(t.shape)}")
-    if t.stride(2) != 1:
+        shape = t.shape
+    if shape != (rows, heads, cache.head_dim):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {cache.head_dim}], got {tuple(shape)}")
+    row, head, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return t.stride(0), t.stride(1)
+    return t.data_ptr(), row, head
 
 
 def _kv_rows(cache: KVCache, page_table, row_seq, row_pos) -> _lib.SpecKvRows:
-    dev = cache.device
-    _need(page_table, "page_table", torch.int32, device=dev)
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table must be [sequences, pages], got {tuple(page_table.shape)}")
-    n = row_seq.numel()
-    _need(row_seq, "row_seq", torch.int32, device=dev)
-    _need(row_pos, "row_pos", torch.int32, n, dev)
-    return _lib.SpecKvRows(n, page_table.shape[0], page_table.shape[1], page_table.data_ptr(), row_seq.data_ptr(),
-                           row_pos.data_ptr())
+    index = cache.index
+    if not (_is(page_table, _I32, index) and _is(row_seq, _I32, index) and _is(row_pos, _I32, index)):
+        dev = cache.k.device
+        _need(page_table, "page_table", _I32, device=dev)
+        _need(row_seq, "row_seq", _I32, device=dev)
+        _need(row_pos, "row_pos", _I32, device=dev)
+    n, shape = row_seq.numel(), page_table.shape
+    if len(shape) != 2:
+        raise ValueError(f"page_table must be [sequences, pages], got {tuple(shape)}")
+    if row_pos.numel() != n:
+        raise ValueError(f"row_pos must have {n} elements, got {row_pos.numel()}")
+    return _lib.SpecKvRows(n, shape[0], shape[1], page_table.data_ptr(), row_seq.data_ptr(), row_pos.data_ptr())
 
 
 def spec_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, row_seq: torch.Tensor,
@@ -553,18 +581,16 @@ def spec_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table:
     are taken as they are); row n goes to position row_pos[n] of sequence row_seq[n]
     (int32 [rows]), whose pages are page_table[row_seq[n]] (int32 [sequences, pages]); a
     negative position leaves the row out. Returns the dict with device_status."""
-    dt = _dtype_code(k)
-    if v.dtype != k.dtype:
-        raise TypeError(f"v must be {k.dtype}, got {v.dtype}")
-    dev = cache.device
+    dt = _KV_DTYPES.get(k.dtype)
+    if dt is None or v.dtype is not k.dtype:
+        raise TypeError(f"k and v must both be bfloat16 or float32, got {k.dtype} and {v.dtype}")
     r = _kv_rows(cache, page_table, row_seq, row_pos)
-    k_row, k_head = _strides(k, "k", r.rows, cache.kv_heads, cache.head_dim, dev)
-    v_row, v_head = _strides(v, "v", r.rows, cache.kv_heads, cache.head_dim, dev)
     o = {} if out is None else out
-    st = _status_word(o, device_status, dev)
-    check("spec_kv_append", _lib.lib().spec_kv_append(cache.desc, r, dt, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row,
-                                                      v_head, st.data_ptr(),
-                                                      _stream_handle(dev)))
+    code = _lib.lib().spec_kv_append(cache.desc, r, dt, *_rows_view(k, "k", r.rows, cache.kv_heads, cache),
+                                     *_rows_view(v, "v", r.rows, cache.kv_heads, cache),
+                                     _status_word(o, device_status, cache), _stream_handle(cache.index))
+    if code:
+        check("spec_kv_append", code)
     return o
 
 
@@ -573,61 +599,71 @@ def spec_kv_read(cache: KVCache, page_table: torch.Tensor, row_seq: torch.Tensor
                  out: dict | None = None, device_status=None) -> dict:
     """Read cached rows back as numbers: k, v [rows, kv_heads, head_dim] of dtype (bfloat16
     or float32, both exact), plus device_status. Rows with a negative position are zeros."""
-    dev = cache.device
+    dt = _KV_DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
     r = _kv_rows(cache, page_table, row_seq, row_pos)
     o = {} if out is None else out
-    shape = (r.rows, cache.kv_heads, cache.head_dim)
-
-    def dst(name, want):
+    n = r.rows * cache.kv_heads * cache.head_dim
+    to = []
+    for name, want in (("k", want_k), ("v", want_v)):
         if not want:
-            return None
-        t = _out(o, name, lambda: torch.empty(shape, dtype=dtype, device=dev))
-        _need(t, name, dtype, r.rows * cache.kv_heads * cache.head_dim, dev)
-        return t
-
-    k, v = dst("k", want_k), dst("v", want_v)
-    st = _status_word(o, device_status, dev)
-    code = {torch.bfloat16: _lib.SPEC_BF16, torch.float32: _lib.SPEC_F32}.get(dtype)
-    if code is None:
-        raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
-    check("spec_kv_read", _lib.lib().spec_kv_read(cache.desc, r, code, _ptr(k), _ptr(v), st.data_ptr(), _stream_handle(dev)))
+            to.append(None)
+            continue
+        t = o.get(name)
+        if t is None:
+            t = o[name] = torch.empty(r.rows, cache.kv_heads, cache.head_dim, dtype=dtype, device=cache.k.device)
+        elif not _is(t, dtype, cache.index) or t.numel() != n:
+            _need(t, name, dtype, n, cache.k.device)
+        to.append(t.data_ptr())
+    code = _lib.lib().spec_kv_read(cache.desc, r, dt, *to, _status_word(o, device_status, cache), _stream_handle(cache.index))
+    if code:
+        check("spec_kv_read", code)
     return o
 
 
 def _attn_batch(q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, prefix_table, prefix_len):
-    """(descriptor, rows, q_heads, keep-alive) of an attention call."""
-    dev = cache.device
-    _need(page_table, "page_table", torch.int32, device=dev)
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table must be [sequences, pages], got {tuple(page_table.shape)}")
-    B = page_table.shape[0]
-    _need(kv_len, "kv_len", torch.int32, B, dev)
-    H = q.shape[-2] if q.dim() >= 3 else 0
+    """(descriptor, rows, q_heads, the parent array it points to) of an attention call."""
+    index = cache.index
+    if not (_is(page_table, _I32, index) and _is(kv_len, _I32, index)):
+        _need(page_table, "page_table", _I32, device=cache.k.device)
+        _need(kv_len, "kv_len", _I32, device=cache.k.device)
+    table = page_table.shape
+    if len(table) != 2:
+        raise ValueError(f"page_table must be [sequences, pages], got {tuple(table)}")
+    B = table[0]
+    if kv_len.numel() != B:
+        raise ValueError(f"kv_len must have {B} elements, got {kv_len.numel()}")
+    shape = q.shape
+    H = shape[-2] if len(shape) >= 3 else 0
     par = None
     if parent is not None:
         if gamma is not None and int(gamma) != len(parent):
             raise ValueError(f"a tree of {len(parent)} nodes has gamma {len(parent)}, got {gamma}")
         gamma = len(parent)
-        par = (ctypes.c_int32 * len(parent))(*[int(x) for x in parent])
+        par = (ctypes.c_int32 * gamma)(*[int(x) for x in parent])
+    cu = None
     if cu_draft is None:
         if gamma is None:
-            if q.dim() != 4:
+            if len(shape) != 4:
                 raise ValueError("a dense batch of [rows, heads, dim] queries needs gamma")
-            gamma = q.shape[1] - 1
+            gamma = shape[1] - 1
         total = B * int(gamma)
     else:
         if gamma is None:
             raise ValueError("packed batches need gamma (an upper bound on every gamma_b)")
-        _need(cu_draft, "cu_draft", torch.int32, B + 1, dev)
-        total = (q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]) - B
-    n = int(prefix_len)
+        if not _is(cu_draft, _I32, index) or cu_draft.numel() != B + 1:
+            _need(cu_draft, "cu_draft", _I32, B + 1, cache.k.device)
+        cu = cu_draft.data_ptr()
+        total = (shape[0] if len(shape) == 3 else shape[0] * shape[1]) - B
+    n, pre = int(prefix_len), None
     if n > 0:
-        _need(prefix_table, "prefix_table", torch.int32, device=dev)
-        if prefix_table.numel() < -(-n // cache.page_size):
+        if not _is(prefix_table, _I32, index):
+            _need(prefix_table, "prefix_table", _I32, device=cache.k.device)
+        if prefix_table.numel() * cache.page_size < n:
             raise ValueError(f"prefix_table has {prefix_table.numel()} pages, {n} tokens need {-(-n // cache.page_size)}")
-    g = _lib.SpecAttnBatch(B, int(gamma), total, None if cu_draft is None else cu_draft.data_ptr(), H,
-                           page_table.shape[1], page_table.data_ptr(), kv_len.data_ptr(), n,
-                           prefix_table.data_ptr() if n > 0 else None,
+        pre = prefix_table.data_ptr()
+    g = _lib.SpecAttnBatch(B, int(gamma), total, cu, H, table[1], page_table.data_ptr(), kv_len.data_ptr(), n, pre,
                            None if par is None else ctypes.cast(par, ctypes.c_void_p),
                            cache.head_dim ** -0.5 if scale is None else float(scale))
     return g, total + B, H, par
@@ -654,28 +690,41 @@ def spec_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv
     `parent`, a host sequence as in spec_verify_tree: its ancestors) and, with prefix_len,
     the shared prefix on the pages prefix_table. scale defaults to head_dim ** -0.5.
     Returns o [rows, q_heads, head_dim], lse [rows, q_heads] (fp32, with want_lse) and
-    device_status."""
-    dt = _dtype_code(q)
-    dev = cache.device
+    device_status. The default workspace is kept for each stream; a call that is captured
+    into a graph takes one of the graph's own memory."""
+    dt = _KV_DTYPES.get(q.dtype)
+    if dt is None:
+        raise TypeError(f"q must be bfloat16 or float32, got {q.dtype}")
     g, rows, H, par = _attn_batch(q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, prefix_table, prefix_len)
-    q_row, q_head = _strides(q, "q", rows, H, cache.head_dim, dev)
+    view = _rows_view(q, "q", rows, H, cache)
     o = {} if out is None else out
-    y = _out(o, "o", lambda: torch.empty(rows, H, cache.head_dim, dtype=q.dtype, device=dev))
-    _need(y, "o", q.dtype, rows * H * cache.head_dim, dev)
+    y = o.get("o")
+    if y is None:
+        y = o["o"] = torch.empty(rows, H, cache.head_dim, dtype=q.dtype, device=cache.k.device)
+    elif not _is(y, q.dtype, cache.index) or y.numel() != rows * H * cache.head_dim:
+        _need(y, "o", q.dtype, rows * H * cache.head_dim, cache.k.device)
     lse = None
     if want_lse:
-        lse = _out(o, "lse", lambda: torch.empty(rows, H, dtype=torch.float32, device=dev))
-        _need(lse, "lse", torch.float32, rows * H, dev)
-    st = _status_word(o, device_status, dev)
+        t = _out(o, "lse", lambda: torch.empty(rows, H, dtype=torch.float32, device=cache.k.device))
+        _need(t, "lse", torch.float32, rows * H, cache.k.device)
+        lse = t.data_ptr()
     lib = _lib.lib()
-    nbytes = int(lib.spec_attention_workspace_bytes(g, cache.desc, dt))
-    stream = _stream_handle(dev)
+    nbytes = lib.spec_attention_workspace_bytes(g, cache.desc, dt)
+    stream = _stream_handle(cache.index)
     if workspace is None:
-        if torch.cuda.is_current_stream_capturing():  # a graph's own, from its memory pool
-            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        else:  # a default workspace for each stream: calls on two streams may overlap
-            workspace = _DEFAULT_WS.setdefault((dev.type, dev.index, stream), Workspace())
-    ws = _workspace(workspace, nbytes, dev)
-    check("spec_attention", lib.spec_attention(g, cache.desc, dt, q.data_ptr(), q_row, q_head, y.data_ptr(), _ptr(lse),
-                                               st.data_ptr(), ws.data_ptr(), ws.numel(), stream))
+        if torch.cuda.is_current_stream_capturing():
+            workspace = torch.empty(max(nbytes, 256), dtype=_U8, device=cache.k.device)
+        else:  # calls on two streams may overlap
+            keep = _DEFAULT_WS.get(("cuda", cache.index, stream))
+            if keep is None:
+                keep = _DEFAULT_WS[("cuda", cache.index, stream)] = Workspace()
+            workspace = keep.buf
+            if workspace is None or workspace.numel() < nbytes:
+                workspace = keep.get(nbytes, cache.k.device)
+    else:
+        workspace = _workspace(workspace, nbytes, cache.k.device)
+    code = lib.spec_attention(g, cache.desc, dt, *view, y.data_ptr(), lse, _status_word(o, device_status, cache),
+                              workspace.data_ptr(), workspace.numel(), stream)
+    if code:
+        check("spec_attention", code)
     return o
