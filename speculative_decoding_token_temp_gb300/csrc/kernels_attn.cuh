@@ -91,35 +91,32 @@ struct Place {
   int b, off;
 };
 
-struct LocateShared {
-  int warp_sum[32];
-  int bad;
-  Place at;
+// Block i's part of the line, as locate() finds it.
+struct Part {
+  int begin, end, total;
+  bool ok;   // cu is a valid prefix sum (nothing else counts when it is not)
+  Place at;  // where the part begins
 };
 
 // Where block i's part of a line of `total` tiles begins, of n blocks (the first total % n
 // have one tile more). The host has seen to it that a line's length fits an int.
 __device__ __forceinline__ int line_at(int total, int i, int n) { return total / n * i + min(i, total % n); }
 
-// Block-wide: the line's length, block i's part of it (of n), and the place where that
-// begins. Each thread sums a stretch of sequences, the block scans the sums, and the thread
-// whose stretch holds the place walks to it. Returns false when cu is no valid prefix sum
-// (nothing else it says is then used).
-template <int NR, int THREADS>
-__device__ __noinline__ bool locate(const AttnParams& p, LocateShared& sh, int i, int n, int* begin, int* end, int* line) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) sh.bad = 0;
-  __syncthreads();
-  const int per = (p.B + THREADS - 1) / THREADS;
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+// Warp-wide: the line's length, block i's part of it (of n), and the place where that
+// begins. Each lane sums a stretch of sequences, the warp scans the sums, and the lane whose
+// stretch holds the place walks to it.
+template <int NR>
+__device__ __noinline__ Part locate(const AttnParams& p, int i, int n) {
+  const int lane = threadIdx.x & 31, per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
   int sum = 0;
-#pragma unroll 1
+  bool bad = false;
+#pragma unroll 4
   for (int b = b0; b < b1; ++b) {
     if (p.cu != nullptr) {
       const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1);
       if (lo < 0 || hi > p.total_draft || hi < lo || hi - lo > p.gamma || (b == 0 && lo != 0) ||
           (b == p.B - 1 && hi != p.total_draft)) {
-        sh.bad = 1;
+        bad = true;
         continue;
       }
     }
@@ -131,34 +128,38 @@ __device__ __noinline__ bool locate(const AttnParams& p, LocateShared& sh, int i
     const int y = __shfl_up_sync(kFull, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) sh.warp_sum[warp] = incl;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += sh.warp_sum[w];
-    total += sh.warp_sum[w];
-  }
-  const int excl = before + incl - sum;
-  const bool ok = sh.bad == 0;
-  *begin = line_at(total, i, n);
-  *end = line_at(total, i + 1, n);
-  *line = total;
-  if (ok && *begin >= excl && *begin < excl + sum) {
-    int at = excl;
+  Part r;
+  r.total = __shfl_sync(kFull, incl, 31);
+  r.ok = !__any_sync(kFull, bad);
+  r.begin = line_at(r.total, i, n);
+  r.end = line_at(r.total, i + 1, n);
+  const int excl = incl - sum;
+  const bool here = r.ok && r.begin >= excl && r.begin < incl;
+  int b = b0, off = r.begin - excl;
+  if (here) {
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
+    for (; b < b1 - 1; ++b) {
       const int t = seq_tiles<NR>(p, seq_info(p, b));
-      if (*begin < at + t) {
-        sh.at.b = b;
-        sh.at.off = *begin - at;
-        break;
-      }
-      at += t;
+      if (off < t) break;
+      off -= t;
     }
   }
+  const unsigned who = __ballot_sync(kFull, here);
+  const int src = who ? __ffs(who) - 1 : 0;
+  r.at.b = __shfl_sync(kFull, b, src);
+  r.at.off = __shfl_sync(kFull, off, src);
+  return r;
+}
+
+// The same for the whole block, by its first warp.
+template <int NR>
+__device__ __forceinline__ Part locate_block(const AttnParams& p, Part& shared) {
+  if (threadIdx.x < 32) {
+    const Part r = locate<NR>(p, blockIdx.x, gridDim.x);
+    if (threadIdx.x == 0) shared = r;
+  }
   __syncthreads();
-  return ok;
+  return shared;
 }
 
 // One segment's stretch that a block works on.
@@ -285,13 +286,13 @@ __device__ __forceinline__ float* slot_of(const AttnParams& p, int s) {
   return p.part + (long long)s * (NR * (D + 2));
 }
 
-// A cu that is no prefix sum of the batch: every row is NaN.
+// A cu that is no prefix sum of the batch: every row is NaN (by the first `threads` threads of each block).
 template <typename E, int D>
-__device__ __noinline__ void fill_nan(const AttnParams& p, int block, int blocks) {
+__device__ __noinline__ void fill_nan(const AttnParams& p, int block, int blocks, int threads) {
   if (block == 0 && threadIdx.x == 0) atomicOr(p.status, SPEC_DEV_OFFSETS);
   const long long n = (long long)p.R * p.Hq * D;
   const float nan = __int_as_float(0x7fffffff);
-  for (long long i = (long long)block * blockDim.x + threadIdx.x; i < n; i += (long long)blocks * blockDim.x) {
+  for (long long i = (long long)block * threads + threadIdx.x; i < n; i += (long long)blocks * threads) {
     put(static_cast<E*>(p.o) + i, nan);
     if (p.lse != nullptr && i % D == 0) p.lse[i / D] = nan;
   }
@@ -375,7 +376,7 @@ template <typename E, int D>
 __global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
   constexpr int NR = kRowsS, KS = D + 16;  // a key's stride: 16 bytes more than its codes, so that 8 lanes hit all banks
   constexpr int NG = 128 / (D / 4);        // token groups of the values' sum
-  __shared__ LocateShared sh;
+  __shared__ Part s_part;
   __shared__ __align__(16) float sq[NR][D];
   __shared__ __align__(16) uint8_t skv[kTile * KS + kTile * D];
   __shared__ __align__(16) float sp[kTile][NR];
@@ -392,19 +393,16 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
   if (p.mask == A_TREE && tid < SPEC_MAX_TREE_NODES) s_sees[tid] = p.sees[tid];
   griddep_wait();
   griddep_launch();
-  int begin, end, total;
-  if (!locate<NR, 128>(p, sh, blockIdx.x, gridDim.x, &begin, &end, &total)) {
-    fill_nan<E, D>(p, blockIdx.x, gridDim.x);
-    begin = end = 0;
-  }
-  Place at = sh.at;
-  int left = end - begin;
+  const Part line = locate_block<NR>(p, s_part);
+  if (!line.ok) fill_nan<E, D>(p, blockIdx.x, gridDim.x, 128);
+  Place at = line.at;
+  int left = line.ok ? line.end - line.begin : 0;
   uint32_t bits = 0;
   if (tid == 0) p.cut[blockIdx.x].parts = 0;
   while (left > 0) {
     const Seg g = next_seg<NR>(p, at, left);
     if (g.n == 0) continue;
-    if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, end, total);
+    if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, line.end, line.total);
     if (g.bad) bits |= SPEC_DEV_OFFSETS;
     __syncthreads();
     for (int e = tid; e < NR * D; e += 128) {

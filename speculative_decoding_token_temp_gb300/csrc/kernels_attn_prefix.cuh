@@ -167,7 +167,7 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
 template <int D>
 struct PreShared {
   using T = PreShape<D>;
-  LocateShared loc;
+  Part line;
   uint64_t k_full[T::kStages], k_free[T::kStages], v_full[T::kStages], v_free[T::kStages];
   uint64_t q_full, drained, s_full[2], p_full[2], o_done[2];
   uint32_t tmem;
@@ -216,12 +216,11 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   }
   griddep_wait();
   griddep_launch();
-  int begin, end, total;
-  locate<NR, kPreThreads>(p, sh.loc, blockIdx.x, gridDim.x, &begin, &end, &total);  // (one dense sequence: no cu)
+  const Part line = locate_block<NR>(p, sh.line);  // (one dense sequence: no cu)
   tc_after();
   const uint32_t tmem = sh.tmem;
-  Place at = sh.loc.at;
-  int left = end - begin;
+  Place at = line.at;
+  int left = line.end - line.begin;
 
   if (warp == 16) {
     // ---- the rings of tiles ----
@@ -330,7 +329,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     while (left > 0) {
       const Seg g = next_seg<NR>(p, at, left);
       if (g.n == 0) continue;
-      if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, end, total);
+      if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, line.end, line.total);
       const int flat = g.rows * p.G, f = g.f0 + c;
       // half of this thread's query row into shared memory, swizzled
       bool bad = false;

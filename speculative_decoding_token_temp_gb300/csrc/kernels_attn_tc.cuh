@@ -228,10 +228,9 @@ __device__ __forceinline__ void tc_sum_parts(uint32_t at, float (&o)[4]) {
 template <int D, int NR>
 struct TcShared {
   using T = TcShape<D, NR>;
-  LocateShared loc;
   uint64_t k_full[T::kNK], k_free[T::kNK], v_full[T::kNV], v_free[T::kNV], q_full, drained, s_full, s_free, p_full, o_done;
   uint64_t seg_full[kSegRing];
-  Seg seg[kSegRing];                // the block's stretches, as the copying warp comes to them; n = 0: no more
+  Seg seg[kSegRing];                // the block's stretches, as the copying warp comes to them; n = 0: no more, -1: a bad cu
   uint32_t tmem;
   int gave_up;
   uint32_t bad_pages[T::kNK];
@@ -362,30 +361,26 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   // everything before the call; so the wait for the prefix's part comes before the first join.
   if (!p.late_wait) griddep_wait();
   griddep_launch();
-  int begin, end, total;
-  const bool ok = locate<NR, kTcThreads>(p, sh.loc, blockIdx.x, gridDim.x, &begin, &end, &total);
+  __syncthreads();
   tc_after();
   const uint32_t tmem = sh.tmem;
-  if (!ok) {
-    if (p.late_wait) griddep_wait();
-    fill_nan<uint16_t, D>(p, blockIdx.x, gridDim.x);
-    begin = end = 0;
-  }
-  Place at = sh.loc.at;
-  int left = end - begin;
 
   if (warp == 8) {
     // ---- the rings of tiles ----
     int gi = 0, ns = 0;
     uint32_t bits = 0;
+    const Part line = locate<NR>(p, blockIdx.x, gridDim.x);
+    Place at = line.at;
+    int left = line.ok ? line.end - line.begin : 0;
     const int psz = 1 << p.page_shift, box = min(psz, kTile), np = kTile / box;
+    const bool bulk = psz >= 64;
     if (lane == 0) p.cut[blockIdx.x].parts = 0;
     while (left > 0) {
       const Seg g = next_seg<NR>(p, at, left);
       if (g.n == 0) continue;
       if (g.bad) bits |= SPEC_DEV_OFFSETS;
       if (lane == 0) {
-        if (left == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, end, total);
+        if (left == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, line.end, line.total);
         // the stretch that had this place is read: its tiles left the rings before the ones in front of this one's came in
         sh.seg[ns % kSegRing] = g;
         mbar_arrive(bar(sh.seg_full[ns % kSegRing]));
@@ -400,12 +395,25 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       }
       auto page_of = [&](int tile) -> int {  // of this lane's part of a tile
         const int t = tile * kTile + lane * box;
-        return lane < np && t < g.len ? __ldg(g.pages + (t >> p.page_shift)) : -2;
+        return lane < np && tile < g.t0 + g.n && t < g.len ? __ldg(g.pages + (t >> p.page_shift)) : -2;
       };
-      int page = page_of(g.t0);
+      // The exponents of a tile: by a bulk copy a page, or, where pages are small and that would be as many operations as the
+      // codes take, by ordinary loads a tile ahead: lane l holds those of tokens 8 (l % 16) .. + 7, the keys' in the lower half
+      // of the warp, the values' in the upper. (32 x 13 rows, head_dim 64, pages of 16: 36.4 -> 32.6 us; with pages of 64 the
+      // warp would stand waiting for them: 256 x 1 row to 8192 330 -> 357 us.)
+      const uint8_t* const exps = (lane < 16 ? p.k_exp : p.v_exp) + ((long long)g.h << p.page_shift);
+      auto exps_of = [&](int tile, int page) -> uint2 {
+        if (bulk) return make_uint2(0, 0);
+        const int t = (lane & 15) * 8, mine = __shfl_sync(kFull, page, t / box);
+        if ((unsigned)mine >= (unsigned)p.num_pages) return make_uint2(0, 0);
+        return __ldcg(reinterpret_cast<const uint2*>(exps + (((long long)mine * p.Hk) << p.page_shift) + ((tile * kTile + t) & (psz - 1))));
+      };
+      int page = page_of(g.t0), next = page_of(g.t0 + 1);
+      uint2 e = exps_of(g.t0, page);
       for (int k = 0; k < g.n; ++k, ++gi) {
         const int sk = gi % NK, sv = gi % NV, tile = g.t0 + k;
-        const int next = k + 1 < g.n ? page_of(tile + 1) : -2;
+        const int after = page_of(tile + 2);
+        const uint2 e_next = exps_of(tile + 1, next);
         const bool there = lane < np && tile * kTile + lane * box < g.len;
         const bool good = there && (unsigned)page < (unsigned)p.num_pages;
         const unsigned bad = __ballot_sync(kFull, there && !good), cnt = __popc(__ballot_sync(kFull, good));
@@ -413,28 +421,28 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         const int tok = (tile * kTile + lane * box) & (psz - 1);
         const uint32_t bk = bar(sh.k_full[sk]), bv = bar(sh.v_full[sv]);
         if (gi >= NK) tc_wait(bar(sh.k_free[sk]), (gi / NK - 1) & 1, gave_up, p.status);
-        __syncwarp();
-        if (lane == 0) {
-          sh.bad_pages[sk] = bad;
-          mbar_expect_arrive(bk, cnt * (uint32_t)(box * (D + 2)));
-        }
-        __syncwarp();
-        if (good) {
-          tma_page(base + T::oK + sk * T::kTileBytes + lane * box * D, &map_k, tok, g.h, page, bk);
+        if (good) tma_page(base + T::oK + sk * T::kTileBytes + lane * box * D, &map_k, tok, g.h, page, bk);
+        if (!bulk) {
+          *reinterpret_cast<uint2*>(mem + T::oE + sk * 2 * kTile + lane * 8) = e;
+        } else if (good) {
           const long long vec = (((long long)page * p.Hk + g.h) << p.page_shift) + tok;
           bulk_copy(base + T::oE + sk * 2 * kTile + lane * box, p.k_exp + vec, box, bk);
           bulk_copy(base + T::oE + sk * 2 * kTile + kTile + lane * box, p.v_exp + vec, box, bk);
         }
-        if (gi >= NV) tc_wait(bar(sh.v_free[sv]), (gi / NV - 1) & 1, gave_up, p.status);
+        if (lane == 0) sh.bad_pages[sk] = bad;
         __syncwarp();
+        if (lane == 0) mbar_expect_arrive(bk, cnt * (uint32_t)(box * (bulk ? D + 2 : D)));
+        if (gi >= NV) tc_wait(bar(sh.v_free[sv]), (gi / NV - 1) & 1, gave_up, p.status);
+        if (good) tma_page(base + T::oV + sv * T::kTileBytes + lane * box * D, &map_v, tok, g.h, page, bv);
         if (lane == 0) mbar_expect_arrive(bv, cnt * (uint32_t)(box * D));
         __syncwarp();
-        if (good) tma_page(base + T::oV + sv * T::kTileBytes + lane * box * D, &map_v, tok, g.h, page, bv);
         page = next;
+        next = after;
+        e = e_next;
       }
     }
     if (lane == 0) {
-      sh.seg[ns % kSegRing].n = 0;
+      sh.seg[ns % kSegRing].n = line.ok ? 0 : -1;
       mbar_arrive(bar(sh.seg_full[ns % kSegRing]));
     }
     if (bits) atomicOr(p.status, bits);
@@ -457,7 +465,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     for (int ns = 0;; ++ns) {
       tc_wait(bar(sh.seg_full[ns % kSegRing]), (ns / kSegRing) & 1, gave_up, p.status);
       const int n = __shfl_sync(kFull, *gave_up ? 0 : sh.seg[ns % kSegRing].n, 0);
-      if (n == 0) break;
+      if (n <= 0) break;
       tc_wait(bar(sh.q_full), ns & 1, gave_up, p.status);
 #pragma unroll 1
       for (int k = -1; k < n; ++k) {
@@ -519,7 +527,11 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     for (int ns = 0;; ++ns) {
       tc_wait(bar(sh.seg_full[ns % kSegRing]), (ns / kSegRing) & 1, gave_up, p.status);
       const Seg g = sh.seg[ns % kSegRing];
-      if (bar_or(1, kTcSoft, g.n == 0 || *gave_up)) break;  // (all threads alike, also after a wait that gave up)
+      if (bar_or(1, kTcSoft, g.n <= 0 || *gave_up)) {  // (all threads alike, also after a wait that gave up)
+        if (p.late_wait) griddep_wait();
+        if (g.n < 0 && !*gave_up) fill_nan<uint16_t, D>(p, blockIdx.x, gridDim.x, kTcSoft);
+        break;
+      }
       stage_queries<D, NR>(p, g, sh, mem + T::oQ, tid);
       fence_async();
       mbar_arrive(bar(sh.q_full));
