@@ -55,19 +55,27 @@ PROFILE = os.path.join(ROOT, "profiles", "stochastic_call_B256_g8_V128256.md")
 
 
 def kernel_sources_sha256() -> str:
-    """Hash of the CUDA sources, the host planning header and the C header (the same recipe
-    as the profile summary)."""
-    import glob
+    """Hash of the verification library's CUDA source with the headers it includes, the host
+    planning header among them, and the C header (the same recipe as the profile summary).
+    Other sources beside them do not enter it."""
     import hashlib
+    import re
     csrc = os.path.join(ROOT, "speculative_decoding_token_temp_gb300", "csrc")
-    files = sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh")) +
-                   glob.glob(os.path.join(csrc, "*.h")))
-    files.append(os.path.join(ROOT, "include", "spec_verify.h"))
+    text, todo = {}, ["spec_verify.cu"]
+    while todo:
+        name = todo.pop()
+        if name in text:
+            continue
+        with open(os.path.join(csrc, name), "rb") as fh:
+            text[name] = fh.read()
+        todo += [n for n in re.findall(r'^#include "([^"]+)"', text[name].decode(), re.M)
+                 if os.path.exists(os.path.join(csrc, n))]
+    with open(os.path.join(ROOT, "include", "spec_verify.h"), "rb") as fh:
+        files = sorted(text.items()) + [("spec_verify.h", fh.read())]
     h = hashlib.sha256()
-    for f in files:
-        h.update(os.path.basename(f).encode())
-        with open(f, "rb") as fh:
-            h.update(fh.read())
+    for name, data in files:
+        h.update(name.encode())
+        h.update(data)
     return h.hexdigest()
 
 

@@ -103,10 +103,13 @@ KvParams kv_params(const spec_kv_cache& c, const spec_kv_rows& r, uint32_t* stat
   return p;
 }
 
-// The split of an append or a read: as many heads to an item as a warp has on the way at
-// once where that leaves work for every resident warp (64 an SM), else as many as it holds
-// side by side; then up to 16 items a warp, which spreads the lookups' latency over them.
-// 32768 rows of 8 heads: 50 us with 8 heads an item, 68 with 2; 256 rows: 3.3 and 2.3 us.
+// The split of an append or a read: an item is one side of a row and as many of its heads as
+// a warp has on the way at once (four steps of what it holds side by side), or only what it
+// holds side by side where a row has no more heads, or where that many items do not fill half
+// of the resident warps (64 an SM); then up to 16 items a warp, which spreads the lookups'
+// latency over them. Append in bf16, one step / four: 8 heads of 128, 256 rows 3.7 / 4.1 us,
+// 512 even, 2304 rows 8.2 / 5.8, 32768 rows 60 / 42; 2 heads (one step holds them) 32768 rows
+// 16.4 / 19.7.
 struct KvGrid {
   unsigned blocks;
   KvSplit k;
@@ -116,7 +119,7 @@ KvGrid kv_grid(const KvParams& p, int D, int unroll) {
   const int side_by_side = 32 / (D / 8);
   KvGrid g;
   g.k.heads = side_by_side * unroll;
-  if (sides * cdiv(p.Hk, g.k.heads) <= 2 * warps) g.k.heads = side_by_side;
+  if (p.Hk <= side_by_side || 2 * sides * cdiv(p.Hk, side_by_side) <= warps) g.k.heads = side_by_side;
   g.k.split = (int)cdiv(p.Hk, g.k.heads);
   const long long items = sides * g.k.split, per = cdiv(items, 2 * warps);
   g.k.per = (int)(per < 1 ? 1 : per > 16 ? 16 : per);
@@ -153,9 +156,9 @@ constexpr long long kMaxLine = 1LL << 30;  // a line of tiles is counted in ints
 constexpr int kMaxGridP = 160;   // of attn_prefix_kernel (one block an SM)
 // The prefix is widened and computed in 128-row tiles where that pays for the widening: from
 // this many row-tiles of keys on (rows that share keys x tiles x kv heads). Below, the 48- or
-// 32-row blocks of attn_tc_kernel do it: head_dim 128, 8 kv heads, 288 rows x 2000 tokens 36 us
-// against 44, 576 x 8192 even, 9216 x 16384 1.5 ms against 0.57; head_dim 64, 576 rows: 2000
-// tokens even, 8192 tokens 66 us against 49.
+// 32-row blocks of attn_tc_kernel do it. Whole calls, 8 kv heads, narrow / wide: head_dim 128,
+// 288 rows x 2000 tokens 34 / 43 us, 1152 x 2000 51 / 57, 576 x 8192 66 / 69, 1152 x 8192
+// 105 / 83; head_dim 64, 576 x 2000 34.5 / 35.6, 1152 x 2000 51 / 47, 576 x 8192 64 / 51.
 constexpr long long kWideWork128 = 300000, kWideWork64 = 75000;
 constexpr int kMaxGridT = 512;   // of the tensor-core kernel (two blocks an SM)
 
