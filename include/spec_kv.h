@@ -102,7 +102,9 @@ typedef struct {
   float scale;                 /* factor of the scores before the softmax, finite and > 0 */
 } spec_attn_batch;
 
-/* Bytes of scratch memory spec_attention needs (0 for an invalid geometry or dtype). */
+/* Bytes of scratch memory spec_attention needs (0 for an invalid geometry or dtype, or one
+ * whose work, counted in 128-token tiles of all sequences at their longest, passes 2^30;
+ * spec_attention refuses those with SPEC_ERR_INVALID_ARG). */
 size_t spec_attention_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype);
 
 /*
