@@ -68,7 +68,7 @@ struct TcShape {
   // tensor memory: scores of the two parts, then the values' sums of the three
   static constexpr int cO = 2 * NR, cHalf = 3 * NR;
   static_assert(cO + kHalves * cHalf <= 256, "two blocks share the tensor memory");
-  static_assert(kHalves == 1 || NR * D * 4 <= kP, "the second half's sums pass through the weights' memory");
+  static_assert((kHalves == 2 ? NR * D * 4 : 0) + NR * D * 2 <= kP, "sums pass through the weights' memory");
   static_assert(kSmem <= 107 * 1024, "two blocks share the shared memory");
 };
 
@@ -184,14 +184,23 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {  // a in the lo
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
-__device__ __forceinline__ uint32_t widen2(uint32_t two) {  // two e4m3 codes (low 16 bits) as f16x2
+// Four f16 values rounded to e4m3 codes (in order from the low byte), and what those codes
+// are as f16. The codes stay 16-bit registers until they are joined: a conversion packs its
+// result beside another's, while a zero-extended one costs an instruction of its own.
+__device__ __forceinline__ uint32_t narrow4(uint32_t h0, uint32_t h1) {
   uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two));
+  asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
+      "mov.b32 %0, {a, b};\n\t}"
+      : "=r"(r)
+      : "r"(h0), "r"(h1));
   return r;
 }
-__device__ __forceinline__ uint32_t narrow2(uint32_t h2) {  // f16x2 rounded to two e4m3 codes
+__device__ __forceinline__ uint32_t narrow4(uint32_t h0, uint32_t h1, uint32_t& w0, uint32_t& w1) {
   uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(r) : "r"(h2));
+  asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f16x2 a, %3;\n\tcvt.rn.satfinite.e4m3x2.f16x2 b, %4;\n\t"
+      "mov.b32 %0, {a, b};\n\tcvt.rn.f16x2.e4m3x2 %1, a;\n\tcvt.rn.f16x2.e4m3x2 %2, b;\n\t}"
+      : "=r"(r), "=&r"(w0), "=r"(w1)
+      : "r"(h0), "r"(h1));
   return r;
 }
 // 16 * (a - b) of f16 pairs (exact where b is a rounded to a part's 4 bits)
@@ -236,14 +245,16 @@ struct TcShared {
   uint32_t bad_pages[T::kNK];
   uint64_t sees[SPEC_MAX_TREE_NODES];
   uint8_t nan_code[kTile];          // of a tile with masked places: the token's values hold a NaN code
-  alignas(16) float rq[NR];         // a row's factor of the scores: scale * log2(e) * its power of two
-  alignas(16) int row[NR];          // query row of a flat row
-  alignas(16) float neg_m[NR];      // the reference, negated
+  struct Rows {                     // of a stretch's rows
+    alignas(16) float rq[NR];       // the factor of the scores: scale * log2(e) * the row's power of two
+    alignas(16) int row[NR];        // query row of a flat row
+    alignas(16) float neg_m[NR];    // the reference, negated
+    alignas(16) int idx[NR];        // row * query heads + head, -1 past the last
+  } rows[2];                        // the next stretch's queries are staged before this one's end
   alignas(16) float delta[NR];      // its last change, and 2^that
   alignas(16) float factor[NR];
   float red[4][NR];                 // of the warps of a token each: maxima of the columns
   float2 coef[NR];                  // weights of a row's values and of the prefix's part
-  alignas(16) int idx[NR];          // row * query heads + head, -1 past the last
 };
 
 // Queries of a stretch staged for the scores' MMA: TPR threads a row find its power of two
@@ -251,7 +262,7 @@ struct TcShared {
 // has them. (Loops kept short: what runs once a stretch should not push the tiles' loop out
 // of the instruction caches.)
 template <int D, int NR>
-__device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g, TcShared<D, NR>& sh, uint8_t* q, int t) {
+__device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g, typename TcShared<D, NR>::Rows& rows, uint8_t* q, int t) {
   constexpr int TPR = NR == 48 ? 4 : 8, E = D / TPR;
   const int c = t / TPR, part = t % TPR, f = g.f0 + c;
   if (c < NR) {  // (whole warps)
@@ -286,30 +297,35 @@ __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g,
     const int e = max((int)(top >> 7) - 127, -100) - 7;  // the largest element comes to [128, 256)
     const float inv = bad ? 0.f : __int_as_float((127 - e) << 23);
     if (part == 0) {
-      sh.rq[c] = bad ? __int_as_float(0x7fffffff) : p.c * __int_as_float((e + 127) << 23);
-      sh.row[c] = i;
-      sh.idx[c] = here ? idx : -1;
-      sh.neg_m[c] = 0.f;
+      rows.rq[c] = bad ? __int_as_float(0x7fffffff) : p.c * __int_as_float((e + 127) << 23);
+      rows.row[c] = i;
+      rows.idx[c] = here ? idx : -1;
+      rows.neg_m[c] = 0.f;
     }
     const int rl = NR + c;
 #pragma unroll
     for (int k = 0; k < E / 8; ++k) {
       const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-      uint32_t hi[4], lo[4];
+      uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
         // scaled to [0, 256) an element is exact in f16 (8 bits) down to 2^-17 of it
-        const uint32_t h = bad ? 0u : half2_of(__uint_as_float(w[j] << 16) * inv, __uint_as_float(w[j] & 0xffff0000u) * inv);
-        hi[j] = narrow2(h);
-        uint32_t r;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(widen2(hi[j])));
-        lo[j] = narrow2(r);
+        uint32_t h[2], c1[2];
+#pragma unroll
+        for (int i2 = 0; i2 < 2; ++i2) {
+          const uint32_t u = w[2 * j + i2];
+          h[i2] = bad ? 0u : half2_of(__uint_as_float(u << 16) * inv, __uint_as_float(u & 0xffff0000u) * inv);
+        }
+        hi[j] = narrow4(h[0], h[1], c1[0], c1[1]);
+#pragma unroll
+        for (int i2 = 0; i2 < 2; ++i2) asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[i2]) : "r"(c1[i2]));
+        lo[j] = narrow4(h[0], h[1]);
       }
       const int at = part * E + k * 8, chunk = at >> 4;
       const int ch_h = D == 128 ? chunk ^ (c & 7) : chunk ^ ((c >> 1) & 3);
       const int ch_l = D == 128 ? chunk ^ (rl & 7) : chunk ^ ((rl >> 1) & 3);
-      *reinterpret_cast<uint2*>(q + c * D + ch_h * 16 + (at & 15)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-      *reinterpret_cast<uint2*>(q + rl * D + ch_l * 16 + (at & 15)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      *reinterpret_cast<uint2*>(q + c * D + ch_h * 16 + (at & 15)) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(q + rl * D + ch_l * 16 + (at & 15)) = make_uint2(lo[0], lo[1]);
     }
   }
 }
@@ -524,18 +540,26 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     const float nan = __int_as_float(0x7fffffff), ninf = __int_as_float(kNegInfBits);
     int gi = 0;
     f2 l2[NH / 2];
-    for (int ns = 0;; ++ns) {
+    // Stretch ns's queries to the MMA warp, if it is one (false: no more stretches, also after a wait that gave up). The
+    // buffer's last reader, the scores of the last tile of the stretch before, is done.
+    auto begin = [&](int ns) -> bool {
       tc_wait(bar(sh.seg_full[ns % kSegRing]), (ns / kSegRing) & 1, gave_up, p.status);
-      const Seg g = sh.seg[ns % kSegRing];
-      if (bar_or(1, kTcSoft, g.n <= 0 || *gave_up)) {  // (all threads alike, also after a wait that gave up)
-        if (p.late_wait) griddep_wait();
-        if (g.n < 0 && !*gave_up) fill_nan<uint16_t, D>(p, blockIdx.x, gridDim.x, kTcSoft);
-        break;
-      }
-      stage_queries<D, NR>(p, g, sh, mem + T::oQ, tid);
+      const Seg& g = sh.seg[ns % kSegRing];
+      if (bar_or(1, kTcSoft, g.n <= 0 || *gave_up)) return false;  // (all threads alike)
+      stage_queries<D, NR>(p, g, sh.rows[ns & 1], mem + T::oQ, tid);
       fence_async();
       mbar_arrive(bar(sh.q_full));
-      bar_sync(1, kTcSoft);  // rq, row and the references are seen by all
+      return true;
+    };
+    bool more = begin(0);
+    if (!more) {
+      if (p.late_wait) griddep_wait();
+      if (sh.seg[0].n < 0 && !*gave_up) fill_nan<uint16_t, D>(p, blockIdx.x, gridDim.x, kTcSoft);
+    }
+    bar_sync(1, kTcSoft);  // what was staged is seen by all
+    for (int ns = 0; more; ++ns) {
+      const Seg g = sh.seg[ns % kSegRing];
+      auto& rows = sh.rows[ns & 1];
 #pragma unroll
       for (int i = 0; i < NH / 2; ++i) l2[i] = 0ull;
       for (int k = 0; k < g.n; ++k, ++gi) {
@@ -587,7 +611,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           if (p.mask == A_TREE && sees.nodes != ~0ull) {
 #pragma unroll 1
             for (int c = 0; c < NH; ++c)
-              if (!sees(sh.row[c0 + c])) sight &= ~(1u << c);
+              if (!sees(rows.row[c0 + c])) sight &= ~(1u << c);
           }
         }
         // scores
@@ -604,8 +628,8 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         tc_wait_ld();
 #pragma unroll
         for (int c = 0; c < NH; c += 4) {
-          const float4 rq = *reinterpret_cast<const float4*>(&sh.rq[c0 + c]);
-          const float4 nm = *reinterpret_cast<const float4*>(&sh.neg_m[c0 + c]);
+          const float4 rq = *reinterpret_cast<const float4*>(&rows.rq[c0 + c]);
+          const float4 nm = *reinterpret_cast<const float4*>(&rows.neg_m[c0 + c]);
           const uint32_t *a = &hi[c / 8][c % 8], *b = &lo[c / 8][c % 8];
           const f2 s0 = add2(pack(__uint_as_float(a[0]), __uint_as_float(a[1])), pack(__uint_as_float(b[0]), __uint_as_float(b[1])));
           const f2 s1 = add2(pack(__uint_as_float(a[2]), __uint_as_float(a[3])), pack(__uint_as_float(b[2]), __uint_as_float(b[3])));
@@ -661,7 +685,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
             if (mx != ninf && (first || mx > kTop)) d = mx - kTop;
             sh.delta[c] = -d;
             sh.factor[c] = first ? 1.f : ex2(-d);  // (nothing is summed yet: 0 times an infinity is no 0)
-            sh.neg_m[c] -= d;
+            rows.neg_m[c] -= d;
           }
           bar_sync(half_bar, 128);
           if (!first) {
@@ -703,19 +727,22 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         for (int c = 0; c < NH; c += 8) {
           uint32_t part[3][2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float a, b;
-            unpack(x[c / 2 + j], a, b);
-            a = ex2(a);
-            b = ex2(b);
-            l2[c / 2 + j] = fma2(pack(a, b), isv2, l2[c / 2 + j]);
-            const uint32_t h = half2_of(a, b), c1 = narrow2(h), h1 = rest16(h, widen2(c1)), c2 = narrow2(h1),
-                           c3 = narrow2(rest16(h1, widen2(c2)));
-            if (j % 2 == 0) {
-              part[0][j / 2] = c1, part[1][j / 2] = c2, part[2][j / 2] = c3;
-            } else {
-              part[0][j / 2] |= c1 << 16, part[1][j / 2] |= c2 << 16, part[2][j / 2] |= c3 << 16;
+          for (int j = 0; j < 2; ++j) {
+            uint32_t h[2], w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float a, b;
+              f2& l = l2[c / 2 + 2 * j + i];
+              unpack(x[c / 2 + 2 * j + i], a, b);
+              a = ex2(a);
+              b = ex2(b);
+              l = fma2(pack(a, b), isv2, l);
+              h[i] = half2_of(a, b);
             }
+            part[0][j] = narrow4(h[0], h[1], w[0], w[1]);
+            h[0] = rest16(h[0], w[0]), h[1] = rest16(h[1], w[1]);
+            part[1][j] = narrow4(h[0], h[1], w[0], w[1]);
+            part[2][j] = narrow4(rest16(h[0], w[0]), rest16(h[1], w[1]));
           }
 #pragma unroll
           for (int k3 = 0; k3 < 3; ++k3) {
@@ -727,19 +754,23 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh.p_full));
       }
-      // ---- the end of the stretch ----
+      // ---- the end of the stretch: the next one's queries first, so that its scores are computed meanwhile ----
+      more = begin(ns + 1);
       const bool whole = g.n == g.nt, join = whole && p.pre_o != nullptr && t < D;
       const int d = t & (D - 1);
       if (p.late_wait) griddep_wait();
       float pre[NH];  // this element of the prefix's part, on its way while the sums are joined
 #pragma unroll
       for (int c = 0; c < NH; ++c) {
-        const int idx = sh.idx[c0 + c];
+        const int idx = rows.idx[c0 + c];
         pre[c] = join && idx >= 0 ? __ldcg(p.pre_o + (long long)idx * D + d) : 0.f;
       }
-      // sums over the tokens: first over the lanes that share a place in the queries' memory (their scores are done)
-      constexpr int kPer = D / 2;  // partial sums of a column that fit there
-      float* const part = reinterpret_cast<float*>(mem + T::oQ);
+      tc_wait(bar(sh.o_done), (gi - 1) & 1, gave_up, p.status);
+      tc_after();
+      // the weights' memory, read by now: the second token half's sums with head_dim 64, then partial sums of the weights
+      float* const half = reinterpret_cast<float*>(mem + T::oP) + c0 * D;
+      float* const part = reinterpret_cast<float*>(mem + T::oP + (kHalves == 2 ? NR * D * 4 : 0));
+      constexpr int kPer = D / 2;  // partial sums of a column: over the lanes first that share a place
 #pragma unroll
       for (int c = 0; c < NH; c += 2) {
         float a, b;
@@ -757,10 +788,10 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
       float* slot = whole ? nullptr : slot_of<NR, D>(p, 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0));
       bar_sync(1, kTcSoft);
       if (tid < 4 * NR) {  // (whole warps) four threads a column
-        const int col = tid >> 2, idx = sh.idx[col];
+        const int col = tid >> 2, idx = rows.idx[col];
         const float lse = whole && idx >= 0 && p.pre_o != nullptr ? __ldcg(p.pre_lse + idx) : ninf;
         float l = 0.f;
-        const float m = -sh.neg_m[col];
+        const float m = -rows.neg_m[col];
 #pragma unroll
         for (int i = 0; i < kPer / 4; ++i) l += part[col * kPer + ((i + col) * 4 & (kPer - 1)) + (tid & 3)];
         l += __shfl_xor_sync(kFull, l, 1);
@@ -775,9 +806,6 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           finish_lse(p, idx, r);
         }
       }
-      tc_wait(bar(sh.o_done), (gi - 1) & 1, gave_up, p.status);
-      tc_after();
-      float* const half = reinterpret_cast<float*>(mem + T::oP) + c0 * D;  // the weights' memory, read by now
       if (kHalves == 2 && t >= D) {
 #pragma unroll 1
         for (int c = 0; c < NH; c += 4) {
@@ -804,7 +832,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           tc_sum_parts<NR>(tO + c, o);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int idx = sh.idx[c0 + c + j];
+            const int idx = rows.idx[c0 + c + j];
             if (kHalves == 2) o[j] += half[(c + j) * D + d];
             const float2 r = sh.coef[c0 + c + j];
             float y = o[j] * r.x;
