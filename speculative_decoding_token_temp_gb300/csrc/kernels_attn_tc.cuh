@@ -50,13 +50,16 @@ constexpr float kOver = 8.f;           // ... and is renewed when one would pass
 
 template <int D, int NR>
 struct TcShape {
+  // Columns that the rows stand in: each half of the softmax warps has half of them, from a multiple of 8 on (a weights'
+  // store and a load of tensor memory take 8); of 24 rows in 32 columns 4 a half are computed by the MMAs and read by none.
+  static constexpr int NH = NR / 2, NC = 2 * ((NH + 7) / 8 * 8);
   static constexpr int kHalves = 128 / D;                    // token halves stacked on the lanes of O^T
-  static constexpr int kNK = D == 64 ? 5 : NR <= 32 ? 3 : 2; // tiles of keys in the ring
+  static constexpr int kNK = D == 64 ? 5 : NC <= 32 ? 3 : 2; // tiles of keys in the ring
   static constexpr int kNV = D == 64 ? 5 : 2;                // tiles of values
   static constexpr int kTileBytes = kTile * D;               // codes of one operand
   static constexpr int kChunk = kTile * 16;                  // 16 columns of the weights' parts: a 16-byte row a token
-  static constexpr int kP = 3 * NR / 16 * kChunk;
-  static constexpr int kQ = 2 * NR * D;                      // high and low parts of the queries
+  static constexpr int kP = 3 * NC / 16 * kChunk;
+  static constexpr int kQ = 2 * NC * D;                      // high and low parts of the queries
   // offsets from a 1024-byte boundary
   static constexpr int oK = 0;
   static constexpr int oV = oK + kNK * kTileBytes;
@@ -66,7 +69,7 @@ struct TcShape {
   static constexpr int kSmem = oE + kNK * 2 * kTile + 1024;
   static constexpr uint64_t kLayoutD = D == 128 ? 2 : 4;     // descriptor: 128- or 64-byte swizzle
   // tensor memory: scores of the two parts, then the values' sums of the three
-  static constexpr int cO = 2 * NR, cHalf = 3 * NR;
+  static constexpr int cO = 2 * NC, cHalf = 3 * NC;
   static_assert(cO + kHalves * cHalf <= 256, "two blocks share the tensor memory");
   static_assert((kHalves == 2 ? NR * D * 4 : 0) + NR * D * 2 <= kP, "sums pass through the weights' memory");
   static_assert(kSmem <= 107 * 1024, "two blocks share the shared memory");
@@ -222,12 +225,12 @@ __device__ __forceinline__ void tc_st4(uint32_t a, const uint32_t (&r)[4]) {
                : "memory");
 }
 // Four columns of the values' sums: the three parts' accumulators joined.
-template <int NR>
+template <int NC>
 __device__ __forceinline__ void tc_sum_parts(uint32_t at, float (&o)[4]) {
   uint32_t a[4], b[4], c[4];
   tc_ld4(at, a);
-  tc_ld4(at + NR, b);
-  tc_ld4(at + 2 * NR, c);
+  tc_ld4(at + NC, b);
+  tc_ld4(at + 2 * NC, c);
   tc_wait_ld();
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -254,7 +257,7 @@ struct TcShared {
   alignas(16) float delta[NR];      // its last change, and 2^that
   alignas(16) float factor[NR];
   float red[4][NR];                 // of the warps of a token each: maxima of the columns
-  float2 coef[NR];                  // weights of a row's values and of the prefix's part
+  alignas(16) float coef[2][NR];    // weights of a row's values and of the prefix's part
 };
 
 // Queries of a stretch staged for the scores' MMA: TPR threads a row find its power of two
@@ -263,7 +266,7 @@ struct TcShared {
 // of the instruction caches.)
 template <int D, int NR>
 __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g, typename TcShared<D, NR>::Rows& rows, uint8_t* q, int t) {
-  constexpr int TPR = NR == 48 ? 4 : 8, E = D / TPR;
+  constexpr int TPR = NR > 32 ? 4 : 8, E = D / TPR, NH = TcShape<D, NR>::NH, NC = TcShape<D, NR>::NC;
   const int c = t / TPR, part = t % TPR, f = g.f0 + c;
   if (c < NR) {  // (whole warps)
     const int i = f / p.G, hq = g.h * p.G + f - i * p.G, idx = (g.row0 + i) * p.Hq + hq;
@@ -302,7 +305,7 @@ __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g,
       rows.idx[c] = here ? idx : -1;
       rows.neg_m[c] = 0.f;
     }
-    const int rl = NR + c;
+    const int rh = c < NH ? c : c - NH + NC / 2, rl = NC + rh;
 #pragma unroll
     for (int k = 0; k < E / 8; ++k) {
       const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
@@ -322,9 +325,9 @@ __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g,
         lo[j] = narrow4(h[0], h[1]);
       }
       const int at = part * E + k * 8, chunk = at >> 4;
-      const int ch_h = D == 128 ? chunk ^ (c & 7) : chunk ^ ((c >> 1) & 3);
+      const int ch_h = D == 128 ? chunk ^ (rh & 7) : chunk ^ ((rh >> 1) & 3);
       const int ch_l = D == 128 ? chunk ^ (rl & 7) : chunk ^ ((rl >> 1) & 3);
-      *reinterpret_cast<uint2*>(q + c * D + ch_h * 16 + (at & 15)) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(q + rh * D + ch_h * 16 + (at & 15)) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(q + rl * D + ch_l * 16 + (at & 15)) = make_uint2(lo[0], lo[1]);
     }
   }
@@ -472,7 +475,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   } else if (warp == 9) {
     // ---- the MMAs: scores of the next tile, then weighted values of this one ----
     // The whole warp walks the tiles, so that descriptors and addresses stay warp-uniform; one elected lane issues.
-    constexpr uint32_t id_s = mma_idesc(2 * NR, false), id_o = mma_idesc(3 * NR, true);
+    constexpr uint32_t id_s = mma_idesc(2 * T::NC, false), id_o = mma_idesc(3 * T::NC, true);
     constexpr uint64_t hi_d = mma_desc_hi(8 * D, T::kLayoutD);                  // codes and queries: rows of D bytes
     constexpr uint64_t lbo_v = (uint64_t)(kTile / 2 * 64 >> 4) << 16;           // head_dim 64: to the second 64 tokens
     constexpr uint64_t hi_p = mma_desc_hi(T::kChunk, 0) | (uint64_t)(128 >> 4) << 16;  // weights: 8 tokens, then 16 columns on
@@ -531,11 +534,11 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     }
   } else {
     // ---- softmax: thread = token (lane of S^T) and element (lane of O^T), half of the columns ----
-    constexpr int NH = NR / 2;
-    const int t = tid & 127, wl = warp & 3, c0 = (warp >> 2) * NH;
+    constexpr int NH = T::NH, NC = T::NC;
+    const int t = tid & 127, wl = warp & 3, c0 = (warp >> 2) * NH, cc = (warp >> 2) * (NC / 2);  // its first row, first column
     const int half_bar = 2 + (warp >> 2);  // the columns' halves have references of their own and run on their own
     const uint32_t lanes = (uint32_t)(wl * 32) << 16;
-    const uint32_t tS = tmem + lanes + c0, tO = tmem + lanes + T::cO + (kHalves == 2 && wl >= 2 ? T::cHalf : 0) + c0;
+    const uint32_t tS = tmem + lanes + cc, tO = tmem + lanes + T::cO + (kHalves == 2 && wl >= 2 ? T::cHalf : 0) + cc;
     uint8_t* const pw = mem + T::oP + t * 16;
     const float nan = __int_as_float(0x7fffffff), ninf = __int_as_float(kNegInfBits);
     int gi = 0;
@@ -619,11 +622,15 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         tc_after();
         f2 x[NH / 2];
         float most = ninf;
-        uint32_t hi[NH / 8][8], lo[NH / 8][8];
+        uint32_t hi[(NH + 7) / 8][8], lo[(NH + 7) / 8][8];
 #pragma unroll
         for (int i = 0; i < NH / 8; ++i) {
           tc_ld8(tS + i * 8, hi[i]);
-          tc_ld8(tS + NR + i * 8, lo[i]);
+          tc_ld8(tS + NC + i * 8, lo[i]);
+        }
+        if (NH % 8) {
+          tc_ld4(tS + NH / 8 * 8, reinterpret_cast<uint32_t(&)[4]>(hi[NH / 8]));
+          tc_ld4(tS + NC + NH / 8 * 8, reinterpret_cast<uint32_t(&)[4]>(lo[NH / 8]));
         }
         tc_wait_ld();
 #pragma unroll
@@ -708,13 +715,13 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
               if (f[0] == 1.f && f[1] == 1.f && f[2] == 1.f && f[3] == 1.f) continue;  // (the same for all threads of a warp)
               uint32_t o[3][4];
 #pragma unroll
-              for (int part = 0; part < 3; ++part) tc_ld4(tO + part * NR + c, o[part]);
+              for (int part = 0; part < 3; ++part) tc_ld4(tO + part * NC + c, o[part]);
               tc_wait_ld();
 #pragma unroll
               for (int part = 0; part < 3; ++part) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[part][j] = __float_as_uint(__uint_as_float(o[part][j]) * f[j]);
-                tc_st4(tO + part * NR + c, o[part]);
+                tc_st4(tO + part * NC + c, o[part]);
               }
             }
             tc_wait_st();
@@ -728,6 +735,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           uint32_t part[3][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
+            if (c + 4 * j >= NH) break;
             uint32_t h[2], w[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -746,8 +754,12 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           }
 #pragma unroll
           for (int k3 = 0; k3 < 3; ++k3) {
-            const int col = k3 * NR + c0 + c;
-            *reinterpret_cast<uint2*>(pw + (col >> 4) * T::kChunk + (col & 8)) = make_uint2(part[k3][0], part[k3][1]);
+            const int col = k3 * NC + cc + c;
+            uint8_t* at = pw + (col >> 4) * T::kChunk + (col & 8);
+            if (c + 4 < NH)
+              *reinterpret_cast<uint2*>(at) = make_uint2(part[k3][0], part[k3][1]);
+            else
+              *reinterpret_cast<uint32_t*>(at) = part[k3][0];
           }
         }
         fence_async();
@@ -802,7 +814,8 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           slot[NR + col] = l;
         } else if (idx >= 0) {
           const Coef r = row_coef(lse, m, l, g.bad);
-          sh.coef[col] = make_float2(r.a, r.b);
+          sh.coef[0][col] = r.a;
+          sh.coef[1][col] = r.b;
           finish_lse(p, idx, r);
         }
       }
@@ -810,7 +823,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
 #pragma unroll 1
         for (int c = 0; c < NH; c += 4) {
           float o[4];
-          tc_sum_parts<NR>(tO + c, o);
+          tc_sum_parts<NC>(tO + c, o);
 #pragma unroll
           for (int j = 0; j < 4; ++j) half[(c + j) * D + d] = o[j];
         }
@@ -821,24 +834,35 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
 #pragma unroll 1
         for (int c = 0; c < NH; c += 4, slot += 4 * D) {
           float o[4];
-          tc_sum_parts<NR>(tO + c, o);
+          tc_sum_parts<NC>(tO + c, o);
 #pragma unroll
           for (int j = 0; j < 4; ++j) slot[j * D] = kHalves == 2 ? o[j] + half[(c + j) * D + d] : o[j];
         }
       } else if (t < D) {
 #pragma unroll
         for (int c = 0; c < NH; c += 4) {
+          const int4 i4 = *reinterpret_cast<const int4*>(&rows.idx[c0 + c]);
+          if (i4.x < 0) break;  // (past the last row)
+          const int idx[4] = {i4.x, i4.y, i4.z, i4.w};
+          const float4 a4 = *reinterpret_cast<const float4*>(&sh.coef[0][c0 + c]);
+          const float a[4] = {a4.x, a4.y, a4.z, a4.w};
           float o[4];
-          tc_sum_parts<NR>(tO + c, o);
+          tc_sum_parts<NC>(tO + c, o);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int idx = rows.idx[c0 + c + j];
             if (kHalves == 2) o[j] += half[(c + j) * D + d];
-            const float2 r = sh.coef[c0 + c + j];
-            float y = o[j] * r.x;
-            if (r.y != 0.f) y = fmaf(pre[c + j], r.y, y);
-            if (idx >= 0) store_out<uint16_t, D>(p, idx, d, y);
+            o[j] *= a[j];
           }
+          if (p.pre_o != nullptr) {
+            const float4 b4 = *reinterpret_cast<const float4*>(&sh.coef[1][c0 + c]);
+            const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (b[j] != 0.f) o[j] = fmaf(pre[c + j], b[j], o[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (idx[j] >= 0) store_out<uint16_t, D>(p, idx[j], d, o[j]);
         }
       }
       tc_before();

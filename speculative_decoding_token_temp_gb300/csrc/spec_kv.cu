@@ -175,12 +175,12 @@ struct AttnLayout {
 long long rows_of(const spec_attn_batch& g) { return (long long)g.total_draft + g.B; }
 
 // Rows of a row block of the tensor-core kernel, for `flat` rows that share keys: as few
-// blocks as hold them, each as small as that allows in steps of 16 (the MMAs' columns, and
-// what a softmax thread does, are in proportion). A block's accumulators take 5 columns of
-// tensor memory a row, 8 with head_dim 64, of 256 a group.
+// blocks as hold them, each as small as that allows in steps of 8 from 16 on (what a softmax
+// thread does is in proportion). A block's accumulators take 5 columns of tensor memory a
+// row, 8 with head_dim 64, of 256 a group.
 int tc_rows(long long flat, int head_dim) {
   const long long per = cdiv(flat, cdiv(flat, head_dim == 64 ? 32 : 48));
-  return (int)(cdiv(per, 16) * 16);
+  return per <= 16 ? 16 : (int)(cdiv(per, 8) * 8);
 }
 
 AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype) {
@@ -397,7 +397,9 @@ cudaError_t pass_tc(const AttnParams& p, long long grid, const Maps& m, cudaStre
 template <int D>
 cudaError_t pass_tc_nr(int nr, const AttnParams& p, long long grid, const Maps& m, cudaStream_t s) {
   if (nr == 16) return pass_tc<D, 16>(p, grid, m, s);
+  if (nr == 24) return pass_tc<D, 24>(p, grid, m, s);
   if constexpr (D == 128) {
+    if (nr == 40) return pass_tc<D, 40>(p, grid, m, s);
     if (nr == 48) return pass_tc<D, 48>(p, grid, m, s);
   }
   return pass_tc<D, 32>(p, grid, m, s);
