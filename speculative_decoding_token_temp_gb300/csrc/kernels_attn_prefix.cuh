@@ -14,18 +14,10 @@
 //
 // A block holds 256 rows as two tiles of 128 and walks the keys in tiles of 128 tokens:
 // S = Q K^T and O += P V, lanes = rows. Two threads share a row, half of a tile's tokens
-// each; the loads of scores find their maxima, and only where a row's passes its reference
-// by 2^15 do the two threads exchange them. Each writes its weights over its own scores.
-// While one group makes weights, the tensor pipe sums the other's values and then computes
-// its next scores: MMAs of one block run in the order they are issued, so a group's next
-// scores may overwrite its weights without a wait.
-//
-// What bounds it (9216 rows a kv head behind 16384 tokens, head_dim 128, 8 kv heads): the
-// tensor pipe and the shared memory that feeds it. 256 rows x 128 tokens take 2820 clocks, of
-// which the MMAs are 2048; the scores' MMAs read both operands from shared memory at its
-// full rate (the weights' read one), beside the copies into it. A softmax group's own work is
-// 1110 clocks, 512 of them the exponentials. Two groups use all 512 columns of tensor
-// memory, so there is no room for scores ahead or for queries there.
+// each, so maxima and sums need one other thread, and that only when the reference is
+// renewed (a row's largest score passes it by 2^15). While one group makes weights, the tensor pipe sums the other's
+// values and then computes its next scores: MMAs of one block run in the order they are
+// issued, so a group's next scores may overwrite its weights without a wait.
 #pragma once
 
 #include "kernels_attn_tc.cuh"
@@ -156,17 +148,6 @@ __device__ __forceinline__ void tc_ld32(uint32_t a, float* r) {
         "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]),
         "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]),
         "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-      : "r"(a));
-}
-// The same with the largest of the 32, which the load finds (a NaN is passed over).
-__device__ __forceinline__ void tc_ld32_max(uint32_t a, float* r, float& top) {
-  asm volatile(
-      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]),
-        "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]),
-        "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31]), "=f"(top)
       : "r"(a));
 }
 __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t* r) {
@@ -316,7 +297,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             const uint32_t b = (base + T::oV + st * T::kTileBytes) >> 4;
 #pragma unroll
             for (int s = 0; s < kTile / 16; ++s)
-              mma_f16_ts(tm + T::cO + w * 128, tm + T::cS + w * 128 + s * 8 + (s < 4 ? 0 : 32), hi | lbo_v | (b + s * (2048 >> 4)), id_o,
+              mma_f16_ts(tm + T::cO + w * 128, tm + T::cS + w * 128 + s * 8, hi | lbo_v | (b + s * (2048 >> 4)), id_o,
                          s > 0 || k > 0);
             if (k + 1 < n)
               scores(w, gi + 1);
@@ -387,19 +368,21 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           tc_wait(bar(sh.s_full[w]), tiles_done & 1, gave_up, p.status);
           tc_after();
           float s[64];
-          float top, top2;
-          tc_ld32_max(tS + half * 64, s, top);
-          tc_ld32_max(tS + half * 64 + 32, s + 32, top2);
+          tc_ld32(tS + half * 64, s);
+          tc_ld32(tS + half * 64 + 32, s + 32);
           tc_wait_ld();
-          top = fmaxf(top, top2);
           if (valid < 64) {
-            top = ninf;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
+            for (int i = 0; i < 64; ++i)
               if (i >= valid) s[i] = ninf;
-              top = fmaxf(top, s[i]);
-            }
           }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i = 4; i < 64; i += 4)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[i + j]);
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // (the barrier also stands between both halves' loads and the weights that overwrite scores)
           if (bar_or(pair_bar, 64, k == 0 || fmaf(top, p.c, E - m) > kOverP)) {
             sh.top[w][half][t] = top;
             bar_sync(pair_bar, 64);
@@ -437,7 +420,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
               sum[(j >> 1) & 3] = add2(sum[(j >> 1) & 3], pack(a, b));
               h[j / 2] = half2_of(a, b);
             }
-            tc_st16(tS + half * 64 + i / 2, h);  // over this thread's own scores
+            tc_st16(tS + half * 32 + i / 2, h);
           }
           tc_wait_st();
           tc_before();
