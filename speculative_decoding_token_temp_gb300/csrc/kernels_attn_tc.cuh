@@ -31,8 +31,10 @@
 // tile's weights are made. Two blocks share an SM, so that one's ends and waits are covered
 // by the other.
 //
-// What bounds it: the cache's bytes. A tile is 32 KB of codes (head_dim 128), 64 KB of them
-// in flight a block.
+// What bounds it: the cache's bytes where stretches are long (a tile, 32 KB of codes with
+// head_dim 128, takes an SM 1270 clocks: 256 sequences x 1 row to 1-8192 tokens 328 us, 98 %
+// of a copy's rate), else the instructions of a stretch's beginning and end, as many as three
+// tiles': 64 x 6 rows to 6-4096 tokens 57 us (DRAM 64 %).
 #pragma once
 
 #include <cuda.h>
