@@ -249,7 +249,9 @@ struct TcShared {
   int gave_up;
   uint32_t bad_pages[T::kNK];
   uint64_t sees[SPEC_MAX_TREE_NODES];
-  uint8_t nan_code[kTile];          // of a tile with masked places: the token's values hold a NaN code
+  // Of a tile with masked places: the token's values hold a NaN code. Of the tile before as well: the second half of the
+  // warps may still read that when the first half comes to this one, while the one before it is behind both (o_done).
+  uint8_t nan_code[2][kTile];
   struct Rows {                     // of a stretch's rows
     alignas(16) float rq[NR];       // the factor of the scores: scale * log2(e) * the row's power of two
     alignas(16) int row[NR];        // query row of a flat row
@@ -597,10 +599,10 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
 #pragma unroll 1
               for (int ch = 0; ch < D / 16; ++ch) src[(ch ^ t) & (D / 16 - 1)] = make_uint4(0, 0, 0, 0);
             }
-            sh.nan_code[t] = nan_here;
+            sh.nan_code[gi & 1][t] = nan_here;
           }
           bar_sync(1, kTcSoft);
-          hurt |= sh.nan_code[t] != 0;
+          hurt |= sh.nan_code[gi & 1][t] != 0;
         }
         const bool fine = live && !hurt;
         const float ks = !live ? 0.f : hurt ? nan : exp_value(kb);

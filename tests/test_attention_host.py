@@ -1,0 +1,55 @@
+"""What the attention kernels' correctness rests on and no GPU is needed for: the order of hand-overs between warps, the
+parts that weights are split into, the binding's own checks."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "speculative_decoding_token_temp_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+def orders(buffers, tiles):
+    """Every order in which the two halves of the softmax warps may pass through `tiles` masked tiles; True when each read of
+    the flags (`buffers` of them, by the tile's number) finds its own tile's.
+
+    A half's steps in tile i: the first one writes the flags, both meet, the second one reads them, each waits until the
+    products of tile i - 1 are summed (which follows both halves' weights of that tile), each hands over its weights."""
+    first = [(what, i) for i in range(tiles) for what in ("write", "meet", "wait", "hand")]
+    second = [(what, i) for i in range(tiles) for what in ("meet", "read", "wait", "hand")]
+    handed = {i: (first.index(("hand", i)), second.index(("hand", i))) for i in range(tiles)}
+    todo, seen = [(0, 0, (None,) * buffers)], set()
+    while todo:
+        state = todo.pop()
+        if state in seen:
+            continue
+        seen.add(state)
+        a, b, flags = state
+
+        def free(steps, at):
+            what, i = steps[at]
+            return what != "wait" or i == 0 or (a > handed[i - 1][0] and b > handed[i - 1][1])
+
+        if a < len(first) and b < len(second) and first[a][0] == second[b][0] == "meet":
+            todo.append((a + 1, b + 1, flags))
+        if a < len(first) and first[a][0] != "meet" and free(first, a):
+            what, i = first[a]
+            todo.append((a + 1, b, tuple(i if what == "write" and k == i % buffers else f for k, f in enumerate(flags))))
+        if b < len(second) and second[b][0] != "meet" and free(second, b):
+            what, i = second[b]
+            if what == "read" and flags[i % buffers] != i:
+                return False
+            todo.append((a, b + 1, flags))
+    return True
+
+
+def test_nan_flags_of_masked_tiles_are_read_before_they_are_written_again():
+    text = source("kernels_attn_tc.cuh")
+    declared = re.search(r"uint8_t nan_code((?:\[\w+\])+);", text).group(1)
+    buffers = 1 if declared == "[kTile]" else int(re.match(r"\[(\d+)\]\[kTile\]$", declared).group(1))
+    uses = re.findall(r"sh\.nan_code((?:\[[^\]]*\])+)", text)
+    assert len(uses) == 2 and all(u == ("[t]" if buffers == 1 else f"[gi & {buffers - 1}][t]") for u in uses)
+    assert orders(buffers, 5)
+    assert not orders(1, 3)  # (one set of flags would not do)
