@@ -280,6 +280,13 @@ __device__ __forceinline__ void finish_lse(const AttnParams& p, long long idx, c
     p.lse[idx] = r.lse2 * 0.69314718055994530942f;
 }
 
+// What the values' sums are kept smaller by. Values may be as large as fp32 holds, so their
+// sum under weights of up to 1, before it is divided by the weights', may not be: in the
+// 32-bit kernel 2^20 tokens of the largest value stay in range, and the smallest (448 * 2^-100)
+// keep 37 bits. The tensor-core kernels' weights hold the values' exponents.
+template <typename E>
+constexpr float kSumUnit = sizeof(E) == 4 ? 1048576.f : 1.f;
+
 // A slot of the workspace: NR maxima, NR sums, NR x D values.
 template <int NR, int D>
 __device__ __forceinline__ float* slot_of(const AttnParams& p, int s) {
@@ -393,7 +400,8 @@ __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(AttnParams p,
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-  const Coef co = row_coef(pre_lse, mu, l, r.bad != 0);
+  Coef co = row_coef(pre_lse, mu, l, r.bad != 0);
+  co.a *= kSumUnit<E>;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     float x = acc[k] * co.a;
@@ -533,7 +541,7 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
         const Sight sight = sight_of(p.mask, s_sees, g.rows, g.len, t);
 #pragma unroll
         for (int c = 0; c < NR; ++c) ss[c][tid] = sight((g.f0 + c) / p.G) ? s[c] * ke : ninf;
-        sx[tid] = ve;
+        sx[tid] = ve * (1.f / kSumUnit<E>);
       }
       __syncthreads();
 #pragma unroll
@@ -603,7 +611,8 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
         slot[2 * NR + e] = v;
       } else if (f < g.rows * p.G) {
         const long long idx = (long long)(g.row0 + f / p.G) * p.Hq + g.h * p.G + f % p.G;
-        const Coef r = row_coef(p.pre_o != nullptr ? __ldcg(p.pre_lse + idx) : ninf, sm[c] == ninf ? 0.f : sm[c], sl[c], g.bad);
+        Coef r = row_coef(p.pre_o != nullptr ? __ldcg(p.pre_lse + idx) : ninf, sm[c] == ninf ? 0.f : sm[c], sl[c], g.bad);
+        r.a *= kSumUnit<E>;
         finish<E, D>(p, idx, d, v, r);
         if (d == 0) finish_lse(p, idx, r);
       }
