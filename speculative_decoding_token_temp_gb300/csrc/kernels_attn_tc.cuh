@@ -5,17 +5,21 @@
 // the 128-lane side, and the few rows on the other: S^T = K q^T (lanes = tokens) and
 // O^T = V^T P^T (lanes = elements), so that few rows cost few columns instead of a
 // 128-row tile that is mostly empty. Both run on the cache's codes as they are
-// (kind::f8f6f4, e4m3 by e4m3): nothing is widened on the way, and a tile crosses shared
-// memory once in and once out for each product. What is not 8 bits wide is split into
-// e4m3 parts that stand side by side as columns of one MMA, and whose products are added:
+// (kind::f8f6f4, e4m3 as the first operand): nothing is widened on the way, and a tile
+// crosses shared memory once in and once out for each product. What is not 8 bits wide is
+// split into 8-bit parts that stand side by side as columns of one MMA, and whose products
+// are added:
 //
-//   queries  a bf16 query is, within its row's power of two, exactly the sum of two parts
-//            (8 significant bits = 4 + 4; elements below 2^-8 of the row's largest keep an
-//            absolute 2^-18 of it);
-//   weights  a weight rounded to f16 (11 bits) is exactly the sum of three parts (each the
-//            rest of the ones before, scaled by 16 and 256 in columns of its own), down to
-//            2^-18, where the largest weights of a row stand between 2^3 and 2^8: what is
-//            dropped of a flat tail is below 2^-21 of the largest weight a token.
+//   queries  a bf16 query is, within its row's power of two, exactly the sum of two e4m3
+//            parts (8 significant bits = 4 + 4; elements below 2^-8 of the row's largest
+//            keep an absolute 2^-18 of it);
+//   weights  a weight is rounded to f16, and every f16 number up to 2^15 is exactly the sum
+//            of three e5m2 parts (each the rest of the ones before, scaled by 16 and 256 in
+//            columns of its own: 11 bits are 3 + 4 + 4 with the rests' signs, and the last
+//            part's smallest step is f16's, 2^-24). The largest weights of a row stand between
+//            2^10 and 2^15: a weight keeps f16's 11 bits down to 2^-24 of the largest, then
+//            an absolute 2^-35 of it. (e4m3 parts, whose range is short, end 2^-21 below the
+//            largest; a long flat tail under one dominant token was lost there.)
 //
 //   Exponents: a key's is a factor of its token's scores, one lane's constant; a value's is
 //   added to the score before the exponential (weights are 2^(x + e - m)), so that the
@@ -23,8 +27,8 @@
 //   differ much in size; the sum takes it out again (2^-e).
 //
 // Eight warps do the softmax: a thread is a token and half of the rows, whose weights sit
-// in its registers. The maximum over tokens, which would cross lanes, is needed only when a score
-// exceeds the row's reference by 2^8 (the first tile of a stretch, then rarely): the
+// in its registers. The maximum over tokens, which would cross lanes, is needed only when a weight
+// would pass 2^15 (the first tile of a stretch, then rarely): the
 // reference is not the maximum itself but anything that keeps the weights in range. One
 // warp keeps rings of key and value tiles filled (a TMA load a page and operand; pages
 // shorter than a tile make several), one issues the MMAs: the next tile's scores while this
@@ -47,8 +51,9 @@ constexpr int kTcThreads = 320;        // eight softmax warps, one for copies, o
 constexpr int kTcSoft = 256;
 constexpr int kSegRing = 8;            // more stretches than tiles can be in the rings
 constexpr int kTcPollLimit = 1 << 18;  // bounded waits (SPEC_DEV_TIMEOUT): about a second
-constexpr float kTop = 3.f;            // a fresh reference puts the largest weight at 2^3 ...
-constexpr float kOver = 8.f;           // ... and is renewed when one would pass 2^8 (e4m3 ends at 448)
+constexpr float kTop = 10.f;           // a fresh reference puts the largest weight at 2^10 ...
+constexpr float kOver = 15.f;          // ... and is renewed when one would pass 2^15 (f16 and e5m2 end just below 2^16)
+constexpr int kSumShift = 6;           // sums of 2^(x - m) are kept 2^6 smaller: values of exponent -100 leave them in range
 
 template <int D, int NR>
 struct TcShape {
@@ -84,9 +89,9 @@ struct TcShape {
 __host__ __device__ constexpr uint64_t mma_desc_hi(uint32_t sbo, uint64_t layout) {
   return (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | layout << 61;
 }
-// Instruction descriptor: fp32 accumulator, e4m3 operands, M = 128.
-__host__ __device__ constexpr uint32_t mma_idesc(int n, bool mn_major) {
-  return 1u << 4 | (mn_major ? 3u << 15 : 0u) | (uint32_t)(n >> 3) << 17 | 8u << 24;
+// Instruction descriptor: fp32 accumulator, e4m3 by e4m3 (or e5m2), M = 128.
+__host__ __device__ constexpr uint32_t mma_idesc(int n, bool mn_major, bool b_e5m2) {
+  return 1u << 4 | (b_e5m2 ? 1u << 10 : 0u) | (mn_major ? 3u << 15 : 0u) | (uint32_t)(n >> 3) << 17 | 8u << 24;
 }
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -208,12 +213,27 @@ __device__ __forceinline__ uint32_t narrow4(uint32_t h0, uint32_t h1, uint32_t& 
       : "r"(h0), "r"(h1));
   return r;
 }
-// 16 * (a - b) of f16 pairs (exact where b is a rounded to a part's 4 bits)
+// The same to e5m2 codes.
+__device__ __forceinline__ uint32_t narrow4_e5(uint32_t h0, uint32_t h1) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e5m2x2.f16x2 a, %1;\n\tcvt.rn.satfinite.e5m2x2.f16x2 b, %2;\n\t"
+      "mov.b32 %0, {a, b};\n\t}"
+      : "=r"(r)
+      : "r"(h0), "r"(h1));
+  return r;
+}
+__device__ __forceinline__ uint32_t narrow4_e5(uint32_t h0, uint32_t h1, uint32_t& w0, uint32_t& w1) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e5m2x2.f16x2 a, %3;\n\tcvt.rn.satfinite.e5m2x2.f16x2 b, %4;\n\t"
+      "mov.b32 %0, {a, b};\n\tcvt.rn.f16x2.e5m2x2 %1, a;\n\tcvt.rn.f16x2.e5m2x2 %2, b;\n\t}"
+      : "=r"(r), "=&r"(w0), "=r"(w1)
+      : "r"(h0), "r"(h1));
+  return r;
+}
+// 16 * (a - b) of f16 pairs: exact where b is a rounded to a part's 3 bits (the difference first: 16 a may pass f16's range)
 __device__ __forceinline__ uint32_t rest16(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("{\n\t.reg .b32 t;\n\tmul.rn.f16x2 t, %1, %3;\n\tfma.rn.f16x2 %0, %2, %4, t;\n\t}"
-      : "=r"(r)
-      : "r"(a), "r"(b), "r"(0x4c004c00u), "r"(0xcc00cc00u));
+  asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}" : "=r"(r) : "r"(a), "r"(b), "r"(0x4c004c00u));
   return r;
 }
 
@@ -479,7 +499,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   } else if (warp == 9) {
     // ---- the MMAs: scores of the next tile, then weighted values of this one ----
     // The whole warp walks the tiles, so that descriptors and addresses stay warp-uniform; one elected lane issues.
-    constexpr uint32_t id_s = mma_idesc(2 * T::NC, false), id_o = mma_idesc(3 * T::NC, true);
+    constexpr uint32_t id_s = mma_idesc(2 * T::NC, false, false), id_o = mma_idesc(3 * T::NC, true, true);
     constexpr uint64_t hi_d = mma_desc_hi(8 * D, T::kLayoutD);                  // codes and queries: rows of D bytes
     constexpr uint64_t lbo_v = (uint64_t)(kTile / 2 * 64 >> 4) << 16;           // head_dim 64: to the second 64 tokens
     constexpr uint64_t hi_p = mma_desc_hi(T::kChunk, 0) | (uint64_t)(128 >> 4) << 16;  // weights: 8 tokens, then 16 columns on
@@ -539,6 +559,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
   } else {
     // ---- softmax: thread = token (lane of S^T) and element (lane of O^T), half of the columns ----
     constexpr int NH = T::NH, NC = T::NC;
+    constexpr float kSumScale = 1.f / (1 << kSumShift);
     const int t = tid & 127, wl = warp & 3, c0 = (warp >> 2) * NH, cc = (warp >> 2) * (NC / 2);  // its first row, first column
     const int half_bar = 2 + (warp >> 2);  // the columns' halves have references of their own and run on their own
     const uint32_t lanes = (uint32_t)(wl * 32) << 16;
@@ -607,7 +628,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         const bool fine = live && !hurt;
         const float ks = !live ? 0.f : hurt ? nan : exp_value(kb);
         const float ev = fine ? (float)((int)vb - kExpBias) : 0.f;
-        const float isv = fine ? __int_as_float((2 * kExpBias - (int)vb) << 23) : 1.f;
+        const float isv = fine ? __int_as_float((2 * kExpBias - (int)vb) << 23) * kSumScale : 1.f;
         const f2 ks2 = pack(ks, ks), ev2 = pack(ev, ev), isv2 = pack(isv, isv);
         uint32_t sight = ~0u;  // bit c: the row of column c0 + c sees this token
         if (masked) {
@@ -751,10 +772,10 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
               l = fma2(pack(a, b), isv2, l);
               h[i] = half2_of(a, b);
             }
-            part[0][j] = narrow4(h[0], h[1], w[0], w[1]);
+            part[0][j] = narrow4_e5(h[0], h[1], w[0], w[1]);
             h[0] = rest16(h[0], w[0]), h[1] = rest16(h[1], w[1]);
-            part[1][j] = narrow4(h[0], h[1], w[0], w[1]);
-            part[2][j] = narrow4(rest16(h[0], w[0]), rest16(h[1], w[1]));
+            part[1][j] = narrow4_e5(h[0], h[1], w[0], w[1]);
+            part[2][j] = narrow4_e5(rest16(h[0], w[0]), rest16(h[1], w[1]));
           }
 #pragma unroll
           for (int k3 = 0; k3 < 3; ++k3) {
@@ -807,7 +828,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
         const int col = tid >> 2, idx = rows.idx[col];
         const float lse = whole && idx >= 0 && p.pre_o != nullptr ? __ldcg(p.pre_lse + idx) : ninf;
         float l = 0.f;
-        const float m = -rows.neg_m[col];
+        const float m = (float)kSumShift - rows.neg_m[col];  // what sums and values, both scaled so, are relative to
 #pragma unroll
         for (int i = 0; i < kPer / 4; ++i) l += part[col * kPer + ((i + col) * 4 & (kPer - 1)) + (tid & 3)];
         l += __shfl_xor_sync(kFull, l, 1);
@@ -818,7 +839,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           slot[NR + col] = l;
         } else if (idx >= 0) {
           const Coef r = row_coef(lse, m, l, g.bad);
-          sh.coef[0][col] = r.a;
+          sh.coef[0][col] = r.a * kSumScale;
           sh.coef[1][col] = r.b;
           finish_lse(p, idx, r);
         }
@@ -840,7 +861,7 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
           float o[4];
           tc_sum_parts<NC>(tO + c, o);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) slot[j * D] = kHalves == 2 ? o[j] + half[(c + j) * D + d] : o[j];
+          for (int j = 0; j < 4; ++j) slot[j * D] = (kHalves == 2 ? o[j] + half[(c + j) * D + d] : o[j]) * kSumScale;
         }
       } else if (t < D) {
 #pragma unroll

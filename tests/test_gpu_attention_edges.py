@@ -1,5 +1,5 @@
-"""spec_attention where single places decide: NaN codes beside what rows see, over several masked tiles; many tokens of
-the smallest and largest values."""
+"""spec_attention where single places decide: NaN codes beside what rows see, over several masked tiles; one dominant
+token before a long flat tail; many tokens of the smallest and largest values."""
 import numpy as np
 import pytest
 import torch
@@ -31,6 +31,40 @@ def test_nan_codes_past_the_end_of_rounds_over_several_tiles(dev, dim, rows, len
     for _ in range(30):
         got = c.call()["o"]
         assert torch.equal(torch.nan_to_num(got, nan=-1e30), torch.nan_to_num(want, nan=-1e30))
+
+
+@pytest.mark.parametrize("dtype,dim,way", [("bf16", 128, "own"), ("bf16", 64, "own"), ("f32", 64, "own"), ("bf16", 64, "prefix")])
+@pytest.mark.parametrize("tail", [2000, 16300])
+@pytest.mark.parametrize("place", ["first", "last"])
+def test_flat_tail_under_one_dominant_token(dev, dtype, dim, way, tail, place):
+    """One token whose weight is 2^20.9 to 2^24 times that of each of the others, whose values are one in every element; its
+    own are one in the first half of the elements, zero in a quarter, 0.01 in the last. Each of 400 sequences reads the same
+    pages, so that every stretch that a block works on is long. The bound is the one of all other cases (kv_util.bounds)."""
+    n, page, B = tail + 1, 256, 400
+    depth = np.array([20.9, 21.0, 21.1, 22.0, 23.0, 24.0])
+    pages = -(-n // page)
+    at = 0 if place == "first" else n - 1
+    k, v = np.zeros((pages * page, dim)), np.ones((pages * page, dim))
+    k[at, 0] = 1.0
+    v[at, dim // 2:3 * dim // 4] = 0.0
+    v[at, 3 * dim // 4:] = 0.01
+    (kc, ke), (vc, ve) = U.quantise(k), U.quantise(v)
+    cache = api.KVCache(*(torch.from_numpy(c).view(pages, 1, page, dim).to(dev).view(torch.float8_e4m3fn) for c in (kc, vc)),
+                        *(torch.from_numpy(e).view(pages, 1, page).to(dev) for e in (ke, ve)))
+    q = torch.zeros(B, 6, dim, dtype=DT[dtype])
+    q[:, :, 0] = torch.from_numpy(depth).to(DT[dtype])
+    table = np.arange(pages, dtype=np.int32).reshape(1, -1)
+    scale = float(np.float32(np.log(2.0)))
+    ref = U.attention(q[:1].double().numpy(), cache, table, [n], [1], scale=scale)
+    ref = [np.repeat(x, B, axis=1 if i == 3 else 0) for i, x in enumerate(ref)]
+    if way == "own":
+        out = api.spec_attention(q.to(dev), cache, i32(np.repeat(table, B, axis=0), dev), i32([n] * B, dev), gamma=0, scale=scale, want_lse=True)
+    else:
+        assert B * 6 * -(-n // 128) >= 75_000 or tail < 16_000  # (the longer tail: in 128-row tiles of the widened prefix)
+        out = api.spec_attention(q.to(dev), cache, torch.zeros(B, 1, dtype=torch.int32, device=dev), i32([0] * B, dev), gamma=0,
+                                 prefix_table=i32(table[0], dev), prefix_len=n, scale=scale, want_lse=True)
+    assert int(out["device_status"][0]) == 0
+    U.compare(out["o"], out["lse"], ref, DT[dtype], n)
 
 
 def one_value(dev, n, dim, exponent, code, dtype, rows):
