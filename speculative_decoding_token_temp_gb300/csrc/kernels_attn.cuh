@@ -462,7 +462,9 @@ __global__ void __launch_bounds__(128) attn_f32_kernel(AttnParams p) {
         else
           x = __ldg(static_cast<const float*>(p.q) + a);
       }
-      sq[c][d] = x * p.c;
+      // an infinite query's scores would be infinities, and -inf stands for a hidden token: the row is to be NaN
+      x *= p.c;
+      sq[c][d] = fabsf(x) <= 3.402823466e38f ? x : nan;
     }
     if (tid < NR) sm[tid] = ninf, sl[tid] = 0.f;
     float acc[NR][4];

@@ -86,3 +86,20 @@ def test_many_tokens_of_the_smallest_and_largest_values(dev, dtype, exponent, co
     rel = n * 2.0 ** -24 + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24)
     assert ((out["o"].double() / want - 1).abs() <= rel).all()
     assert abs(float(out["lse"][0, 0]) - np.log(n)) <= n * 2.0 ** -24 + 2.0 ** -18
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("tokens,prefix", [(1, 0), (3, 0), (0, 2), (1, 1)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinite_queries_make_their_rows_nan(dev, dtype, what, tokens, prefix, sign):
+    """Whatever the sign of the keys that the infinite element meets, all of them the same here."""
+    c = Case(dev, [tokens], [1], heads=2, kv_heads=1, dim=64, dtype=dtype, prefix=prefix)
+    c.codes[0][..., 9] = 56 if sign > 0 else 184  # 1 and -1
+    c.q[0, 1, 9] = what
+    out = c.call()
+    assert torch.isnan(out["o"][0, 1]).all() and torch.isnan(out["lse"][0, 1])
+    assert torch.isfinite(out["o"][0, 0].float()).all() and torch.isfinite(out["lse"][0, 0])
+    c = Case(dev, [0], [1], heads=2, kv_heads=1, dim=64, dtype=dtype)
+    c.q[0, 1, 9] = what
+    assert (c.call()["o"] == 0).all()  # (it sees nothing)
