@@ -546,7 +546,7 @@ def _rows_view(t: torch.Tensor, name: str, rows: int, heads: int, cache: KVCache
     if t.get_device() != cache.index:
         raise ValueError(f"{name} must be a CUDA tensor on {cache.k.device}, got {t.device}")
     if len(shape) == 4 and shape[0] * shape[1] == rows:
-        if shape[0] > 1 and t.stride(0) != shape[1] * t.stride(1):
+        if shape[0] > 1 and shape[1] > 1 and t.stride(0) != shape[1] * t.stride(1):  # (one row: its stride means nothing)
             raise ValueError(f"{name}: the rows of a [B, rows, heads, dim] view must be evenly spaced")
         t = t.flatten(0, 1)
         shape = t.shape

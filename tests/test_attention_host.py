@@ -2,6 +2,12 @@
 parts that weights are split into, the binding's own checks."""
 import os
 import re
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from speculative_decoding_token_temp_gb300 import api
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "speculative_decoding_token_temp_gb300", "csrc")
 
@@ -53,3 +59,23 @@ def test_nan_flags_of_masked_tiles_are_read_before_they_are_written_again():
     assert len(uses) == 2 and all(u == ("[t]" if buffers == 1 else f"[gi & {buffers - 1}][t]") for u in uses)
     assert orders(buffers, 5)
     assert not orders(1, 3)  # (one set of flags would not do)
+
+
+def host_cache(kv_heads=2, page=16, dim=64, pages=4):
+    """What the binding looks at of a cache, with tensors of the host in the place of the device's (device number -1)."""
+    k = torch.zeros(pages, kv_heads, page, dim, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    return SimpleNamespace(k=k, index=-1, kv_heads=kv_heads, page_size=page, head_dim=dim, num_pages=pages, desc=None)
+
+
+def test_rows_of_one_token_cut_out_of_a_fused_projection_are_taken_as_they_are():
+    cache = host_cache()
+    for B in (1, 2, 5):
+        qkv = torch.randn(B, (4 + 2 * 2) * 64)
+        q = qkv[:, :4 * 64].unflatten(1, (4, 64)).unsqueeze(1)  # [B, 1, 4, 64], whose second stride means nothing
+        assert api._rows_view(q, "q", B, 4, cache) == (qkv.data_ptr(), qkv.shape[1], 64)
+        k = qkv[:, 4 * 64:6 * 64].view(B, 1, 2, 64)
+        assert api._rows_view(k, "k", B, 2, cache) == (qkv.data_ptr() + 4 * 4 * 64, qkv.shape[1], 64)
+    wide = torch.randn(2, 4, 3, 64)
+    assert api._rows_view(wide, "q", 8, 3, cache) == (wide.data_ptr(), 3 * 64, 64)
+    with pytest.raises(ValueError, match="evenly spaced"):
+        api._rows_view(wide[:, :3], "q", 6, 3, cache)
