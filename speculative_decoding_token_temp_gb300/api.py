@@ -10,6 +10,7 @@ Logits are torch.bfloat16 or torch.float32 tensors on a CUDA device, shaped
 [B, gamma+1, V] / [B, gamma, V]."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -465,6 +466,8 @@ def spec_verify_multi(target: torch.Tensor, draft: torch.Tensor, draft_tokens: t
 # the 8-bit key/value cache and the attention over it (include/spec_kv.h)
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_HERE = contextlib.nullcontext()
 _I32, _U8, _E4M3 = torch.int32, torch.uint8, torch.float8_e4m3fn
 _KV_DTYPES = {torch.bfloat16: _lib.SPEC_BF16, torch.float32: _lib.SPEC_F32}
 
@@ -476,6 +479,11 @@ _KV_DTYPES = {torch.bfloat16: _lib.SPEC_BF16, torch.float32: _lib.SPEC_F32}
 def _stream_handle(index: int) -> int:
     """The current stream's handle, without the Stream object where torch gives it directly (2 us a call)."""
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _on(index: int):
+    """The cache's device as the current one: a launch goes to the current device, whatever the stream's."""
+    return _HERE if _current_device() == index else torch.cuda.device(index)
 
 
 def _is(t, dtype, index) -> bool:
@@ -586,9 +594,10 @@ def spec_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, page_table:
         raise TypeError(f"k and v must both be bfloat16 or float32, got {k.dtype} and {v.dtype}")
     r = _kv_rows(cache, page_table, row_seq, row_pos)
     o = {} if out is None else out
-    code = _lib.lib().spec_kv_append(cache.desc, r, dt, *_rows_view(k, "k", r.rows, cache.kv_heads, cache),
-                                     *_rows_view(v, "v", r.rows, cache.kv_heads, cache),
-                                     _status_word(o, device_status, cache), _stream_handle(cache.index))
+    with _on(cache.index):
+        code = _lib.lib().spec_kv_append(cache.desc, r, dt, *_rows_view(k, "k", r.rows, cache.kv_heads, cache),
+                                         *_rows_view(v, "v", r.rows, cache.kv_heads, cache),
+                                         _status_word(o, device_status, cache), _stream_handle(cache.index))
     if code:
         check("spec_kv_append", code)
     return o
@@ -616,7 +625,8 @@ def spec_kv_read(cache: KVCache, page_table: torch.Tensor, row_seq: torch.Tensor
         elif not _is(t, dtype, cache.index) or t.numel() != n:
             _need(t, name, dtype, n, cache.k.device)
         to.append(t.data_ptr())
-    code = _lib.lib().spec_kv_read(cache.desc, r, dt, *to, _status_word(o, device_status, cache), _stream_handle(cache.index))
+    with _on(cache.index):
+        code = _lib.lib().spec_kv_read(cache.desc, r, dt, *to, _status_word(o, device_status, cache), _stream_handle(cache.index))
     if code:
         check("spec_kv_read", code)
     return o
@@ -710,21 +720,22 @@ def spec_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv
         lse = t.data_ptr()
     lib = _lib.lib()
     nbytes = lib.spec_attention_workspace_bytes(g, cache.desc, dt)
-    stream = _stream_handle(cache.index)
-    if workspace is None:
-        if torch.cuda.is_current_stream_capturing():
-            workspace = torch.empty(max(nbytes, 256), dtype=_U8, device=cache.k.device)
-        else:  # calls on two streams may overlap
-            keep = _DEFAULT_WS.get(("cuda", cache.index, stream))
-            if keep is None:
-                keep = _DEFAULT_WS[("cuda", cache.index, stream)] = Workspace()
-            workspace = keep.buf
-            if workspace is None or workspace.numel() < nbytes:
-                workspace = keep.get(nbytes, cache.k.device)
-    else:
-        workspace = _workspace(workspace, nbytes, cache.k.device)
-    code = lib.spec_attention(g, cache.desc, dt, *view, y.data_ptr(), lse, _status_word(o, device_status, cache),
-                              workspace.data_ptr(), workspace.numel(), stream)
+    with _on(cache.index):
+        stream = _stream_handle(cache.index)
+        if workspace is None:
+            if torch.cuda.is_current_stream_capturing():
+                workspace = torch.empty(max(nbytes, 256), dtype=_U8, device=cache.k.device)
+            else:  # calls on two streams may overlap
+                keep = _DEFAULT_WS.get(("cuda", cache.index, stream))
+                if keep is None:
+                    keep = _DEFAULT_WS[("cuda", cache.index, stream)] = Workspace()
+                workspace = keep.buf
+                if workspace is None or workspace.numel() < nbytes:
+                    workspace = keep.get(nbytes, cache.k.device)
+        else:
+            workspace = _workspace(workspace, nbytes, cache.k.device)
+        code = lib.spec_attention(g, cache.desc, dt, *view, y.data_ptr(), lse, _status_word(o, device_status, cache),
+                                  workspace.data_ptr(), workspace.numel(), stream)
     if code:
         check("spec_attention", code)
     return o

@@ -83,3 +83,50 @@ def test_rows_of_one_token_cut_out_of_a_fused_projection_are_taken_as_they_are()
     assert api._rows_view(wide, "q", 8, 3, cache) == (wide.data_ptr(), 3 * 64, 64)
     with pytest.raises(ValueError, match="evenly spaced"):
         api._rows_view(wide[:, :3], "q", 6, 3, cache)
+
+
+class Calls:
+    """In the place of the library: what each call finds as the current device."""
+
+    def __init__(self, device):
+        self.device, self.seen = device, []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.seen.append((name, self.device[0]))
+            return 256 if name.endswith("bytes") else 0
+        return call
+
+
+def test_calls_launch_on_the_caches_device(monkeypatch):
+    device = [3]  # the current one; the cache's is -1
+
+    class guard:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, device[0] = device[0], self.index
+
+        def __exit__(self, *a):
+            device[0] = self.before
+
+    lib, cache = Calls(device), host_cache()
+    monkeypatch.setattr(api, "_current_device", lambda: device[0], raising=False)
+    monkeypatch.setattr(api, "_stream_handle", lambda index: 0)
+    monkeypatch.setattr(torch.cuda, "device", guard)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: device[0] != -1)
+    monkeypatch.setattr(api._lib, "lib", lambda: lib)
+    monkeypatch.setattr(api, "_need", lambda *a, **k: None)
+    table, seq, pos = torch.zeros(3, 1, dtype=torch.int32), *torch.zeros(2, 3, dtype=torch.int32)
+    x = torch.zeros(3, 2, 64)
+    for now in (3, -1):  # (and where it is the current one)
+        device[0] = now
+        api.spec_kv_append(cache, x, x, table, seq, pos)
+        api.spec_kv_read(cache, table, seq, pos, dtype=torch.float32)
+        api.spec_attention(torch.zeros(3, 4, 64), cache, table, seq, gamma=0)
+        api.spec_attention(torch.zeros(3, 4, 64), cache, table, seq, gamma=0, workspace=torch.zeros(256, dtype=torch.uint8))
+        assert [d for name, d in lib.seen if not name.endswith("bytes")] == [-1] * 4, lib.seen
+        assert device[0] == now
+        lib.seen.clear()
+    api._DEFAULT_WS.pop(("cuda", -1, 0), None)
