@@ -78,6 +78,8 @@ def _out(o: dict, name: str, make):
 
 def _workspace(ws, nbytes, device):
     if isinstance(ws, torch.Tensor):
+        if ws.device != device or not ws.is_contiguous():
+            _need(ws, "workspace", device=device)
         if ws.numel() < nbytes:
             raise ValueError(f"workspace has {ws.numel()} bytes, needs {nbytes}")
         return ws

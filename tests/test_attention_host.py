@@ -130,3 +130,16 @@ def test_calls_launch_on_the_caches_device(monkeypatch):
         assert device[0] == now
         lib.seen.clear()
     api._DEFAULT_WS.pop(("cuda", -1, 0), None)
+
+
+def test_workspaces_of_other_places_are_refused(monkeypatch):
+    """Memory of the host, and a view whose elements are fewer than it says: kernels would write outside it."""
+    with pytest.raises(ValueError, match="CUDA"):
+        api._workspace(torch.empty(512, dtype=torch.uint8), 256, torch.device("cuda", 0))
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    with pytest.raises(ValueError, match="contiguous"):
+        api._workspace(torch.empty(1, dtype=torch.uint8).expand(512), 256, torch.device("cpu"))
+    ws = torch.empty(512, dtype=torch.uint8)
+    assert api._workspace(ws, 256, torch.device("cpu")) is ws
+    with pytest.raises(ValueError, match="needs"):
+        api._workspace(ws, 513, torch.device("cpu"))
