@@ -675,7 +675,10 @@ def _attn_batch(q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, pr
         if prefix_table.numel() * cache.page_size < n:
             raise ValueError(f"prefix_table has {prefix_table.numel()} pages, {n} tokens need {-(-n // cache.page_size)}")
         pre = prefix_table.data_ptr()
-    g = _lib.SpecAttnBatch(B, int(gamma), total, cu, H, table[1], page_table.data_ptr(), kv_len.data_ptr(), n, pre,
+    gamma = int(gamma)
+    if n >= 1 << 31 or n < 0 or gamma >= 1 << 31 or gamma < 0:  # (the descriptor's fields would hold something else)
+        raise ValueError(f"gamma and prefix_len must be 32-bit numbers of at least 0, got {gamma} and {n}")
+    g = _lib.SpecAttnBatch(B, gamma, total, cu, H, table[1], page_table.data_ptr(), kv_len.data_ptr(), n, pre,
                            None if par is None else ctypes.cast(par, ctypes.c_void_p),
                            cache.head_dim ** -0.5 if scale is None else float(scale))
     return g, total + B, H, par

@@ -143,3 +143,18 @@ def test_workspaces_of_other_places_are_refused(monkeypatch):
     assert api._workspace(ws, 256, torch.device("cpu")) is ws
     with pytest.raises(ValueError, match="needs"):
         api._workspace(ws, 513, torch.device("cpu"))
+
+
+@pytest.mark.parametrize("gamma,prefix_len", [((1 << 32) + 1, 0), (1, (1 << 32) + 5), (1, -(1 << 32) + 5), (-(1 << 32) + 1, 0)])
+def test_numbers_past_32_bits_are_refused(gamma, prefix_len):
+    """They would arrive in the descriptor as other, valid ones."""
+    cache = host_cache()
+    table, n = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    pages = SimpleNamespace(numel=lambda: 1 << 32, data_ptr=lambda: 0)
+    real = api._is
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(api, "_is", lambda t, *a: t is pages or real(t, *a))
+        with pytest.raises(ValueError, match="32-bit"):
+            api._attn_batch(torch.zeros(4, 2, 64), cache, table, n, gamma, torch.zeros(3, dtype=torch.int32), None, None, pages, prefix_len)
+        g, *_ = api._attn_batch(torch.zeros(4, 2, 64), cache, table, n, 1, torch.zeros(3, dtype=torch.int32), None, None, pages, 16)
+    assert (g.gamma, g.prefix_len) == (1, 16)
