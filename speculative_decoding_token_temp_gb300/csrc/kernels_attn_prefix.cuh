@@ -7,9 +7,9 @@
 //   keys    bf16, exponent included: exact (4 significant bits, bf16's exponent range), and
 //           bf16 queries times bf16 keys need no scaling at all;
 //   values  f16, relative to the largest exponent of their 128 tokens (one number a tile
-//           and head): code * 2^(6 + e - E), exact down to 21 binades below the tile's
-//           largest exponent; E joins the tile's scores before the exponential, as the
-//           exponents of single values do in attn_tc_kernel;
+//           and head): code * 2^(6 + e - largest), exact down to 21 binades below the tile's
+//           largest exponent; it joins the tile's scores before the exponential (as E), as
+//           the exponents of single values do in attn_tc_kernel;
 //   weights f16 (11 bits), kept in tensor memory where the scores were.
 //
 // A block holds 256 rows as two tiles of 128 and walks the keys in tiles of 128 tokens:
@@ -52,7 +52,7 @@ struct PreShape {
 // The widened prefix in the workspace: [kv head][tokens, up to whole tiles][D].
 struct WideParams {
   uint16_t *k16, *v16;
-  float* exp;  // [kv head][tile]: E
+  float* exp;  // [kv head][tile]: E, kSumShift more than the values are relative to (so the sums of 2^(x - m) are that much smaller)
   int tiles;
 };
 
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(256) widen_kernel(AttnParams p, WideParams w) 
   __syncthreads();
   float e = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
   if (e < -200.f) e = 0.f;  // no token with values
-  if (tid == 0) w.exp[(long long)h * w.tiles + tile] = e;
+  if (tid == 0) w.exp[(long long)h * w.tiles + tile] = e + (float)kSumShift;
   const int sub = tid % L, u0 = tid / L;
   uint2 kw[STEPS], vw[STEPS];
 #pragma unroll
@@ -459,7 +459,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           if (half == 0) finish_lse(p, idx, r);
         }
         float* dst = whole ? p.dst_o + idx * D : slot + 2 * NR + c * D;
-        const float scale = (whole ? r.a : 1.f) * (1.f / (1 << kValueShift));
+        const float scale = (whole ? r.a : 1.f) * (1.f / (1 << (kValueShift + kSumShift)));
 #pragma unroll 1
         for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
           float o[32];

@@ -88,6 +88,17 @@ def test_many_tokens_of_the_smallest_and_largest_values(dev, dtype, exponent, co
     assert abs(float(out["lse"][0, 0]) - np.log(n)) <= n * 2.0 ** -24 + 2.0 ** -18
 
 
+@pytest.mark.parametrize("exponent,code", [(-100, 448.0), (120, 128.0)])
+def test_many_shared_tokens_of_the_smallest_and_largest_values(dev, exponent, code):
+    """The same of a prefix of 1100000 tokens that 128 rows share (in 128-row tiles of the widened prefix)."""
+    n = 1_100_000
+    cache, q, table = one_value(dev, n, 64, exponent, code, "bf16", 128)
+    out = api.spec_attention(q, cache, torch.zeros(128, 1, dtype=torch.int32, device=dev), i32([0] * 128, dev), gamma=0,
+                             prefix_table=i32(table[0], dev), prefix_len=n, want_lse=True)
+    assert ((out["o"].double() / (code * 2.0 ** exponent) - 1).abs() <= n * 2.0 ** -24 + 2.0 ** -8).all()
+    assert ((out["lse"].double() - np.log(n)).abs() <= n * 2.0 ** -24 + 2.0 ** -18).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("what", [float("inf"), float("-inf")])
 @pytest.mark.parametrize("tokens,prefix", [(1, 0), (3, 0), (0, 2), (1, 1)])
