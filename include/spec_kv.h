@@ -104,7 +104,9 @@ typedef struct {
 
 /* Bytes of scratch memory spec_attention needs (0 for an invalid geometry or dtype, or one
  * whose work, counted in 128-token tiles of all sequences at their longest, passes 2^30;
- * spec_attention refuses those with SPEC_ERR_INVALID_ARG). */
+ * spec_attention refuses those with SPEC_ERR_INVALID_ARG). For bf16 queries, where many rows
+ * share a long prefix, it holds that prefix in 16 bits: 4 bytes for each element of its keys
+ * (4.3 GB for 2^20 tokens at 8 kv heads of 128). */
 size_t spec_attention_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype);
 
 /*
@@ -119,6 +121,13 @@ size_t spec_attention_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_d
  *   q [total_draft + B][q_heads][head_dim] of dtype with the strides given (in elements);
  *   o [total_draft + B][q_heads][head_dim] of dtype, contiguous
  *   lse [total_draft + B][q_heads] fp32 or NULL: ln sum_t exp(scale * q . k_t)
+ *
+ * Accuracy. Scores, sums and lse are fp32. With bf16 queries a query's element is held to
+ * 2^-17 of its row's largest, and a weight enters the values' sum with 11 bits down to 2^-24
+ * of the row's largest weight (each times the token's 2^exponent) and to 2^-35 of that below.
+ * Where many rows share a long prefix these are 2^-22 and 2^-33, and its values are exact
+ * down to 2^-21 of the largest exponent among 128 tokens. The exponents of the values that a
+ * row sees may differ by 100: past that the weight of a token of the smaller ones may be lost.
  *
  * What no row sees does not matter: unwritten places, pages past kv_len, NaN codes or
  * exponents of tokens that a row's mask hides. A row that sees a token stored as NaN (or

@@ -23,7 +23,7 @@
 // 2048 at their nominal rate; the scores' read both operands from shared memory at its full
 // rate, beside the copies into it. A softmax group's own work is 1300 clocks; 1110 (maxima
 // from the loads of scores) left the time as it was. 9216 rows a kv head x 16384 tokens, 8 kv
-// heads: 408 us, and 17 us to widen (34 MB read, 67 MB written, mostly to L2).
+// heads: 410 us, and 17 us to widen (34 MB read, 67 MB written, mostly to L2).
 #pragma once
 
 #include "kernels_attn_tc.cuh"

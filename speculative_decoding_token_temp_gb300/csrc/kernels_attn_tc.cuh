@@ -12,7 +12,7 @@
 //
 //   queries  a bf16 query is, within its row's power of two, exactly the sum of two e4m3
 //            parts (8 significant bits = 4 + 4; elements below 2^-8 of the row's largest
-//            keep an absolute 2^-18 of it);
+//            keep an absolute 2^-17 of it);
 //   weights  a weight is rounded to f16, and every f16 number up to 2^15 is exactly the sum
 //            of three e5m2 parts (each the rest of the ones before, scaled by 16 and 256 in
 //            columns of its own: 11 bits are 3 + 4 + 4 with the rests' signs, and the last
@@ -38,7 +38,7 @@
 // What bounds it: the cache's bytes where stretches are long (a tile, 32 KB of codes with
 // head_dim 128, takes an SM 1270 clocks: 256 sequences x 1 row to 1-8192 tokens 328 us, 98 %
 // of a copy's rate), else the instructions of a stretch's beginning and end, as many as three
-// tiles': 64 x 6 rows to 6-4096 tokens 57 us (DRAM 64 %).
+// tiles': 64 x 6 rows to 6-4096 tokens 57 us (DRAM 66 %).
 #pragma once
 
 #include <cuda.h>

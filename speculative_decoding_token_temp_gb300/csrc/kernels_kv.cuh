@@ -5,10 +5,10 @@
 // elements a lane, so that the bf16 side of a lane is one 16-byte access, its code side
 // one 8-byte access, and the maximum of a vector is log2(head_dim / 8) shuffles.
 //
-// 32768 rows of 8 heads of 128 in bf16: append 41 us (4.9 TB/s), read 37 us (5.5 TB/s). What
-// bounds the append is instruction issue (72 % of cycles, four vectors a lane on the way; two
-// 47 us, eight 50), the read the latency of its loads. A few hundred rows are one chain of
-// dependent loads, position, page, data: 256 rows 2.5 us.
+// 32768 rows of 8 heads of 128 in bf16: append 41 us (4.9 TB/s), read 37 us (5.5 TB/s). The
+// append issues instructions in 72 % of cycles (four vectors a lane on the way; two 47 us,
+// eight 50), the read waits for its loads; neither is a limit by itself. A few hundred rows are
+// one chain of dependent loads, position, page, data: 256 rows 2.5 us.
 #pragma once
 
 #include <cuda_bf16.h>
