@@ -13,6 +13,15 @@
  *                    sequence of the batch shares and whose part is computed once for all
  *   spec_kv_read     cached tokens read back as numbers
  *
+ * and around these what a target's layer and a long context need besides:
+ *
+ *   spec_qk_rope, spec_qk_rope_append   the norms of each head and the rotation by positions,
+ *                    on the way from the projection to the attention, the second with the
+ *                    cache's write in the same pass
+ *   spec_attention_chunk   spec_attention for more rows a sequence: prompts, pieces of them
+ *   spec_kv_weigh    the softmax weight that each cached token has gathered
+ *   spec_kv_evict    cuts sequences to a budget of tokens, the heaviest kept
+ *
  * Cache format. A vector of head_dim elements x (the key or the value of one token at one
  * kv head) is held as head_dim e4m3 codes c and one exponent byte: x ~ c * 2^(byte - 127).
  * The exponent e is the smallest whole number with max|x| <= 448 * 2^e (448 is the code's
@@ -140,6 +149,119 @@ size_t spec_attention_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_d
 spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,
                            int64_t q_head_stride, void* o, float* lse, uint32_t* device_status, void* workspace,
                            size_t workspace_bytes, spec_stream_t stream);
+
+/* ---- chunks of new tokens ---------------------------------------------------- */
+
+#define SPEC_MAX_CHUNK_GAMMA ((1 << 20) - 1) /* rows of a sequence in one spec_attention_chunk call, less one */
+
+/*
+ * spec_attention for chunks: the same rows, masks (chains only: parent NULL), prefix,
+ * outputs, accuracy and data errors, with gamma up to SPEC_MAX_CHUNK_GAMMA. Row i of a
+ * sequence of n_b = gamma_b + 1 rows sees the prefix, the first kv_len[b] - n_b tokens and
+ * the chunk's own up to i; a packed batch may mix prompts with single tokens.
+ */
+size_t spec_attention_chunk_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype);
+spec_status spec_attention_chunk(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,
+                                 int64_t q_head_stride, void* o, float* lse, uint32_t* device_status, void* workspace,
+                                 size_t workspace_bytes, spec_stream_t stream);
+
+/* ---- norms and rotation of queries and keys ---------------------------------- */
+
+#define SPEC_ROPE_MAX_AXES 4
+
+/* How heads are rotated. Pair j of a head (elements j and j + rot_dim / 2, or 2 j and
+ * 2 j + 1 when interleaved) turns by position * step[j], where the position is the one of
+ * the row's `axes` that axis[j] names. step is in units of 2^-64 turn, modulo one turn:
+ * round(frequency / (2 pi) * 2^64); the angle is then right to 2^-32 of a turn for every
+ * 32-bit position. */
+typedef struct {
+  int32_t rot_dim;      /* leading elements of a head that rotate: a multiple of 16, 0..head_dim */
+  int32_t axes;         /* positions of a row, 1..SPEC_ROPE_MAX_AXES */
+  int32_t interleaved;
+  const uint64_t* step; /* device [rot_dim / 2] */
+  const uint8_t* axis;  /* device [rot_dim / 2], or NULL: all of the first axis (a number past the last is the last) */
+} spec_rope;
+
+/* The norm of each head before the rotation: x * weight / sqrt(mean(x^2) + eps), over the
+ * head's elements (whose squares' sum has to be in fp32's range). */
+typedef struct {
+  const void* q_weight; /* device [head_dim] of the call's dtype, or NULL: ones */
+  const void* k_weight; /* the same */
+  float eps;            /* negative: no norms (weights NULL) */
+} spec_head_norm;
+
+/*
+ * Queries and keys normed and rotated: q_out [rows][q_heads][head_dim], k_out
+ * [rows][k_heads][head_dim] of dtype, contiguous and 16-byte aligned, from rows with the
+ * strides given (in elements). positions: device [rows][axes]. fp32 arithmetic, one rounding
+ * at the end. The outputs must not overlap the inputs.
+ */
+spec_status spec_qk_rope(int32_t rows, int32_t q_heads, int32_t k_heads, int32_t head_dim, spec_rope rope, spec_head_norm norm,
+                         const int32_t* positions, spec_dtype dtype, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                         const void* k, int64_t k_row_stride, int64_t k_head_stride, void* q_out, void* k_out,
+                         spec_stream_t stream);
+
+/*
+ * The same with the cache's write: the rotated keys and the values go to the cache as by
+ * spec_kv_append (whose rules hold for r and the status word), quantised from their fp32
+ * values; the queries to q_out. Rows left out of the cache still give their queries.
+ */
+spec_status spec_qk_rope_append(spec_kv_cache c, spec_kv_rows r, int32_t q_heads, spec_rope rope, spec_head_norm norm,
+                                const int32_t* positions, spec_dtype dtype, const void* q, int64_t q_row_stride,
+                                int64_t q_head_stride, const void* k, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                                int64_t v_row_stride, int64_t v_head_stride, void* q_out, uint32_t* device_status,
+                                spec_stream_t stream);
+
+/* ---- eviction ---------------------------------------------------------------- */
+
+/*
+ * The weight that cached tokens gather. For every cached token t of sequence b and kv head h
+ *   mass = keep * mass + sum_i sum_{heads of the group} exp(scale * q_i . k_t - lse_i)
+ * over the rows i that see t (a chain, as in spec_attention; g.parent NULL, g.prefix_len 0).
+ * The round's own tokens, the last gamma_b + 1, begin anew: their old mass counts as 0, and
+ * with keep = 0 no old mass is read. What else mass holds is left as it is.
+ *   lse [total_draft + B][q_heads] fp32 of spec_attention or spec_attention_chunk (with a
+ *     shared prefix: its lse has the prefix in it). A row whose lse is not finite adds nothing.
+ *   n_accepted [B] or NULL: only rows 0..n_accepted[b] count (what a verification accepted)
+ *   mass [num_pages][kv_heads][page_size] fp32, 4-byte aligned
+ * gamma at most SPEC_MAX_GAMMA: of a long chunk, pass its last rows. No two sequences may
+ * share a page that holds a token of theirs. fp32 sums over queries held to 22 bits of
+ * their row's largest element; results do not depend on timing.
+ * Data errors: a bad kv_len or n_accepted (outside 0..gamma_b) sets SPEC_DEV_OFFSETS and
+ * leaves its sequence out; tokens on pages outside the cache are left out (SPEC_DEV_PAGE); a
+ * bad cu_draft sets SPEC_DEV_OFFSETS and leaves all out.
+ */
+spec_status spec_kv_weigh(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,
+                          int64_t q_head_stride, const float* lse, const int32_t* n_accepted, float keep, float* mass,
+                          uint32_t* device_status, spec_stream_t stream);
+
+typedef struct {
+  int32_t B; /* sequences, 0..65535 */
+  int32_t pages_per_seq;
+  const int32_t* page_table;     /* device [B][pages_per_seq] */
+  const int32_t* kv_len;         /* device [B] */
+  int32_t new_pages_per_seq;
+  const int32_t* new_page_table; /* device [B][new_pages_per_seq]: pages that the kept tokens go to, none of them among
+                                    the sequences' own; NULL (or page_table itself): in place */
+  int32_t budget;                /* tokens of a sequence that stay at most, >= 1 */
+  int32_t sinks, recent;         /* the first and the last tokens that stay in any case, sinks + recent <= budget */
+} spec_evict_batch;
+
+/*
+ * Cuts every sequence of more than `budget` tokens to `budget`. At each kv head stay the first
+ * `sinks`, the last `recent` and, of those between, the ones of the largest mass (of equal ones
+ * the earliest; a NaN is lighter than every number). They keep their order: place j of the
+ * sequence at that head is then the token that was at kept[b][h][j], with its key, value,
+ * exponents and mass. To other pages shorter sequences are copied whole.
+ *   kept device [B][kv_heads][budget]: old places, ascending; -1 past the last
+ *   kv_len_out device [B] (not kv_len itself): min(kv_len, budget)
+ * A sequence's pages must be its own. Rotated keys hold their positions, so attention over
+ * what stays goes on as before; later tokens keep the positions they would have had.
+ * Data errors: a bad kv_len sets SPEC_DEV_OFFSETS, a page outside the cache SPEC_DEV_PAGE; the
+ * sequence is left as it was, its row of kept is -1, its kv_len_out kv_len (0 with other pages).
+ */
+spec_status spec_kv_evict(spec_evict_batch g, spec_kv_cache c, float* mass, int32_t* kept, int32_t* kv_len_out,
+                          uint32_t* device_status, spec_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -35,6 +35,8 @@ SPEC_MODE_GREEDY = 1
 SPEC_MODE_NKL = 2
 
 SPEC_MAX_GAMMA = 128
+SPEC_MAX_CHUNK_GAMMA = (1 << 20) - 1
+SPEC_ROPE_MAX_AXES = 4
 SPEC_MAX_TREE_NODES = 64
 SPEC_STATS_SLOTS = 64
 SPEC_MAX_CANDIDATES = 4
@@ -82,6 +84,21 @@ class SpecAttnBatch(ctypes.Structure):
                 ("prefix_table", ctypes.c_void_p), ("parent", ctypes.c_void_p), ("scale", ctypes.c_float)]
 
 
+class SpecRope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("step", ctypes.c_void_p), ("axis", ctypes.c_void_p)]
+
+
+class SpecHeadNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class SpecEvictBatch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32), ("page_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("new_pages_per_seq", ctypes.c_int32), ("new_page_table", ctypes.c_void_p),
+                ("budget", ctypes.c_int32), ("sinks", ctypes.c_int32), ("recent", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _F = ctypes.c_float
@@ -115,6 +132,14 @@ SIGNATURES = {
     "spec_kv_read": (ctypes.c_int, [SpecKvCache, SpecKvRows, ctypes.c_int, _P, _P, _P, _P]),
     "spec_attention_workspace_bytes": (_S, [SpecAttnBatch, SpecKvCache, ctypes.c_int]),
     "spec_attention": (ctypes.c_int, [SpecAttnBatch, SpecKvCache, ctypes.c_int, _P, _L, _L, _P, _P, _P, _P, _S, _P]),
+    "spec_attention_chunk_workspace_bytes": (_S, [SpecAttnBatch, SpecKvCache, ctypes.c_int]),
+    "spec_attention_chunk": (ctypes.c_int, [SpecAttnBatch, SpecKvCache, ctypes.c_int, _P, _L, _L, _P, _P, _P, _P, _S, _P]),
+    "spec_qk_rope": (ctypes.c_int, [_I, _I, _I, _I, SpecRope, SpecHeadNorm, _P, ctypes.c_int, _P, _L, _L, _P, _L, _L, _P, _P,
+                                    _P]),
+    "spec_qk_rope_append": (ctypes.c_int, [SpecKvCache, SpecKvRows, _I, SpecRope, SpecHeadNorm, _P, ctypes.c_int, _P, _L, _L,
+                                           _P, _L, _L, _P, _L, _L, _P, _P, _P]),
+    "spec_kv_weigh": (ctypes.c_int, [SpecAttnBatch, SpecKvCache, ctypes.c_int, _P, _L, _L, _P, _P, _F, _P, _P, _P]),
+    "spec_kv_evict": (ctypes.c_int, [SpecEvictBatch, SpecKvCache, _P, _P, _P, _P, _P]),
     "spec_status_str": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

@@ -12,6 +12,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import fractions
+import math
 
 import torch
 
@@ -691,22 +693,9 @@ def spec_attention_workspace_bytes(q, cache: KVCache, page_table, kv_len, *, gam
     return int(_lib.lib().spec_attention_workspace_bytes(g, cache.desc, _dtype_code(q)))
 
 
-def spec_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_len: torch.Tensor, *,
-                   gamma: int | None = None, cu_draft: torch.Tensor | None = None, parent=None,
-                   scale: float | None = None, prefix_table: torch.Tensor | None = None, prefix_len: int = 0,
-                   want_lse: bool = False, out: dict | None = None, workspace=None, device_status=None) -> dict:
-    """Attention of a verification round's rows over the cache.
-
-    q [rows, q_heads, head_dim] in bfloat16 or float32, rows packed as the target rows of
-    the verification calls (sequence b's gamma_b + 1 rows from cu_draft[b] + b on), or
-    [B, gamma + 1, q_heads, head_dim]; views of a wider buffer are taken as they are.
-    kv_len [B] int32: cached tokens of each sequence, this round's rows (appended before)
-    among them. Row i sees its sequence's earlier tokens, this round's rows up to i (with
-    `parent`, a host sequence as in spec_verify_tree: its ancestors) and, with prefix_len,
-    the shared prefix on the pages prefix_table. scale defaults to head_dim ** -0.5.
-    Returns o [rows, q_heads, head_dim], lse [rows, q_heads] (fp32, with want_lse) and
-    device_status. The default workspace is kept for each stream; a call that is captured
-    into a graph takes one of the graph's own memory."""
+def _attend(name, q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, prefix_table, prefix_len, want_lse, out,
+            workspace, device_status) -> dict:
+    """The call of spec_attention or spec_attention_chunk (`name`)."""
     dt = _KV_DTYPES.get(q.dtype)
     if dt is None:
         raise TypeError(f"q must be bfloat16 or float32, got {q.dtype}")
@@ -724,7 +713,7 @@ def spec_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv
         _need(t, "lse", torch.float32, rows * H, cache.k.device)
         lse = t.data_ptr()
     lib = _lib.lib()
-    nbytes = lib.spec_attention_workspace_bytes(g, cache.desc, dt)
+    nbytes = getattr(lib, name + "_workspace_bytes")(g, cache.desc, dt)
     with _on(cache.index):
         stream = _stream_handle(cache.index)
         if workspace is None:
@@ -739,8 +728,294 @@ def spec_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv
                     workspace = keep.get(nbytes, cache.k.device)
         else:
             workspace = _workspace(workspace, nbytes, cache.k.device)
-        code = lib.spec_attention(g, cache.desc, dt, *view, y.data_ptr(), lse, _status_word(o, device_status, cache),
+        code = getattr(lib, name)(g, cache.desc, dt, *view, y.data_ptr(), lse, _status_word(o, device_status, cache),
                                   workspace.data_ptr(), workspace.numel(), stream)
     if code:
-        check("spec_attention", code)
+        check(name, code)
+    return o
+
+
+def spec_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_len: torch.Tensor, *,
+                   gamma: int | None = None, cu_draft: torch.Tensor | None = None, parent=None,
+                   scale: float | None = None, prefix_table: torch.Tensor | None = None, prefix_len: int = 0,
+                   want_lse: bool = False, out: dict | None = None, workspace=None, device_status=None) -> dict:
+    """Attention of a verification round's rows over the cache.
+
+    q [rows, q_heads, head_dim] in bfloat16 or float32, rows packed as the target rows of
+    the verification calls (sequence b's gamma_b + 1 rows from cu_draft[b] + b on), or
+    [B, gamma + 1, q_heads, head_dim]; views of a wider buffer are taken as they are.
+    kv_len [B] int32: cached tokens of each sequence, this round's rows (appended before)
+    among them. Row i sees its sequence's earlier tokens, this round's rows up to i (with
+    `parent`, a host sequence as in spec_verify_tree: its ancestors) and, with prefix_len,
+    the shared prefix on the pages prefix_table. scale defaults to head_dim ** -0.5.
+    Returns o [rows, q_heads, head_dim], lse [rows, q_heads] (fp32, with want_lse) and
+    device_status. The default workspace is kept for each stream; a call that is captured
+    into a graph takes one of the graph's own memory."""
+    return _attend("spec_attention", q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, prefix_table, prefix_len, want_lse,
+                   out, workspace, device_status)
+
+
+def spec_attention_chunk_workspace_bytes(q, cache: KVCache, page_table, kv_len, *, gamma=None, cu_draft=None, scale=None,
+                                         prefix_table=None, prefix_len: int = 0) -> int:
+    """Workspace bytes of the same spec_attention_chunk call."""
+    g = _attn_batch(q, cache, page_table, kv_len, gamma, cu_draft, None, scale, prefix_table, prefix_len)[0]
+    return int(_lib.lib().spec_attention_chunk_workspace_bytes(g, cache.desc, _dtype_code(q)))
+
+
+def spec_attention_chunk(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_len: torch.Tensor, *,
+                         gamma: int | None = None, cu_draft: torch.Tensor | None = None, scale: float | None = None,
+                         prefix_table: torch.Tensor | None = None, prefix_len: int = 0, want_lse: bool = False,
+                         out: dict | None = None, workspace=None, device_status=None) -> dict:
+    """Attention of chunks of new tokens over the cache: spec_attention (without trees) for up to
+    2^20 rows a sequence, whose arguments, layouts and results it shares. A chunk of n tokens
+    has gamma = n - 1; packed batches (cu_draft) may mix prompts with single tokens."""
+    return _attend("spec_attention_chunk", q, cache, page_table, kv_len, gamma, cu_draft, None, scale, prefix_table, prefix_len,
+                   want_lse, out, workspace, device_status)
+
+
+class Rope:
+    """How heads are rotated by positions: the plan of spec_qk_rope and spec_qk_rope_append.
+
+    Pair j of a head turns by positions[row, axis[j]] * inv_freq[j] radians. By default the whole
+    head rotates with base ** (-2 j / rot_dim); inv_freq gives other frequencies (rot_dim / 2
+    numbers, taken in 64 bits), rot_dim fewer elements (a multiple of 16). Positions of several
+    axes (time, height, width): `sections` counts the pairs of each axis in order, or `axis`
+    names each pair's. interleaved: pairs are elements 2 j and 2 j + 1 instead of j and
+    j + rot_dim / 2. Angles are right to 2^-32 of a turn for every 32-bit position (the
+    frequencies are held in units of 2^-64 turn)."""
+
+    __slots__ = ("head_dim", "rot_dim", "axes", "interleaved", "step", "axis", "index", "desc")
+
+    def __init__(self, head_dim: int, device, *, base: float = 10000.0, rot_dim: int | None = None, inv_freq=None,
+                 sections=None, axis=None, interleaved: bool = False):
+        head_dim = int(head_dim)
+        rot = head_dim if rot_dim is None else int(rot_dim)
+        if head_dim not in (64, 128):
+            raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+        if rot < 0 or rot > head_dim or rot % 16:
+            raise ValueError(f"rot_dim must be a multiple of 16 from 0 to {head_dim}, got {rot}")
+        pairs = rot // 2
+        freq = [float(base) ** (-2.0 * j / rot) for j in range(pairs)] if inv_freq is None else [float(x) for x in inv_freq]
+        if len(freq) != pairs or not all(math.isfinite(x) for x in freq):
+            raise ValueError(f"inv_freq must be {pairs} finite numbers")
+        if sections is not None:
+            if axis is not None:
+                raise ValueError("sections or axis, not both")
+            sections = [int(n) for n in sections]
+            if any(n < 0 for n in sections) or sum(sections) != pairs:
+                raise ValueError(f"sections must count {pairs} pairs, got {sections}")
+            axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        which = [0] * pairs if axis is None else [int(a) for a in axis]
+        axes = len(sections) if sections else max(which, default=0) + 1
+        if len(which) != pairs or any(a < 0 for a in which) or axes > _lib.SPEC_ROPE_MAX_AXES:
+            raise ValueError(f"axis must name one of at most {_lib.SPEC_ROPE_MAX_AXES} axes for each of {pairs} pairs")
+        # turns in units of 2^-64, from the frequency's exact value and 2 pi to 40 digits
+        two_pi = fractions.Fraction(6283185307179586476925286766559005768394, 10 ** 39)
+        steps = [round(fractions.Fraction(x) / two_pi * (1 << 64)) % (1 << 64) for x in freq]
+        self.step = torch.tensor([s - (1 << 64) if s >> 63 else s for s in steps], dtype=torch.int64).to(device)
+        if self.step.device.type != "cuda":
+            raise ValueError(f"device must be a CUDA device, got {device}")
+        self.axis = torch.tensor(which, dtype=_U8).to(device) if axes > 1 else None
+        self.head_dim, self.rot_dim, self.axes, self.interleaved = head_dim, rot, axes, bool(interleaved)
+        self.index = self.step.get_device()
+        self.desc = _lib.SpecRope(rot, axes, int(self.interleaved), self.step.data_ptr() if pairs else None,
+                                  None if self.axis is None else self.axis.data_ptr())
+
+
+def _rope_rows(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, index: int):
+    """(address, row stride, head stride) of a [rows, heads, head_dim] view whose vectors are contiguous."""
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on device {index}, got {t.device}")
+    if t.shape != (rows, heads, dim):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {dim}], got {tuple(t.shape)}")
+    row, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return t.data_ptr(), row, head
+
+
+_NO_NORM = _lib.SpecHeadNorm(None, None, -1.0)
+
+
+def _rope_norm(q_weight, k_weight, eps, dtype, dim: int, index: int, device) -> _lib.SpecHeadNorm:
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("weights of a norm need eps")
+        return _NO_NORM
+    eps = float(eps)
+    if not 0.0 <= eps < math.inf:
+        raise ValueError(f"eps must be finite and at least 0, got {eps}")
+    at = []
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (not _is(w, dtype, index) or w.numel() != dim):
+            _need(w, name, dtype, dim, device)
+        at.append(None if w is None else w.data_ptr())
+    return _lib.SpecHeadNorm(at[0], at[1], eps)
+
+
+def _rope_check(rope, positions, rows: int, dim: int, index: int, device) -> int:
+    """The positions' address, once they and the plan fit the rows."""
+    if rope.head_dim != dim or rope.index != index:
+        raise ValueError(f"the Rope is for heads of {rope.head_dim} on device {rope.index}, got {dim} on {index}")
+    if not _is(positions, _I32, index):
+        _need(positions, "positions", _I32, device=device)
+    shape = positions.shape
+    if shape != (rows, rope.axes) and not (rope.axes == 1 and shape == (rows,)):
+        raise ValueError(f"positions must be [{rows}, {rope.axes}], got {tuple(shape)}")
+    return positions.data_ptr()
+
+
+def _rope_out(o: dict, name: str, rows: int, heads: int, dim: int, like: torch.Tensor) -> int:
+    t = o.get(name)
+    if t is None:
+        t = o[name] = torch.empty(rows, heads, dim, dtype=like.dtype, device=like.device)
+    elif not _is(t, like.dtype, like.get_device()) or t.numel() != rows * heads * dim:
+        _need(t, name, like.dtype, rows * heads * dim, like.device)
+    return t.data_ptr()
+
+
+def spec_qk_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope, positions: torch.Tensor, *, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float | None = None, out: dict | None = None) -> dict:
+    """Norm (with eps) and rotation of each head of queries and keys, in one pass.
+
+    q [rows, q_heads, head_dim], k [rows, k_heads, head_dim] in bfloat16 or float32; slices of a
+    fused projection are taken as they are. positions int32 [rows] or [rows, rope.axes]. eps
+    turns the norms on, x * weight / sqrt(mean(x^2) + eps), with weights [head_dim] of q's type
+    or none. Returns q and k, contiguous, of the same type."""
+    dt = _KV_DTYPES.get(q.dtype)
+    if dt is None or k.dtype is not q.dtype:
+        raise TypeError(f"q and k must both be bfloat16 or float32, got {q.dtype} and {k.dtype}")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q and k must be [rows, heads, head_dim], got {tuple(q.shape)} and {tuple(k.shape)}")
+    rows, H, D = q.shape
+    Hk, index = k.shape[1], q.get_device()
+    vq, vk = _rope_rows(q, "q", rows, H, D, index), _rope_rows(k, "k", rows, Hk, D, index)
+    pos = _rope_check(rope, positions, rows, D, index, q.device)
+    norm = _rope_norm(q_weight, k_weight, eps, q.dtype, D, index, q.device)
+    o = {} if out is None else out
+    to = _rope_out(o, "q", rows, H, D, q), _rope_out(o, "k", rows, Hk, D, k)
+    with _on(index):
+        code = _lib.lib().spec_qk_rope(rows, H, Hk, D, rope.desc, norm, pos, dt, *vq, *vk, *to, _stream_handle(index))
+    if code:
+        check("spec_qk_rope", code)
+    return o
+
+
+def spec_qk_rope_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: Rope, positions: torch.Tensor,
+                        page_table: torch.Tensor, row_seq: torch.Tensor, row_pos: torch.Tensor, *,
+                        q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float | None = None,
+                        out: dict | None = None, device_status=None) -> dict:
+    """spec_qk_rope and spec_kv_append in one pass: the normed and rotated keys and the values are
+    quantised into the cache (rows placed as by spec_kv_append), the queries come back.
+
+    positions are the rotation's and independent of row_pos, the rows' places in the cache: they
+    differ behind a shared prefix, after an eviction, or with several axes. Returns q
+    [rows, q_heads, head_dim] and device_status."""
+    dt = _KV_DTYPES.get(q.dtype)
+    if dt is None or k.dtype is not q.dtype or v.dtype is not q.dtype:
+        raise TypeError(f"q, k and v must all be bfloat16 or float32, got {q.dtype}, {k.dtype} and {v.dtype}")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [rows, heads, head_dim], got {tuple(q.shape)}")
+    r = _kv_rows(cache, page_table, row_seq, row_pos)
+    rows, H, D, Hk, index, device = r.rows, q.shape[1], cache.head_dim, cache.kv_heads, cache.index, cache.k.device
+    vq = _rope_rows(q, "q", rows, H, D, index)
+    vk, vv = _rope_rows(k, "k", rows, Hk, D, index), _rope_rows(v, "v", rows, Hk, D, index)
+    pos = _rope_check(rope, positions, rows, D, index, device)
+    norm = _rope_norm(q_weight, k_weight, eps, q.dtype, D, index, device)
+    o = {} if out is None else out
+    to = _rope_out(o, "q", rows, H, D, q)
+    with _on(index):
+        code = _lib.lib().spec_qk_rope_append(cache.desc, r, H, rope.desc, norm, pos, dt, *vq, *vk, *vv, to,
+                                              _status_word(o, device_status, cache), _stream_handle(index))
+    if code:
+        check("spec_qk_rope_append", code)
+    return o
+
+
+def _mass(mass, cache: KVCache) -> None:
+    if not _is(mass, torch.float32, cache.index) or mass.shape != cache.k_exp.shape:
+        _need(mass, "mass", torch.float32, device=cache.k.device)
+        raise ValueError(f"mass must be {tuple(cache.k_exp.shape)}, got {tuple(mass.shape)}")
+
+
+def spec_kv_weigh(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_len: torch.Tensor, lse: torch.Tensor,
+                  mass: torch.Tensor, *, gamma: int | None = None, cu_draft: torch.Tensor | None = None,
+                  n_accepted: torch.Tensor | None = None, scale: float | None = None, keep: float = 1.0,
+                  out: dict | None = None, device_status=None) -> dict:
+    """The softmax weight that cached tokens gather, added up in mass [num_pages, kv_heads, page_size]
+    (float32): mass = keep * mass + the weights that the round's rows give the token, summed over
+    rows and the kv head's query heads.
+
+    q, kv_len, gamma, cu_draft, scale as in the round's attention call (chains); lse [rows, q_heads]
+    is what that call left (want_lse). n_accepted int32 [B]: only rows 0..n_accepted[b] count, as a
+    verification leaves it. The round's own tokens begin at 0; keep = 0 reads no old mass, so
+    that mass needs no initialisation before a first call that covers a sequence. Returns the
+    dict with device_status."""
+    dt = _KV_DTYPES.get(q.dtype)
+    if dt is None:
+        raise TypeError(f"q must be bfloat16 or float32, got {q.dtype}")
+    g, rows, H, _ = _attn_batch(q, cache, page_table, kv_len, gamma, cu_draft, None, scale, None, 0)
+    view = _rows_view(q, "q", rows, H, cache)
+    index, device = cache.index, cache.k.device
+    if not _is(lse, torch.float32, index) or lse.numel() != rows * H:
+        _need(lse, "lse", torch.float32, rows * H, device)
+    _mass(mass, cache)
+    at = None
+    if n_accepted is not None:
+        if not _is(n_accepted, _I32, index) or n_accepted.numel() != g.B:
+            _need(n_accepted, "n_accepted", _I32, g.B, device)
+        at = n_accepted.data_ptr()
+    o = {} if out is None else out
+    with _on(index):
+        code = _lib.lib().spec_kv_weigh(g, cache.desc, dt, *view, lse.data_ptr(), at, float(keep), mass.data_ptr(),
+                                        _status_word(o, device_status, cache), _stream_handle(index))
+    if code:
+        check("spec_kv_weigh", code)
+    return o
+
+
+def spec_kv_evict(cache: KVCache, mass: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, budget: int, *,
+                  sinks: int = 0, recent: int = 0, new_table: torch.Tensor | None = None, out: dict | None = None,
+                  device_status=None) -> dict:
+    """Cut every sequence of more than `budget` tokens to `budget`: at each kv head the first `sinks`,
+    the last `recent` and the heaviest of the others stay (by mass [num_pages, kv_heads, page_size];
+    of equal ones the earliest), in their order and moved together to the sequence's first places,
+    with their mass; or, with new_table (int32 [B, pages]), to those pages. Returns kept [B, kv_heads,
+    budget] (int32: the old places, -1 past the last), kv_len [B] (the new lengths) and
+    device_status. The sequences' pages must be their own; new_table's must be none of theirs."""
+    index, device = cache.index, cache.k.device
+    if not (_is(page_table, _I32, index) and _is(kv_len, _I32, index)):
+        _need(page_table, "page_table", _I32, device=device)
+        _need(kv_len, "kv_len", _I32, device=device)
+    shape = page_table.shape
+    if len(shape) != 2:
+        raise ValueError(f"page_table must be [sequences, pages], got {tuple(shape)}")
+    B, budget, sinks, recent = shape[0], int(budget), int(sinks), int(recent)
+    if kv_len.numel() != B:
+        raise ValueError(f"kv_len must have {B} elements, got {kv_len.numel()}")
+    if not (1 <= budget < 1 << 31 and sinks >= 0 and recent >= 0 and sinks + recent <= budget):
+        raise ValueError(f"budget must be at least 1 and at least sinks + recent, got {budget}, {sinks} and {recent}")
+    _mass(mass, cache)
+    width, new = 0, None
+    if new_table is not None:
+        if not _is(new_table, _I32, index):
+            _need(new_table, "new_table", _I32, device=device)
+        if new_table.dim() != 2 or new_table.shape[0] != B:
+            raise ValueError(f"new_table must be [{B}, pages], got {tuple(new_table.shape)}")
+        width, new = new_table.shape[1], new_table.data_ptr()
+        if width * cache.page_size < min(budget, shape[1] * cache.page_size):
+            raise ValueError(f"new_table has {width} pages a sequence, {min(budget, shape[1] * cache.page_size)} tokens may stay")
+    o = {} if out is None else out
+    kept = _out(o, "kept", lambda: torch.empty(B, cache.kv_heads, budget, dtype=_I32, device=device))
+    if not _is(kept, _I32, index) or kept.numel() != B * cache.kv_heads * budget:
+        _need(kept, "kept", _I32, B * cache.kv_heads * budget, device)
+    n = _out(o, "kv_len", lambda: torch.empty(B, dtype=_I32, device=device))
+    if not _is(n, _I32, index) or n.numel() != B:
+        _need(n, "kv_len", _I32, B, device)
+    g = _lib.SpecEvictBatch(B, shape[1], page_table.data_ptr(), kv_len.data_ptr(), width, new, budget, sinks, recent)
+    with _on(index):
+        code = _lib.lib().spec_kv_evict(g, cache.desc, mass.data_ptr(), kept.data_ptr(), n.data_ptr(),
+                                        _status_word(o, device_status, cache), _stream_handle(index))
+    if code:
+        check("spec_kv_evict", code)
     return o

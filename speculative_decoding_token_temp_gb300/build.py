@@ -20,10 +20,10 @@ LIB = os.path.join(PKG, "libspecverify.so")
 # the same library with every computed access bounds-checked (SPEC_BOUNDS_CHECK=1): a debug
 # variant for tests, which reports an access outside its buffer as SPEC_DEV_BOUNDS
 LIB_BOUNDS = os.path.join(PKG, "libspecverify_bounds.so")
-SOURCES = ["spec_verify.cu", "spec_kv.cu"]
+SOURCES = ["spec_verify.cu", "spec_kv.cu", "spec_kv_ops.cu"]
 HEADERS = ["kernels.cuh", "kernels_rows.cuh", "kernels_sample.cuh", "kernels_multi.cuh", "plan.h",
            "kernels_kv.cuh", "kernels_attn.cuh", "kernels_attn_tc.cuh",
-           "kernels_attn_prefix.cuh"]
+           "kernels_attn_prefix.cuh", "kernels_rope.cuh", "kernels_weigh.cuh", "kernels_evict.cuh", "kv_host.h"]
 PUBLIC = ["spec_verify.h", "spec_kv.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,0 +1,244 @@
+// The weight that cached tokens gather: for each token and kv head, the sum over a round's
+// rows and the head's query heads of the softmax weights exp(scale * q . k - lse), from the
+// log-sums that the attention has left.
+//
+// Only the keys are read. A warp takes 32 tokens and keeps their codes, widened to f16 (exact),
+// in registers as the first operand of m16n8k16 MMAs; the queries, f16 in shared memory, are
+// the second, 8 rows at a time. Which elements share a step of an MMA does not matter as long
+// as both operands agree, so a lane takes 16 neighbouring codes of a token by one load and no
+// data passes through shared memory on its way. The sum over rows ends in the lanes that hold
+// the token: no maxima, no second product, and the sum does not depend on what runs when.
+//
+// A bf16 query is, scaled by its row's power of two to below 2^15, exactly an f16 number down
+// to 2^-39 of the row's largest element; an fp32 query is two of them (22 bits).
+//
+// Few rows leave it bound by the keys' bytes, so the legacy MMA's rate is enough there. Many
+// rows (a window of 32 rows and 4 heads: 128 columns) are bound by it and by the exponentials.
+#pragma once
+
+#include "kernels_attn.cuh"
+
+namespace sv {
+
+constexpr int kWeighThreads = 128;
+constexpr int kWeighCols = 64;          // rows (query rows times heads of a kv head) at a time
+constexpr int kWeighAllRows = 1 << 14;  // a sequence's rows are one row block on the line of tiles
+
+struct WeighParams {
+  AttnParams a;
+  const float* lse;           // [R][Hq]
+  const int32_t* n_accepted;  // [B]: rows 0..n_accepted[b] count; null: all
+  float* mass;                // [num_pages][Hk][page_size]
+  float keep, scale;
+};
+
+// four e4m3 codes as two pairs of f16
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=&r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename E, int D>
+struct WeighShape {
+  static constexpr int kParts = sizeof(E) == 2 ? 1 : 2;
+  static constexpr int kStride = D + 8;  // halves of a row: neighbouring rows' 16-byte loads fall into different banks
+};
+
+// Columns c0 .. c0 + 63 of a segment's rows into shared memory, two threads a column.
+template <typename E, int D>
+__device__ __forceinline__ void weigh_stage(const WeighParams& p, const Seg& g, int counted, int c0, __half* q, float* rq, float* neg, int* lim) {
+  using T = WeighShape<E, D>;
+  const AttnParams& a = p.a;
+  const int col = threadIdx.x >> 1, part = threadIdx.x & 1, f = c0 + col, i = f / a.G;
+  bool here = f < g.rows * a.G && i < counted;
+  float x[D / 2];
+#pragma unroll
+  for (int k = 0; k < D / 2; ++k) x[k] = 0.f;
+  float lse = 0.f;
+  if (here) {
+    const int hq = g.h * a.G + f - i * a.G;
+    lse = __ldg(p.lse + (long long)(g.row0 + i) * a.Hq + hq);
+    here = fabsf(lse) <= 3.402823466e38f;  // a row that sees nothing, or whose sum is no number, adds nothing
+    const E* src = static_cast<const E*>(a.q) + (long long)(g.row0 + i) * a.q_row + (long long)hq * a.q_head + part * (D / 2);
+    if (here) {
+      if (((uintptr_t)src & 15) == 0) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          Raw8<E> r;
+          r.template load<true>(src + 8 * k);
+          r.floats(*reinterpret_cast<float(*)[8]>(x + 8 * k));
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          Raw8<E> r;
+          r.template load<false>(src + 8 * k);
+          r.floats(*reinterpret_cast<float(*)[8]>(x + 8 * k));
+        }
+      }
+    }
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < D / 2; ++k) top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
+  top = max(top, __shfl_xor_sync(kFull, top, 1));
+  const int e = max((int)(top >> 23) - 127, -100) - 14;  // the largest element comes to [2^14, 2^15)
+  const float inv = __int_as_float((127 - e) << 23);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(q + col * T::kStride + part * (D / 2));
+#pragma unroll
+  for (int k = 0; k < D / 2; k += 2) {
+    const float y0 = x[k] * inv, y1 = x[k + 1] * inv;
+    const uint32_t hi = pack_f16(y0, y1);
+    dst[k / 2] = hi;
+    if constexpr (T::kParts == 2) {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      dst[kWeighCols * T::kStride / 2 + k / 2] = pack_f16(y0 - h.x, y1 - h.y);
+    }
+  }
+  if (part == 0) {
+    rq[col] = here ? p.scale * __int_as_float((e + 127) << 23) : 0.f;
+    neg[col] = here ? -lse : 0.f;
+    lim[col] = here ? g.len - g.rows + i + 1 : 0;  // the row sees the tokens before this one
+  }
+}
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ WeighParams p) {
+  using T = WeighShape<E, D>;
+  constexpr int CH = D / 64;  // 16-byte pieces of a token in a lane
+  __shared__ Part s_part;
+  __shared__ __align__(16) __half s_q[T::kParts * kWeighCols * T::kStride];
+  __shared__ __align__(16) float s_rq[kWeighCols], s_neg[kWeighCols];
+  __shared__ __align__(16) int s_lim[kWeighCols];
+  const AttnParams& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t4 = lane & 3, g8 = lane >> 2;
+  griddep_wait();
+  griddep_launch();
+  const Part line = locate_block<kWeighAllRows>(a, s_part);
+  uint32_t bits = line.ok ? 0 : SPEC_DEV_OFFSETS;
+  Place at = line.at;
+  int left = line.ok ? line.end - line.begin : 0;
+  while (left > 0) {
+    const int b = at.b;
+    const Seg g = next_seg<kWeighAllRows>(a, at, left);
+    if (g.n == 0) continue;
+    int counted = g.rows;
+    bool bad = g.bad;
+    if (p.n_accepted != nullptr) {
+      const int n = __ldg(p.n_accepted + b);
+      bad |= n < 0 || n >= g.rows;
+      counted = min(n + 1, g.rows);
+    }
+    if (bad) {
+      bits |= SPEC_DEV_OFFSETS;
+      continue;
+    }
+    const int ctx = g.len - g.rows;
+    for (int c0 = 0; c0 == 0 || c0 < counted * a.G; c0 += kWeighCols) {
+      __syncthreads();
+      weigh_stage<E, D>(p, g, counted, c0, s_q, s_rq, s_neg, s_lim);
+      __syncthreads();
+      const int tiles_n = min(kWeighCols, counted * a.G - c0 + 7) / 8;  // of 8 columns
+      for (int tile = g.t0; tile < g.t0 + g.n; ++tile) {
+        const int tb = tile * kTile + warp * 32, own_t = tb + lane;
+        if (tb >= g.len) break;
+        // this lane's token: its place, exponent, weight so far
+        long long vec = -1;
+        if (own_t < g.len) {
+          const int page = __ldg(g.pages + (own_t >> a.page_shift));
+          if ((unsigned)page < (unsigned)a.num_pages)
+            vec = (((long long)page * a.Hk + g.h) << a.page_shift) + (own_t & ((1 << a.page_shift) - 1));
+          else
+            bits |= SPEC_DEV_PAGE;
+          if (vec >= 0 && !in_idx(vec, ((long long)a.num_pages * a.Hk) << a.page_shift, a.status)) vec = -1;
+        }
+        uint4 raw[4][CH];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const long long v = __shfl_sync(kFull, vec, g8 + 8 * m);
+#pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            raw[m][j] = make_uint4(0, 0, 0, 0);
+            if (v >= 0) raw[m][j] = __ldg(reinterpret_cast<const uint4*>(a.k + v * D) + 4 * j + t4);
+          }
+        }
+        const unsigned kb = vec >= 0 ? __ldg(a.k_exp + vec) : 0u;
+        const float old = vec < 0 || (c0 == 0 && (own_t >= ctx || p.keep == 0.f)) ? 0.f : p.mass[vec];
+        const float own_ks = exp_value(kb);
+        float ks[4], sum[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          ks[m] = __shfl_sync(kFull, own_ks, g8 + 8 * m);
+          sum[m] = 0.f;
+        }
+        uint32_t lo[4][CH][4], hi[4][CH][4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            const uint32_t w[4] = {raw[m][j].x, raw[m][j].y, raw[m][j].z, raw[m][j].w};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) widen4(w[s], lo[m][j][s], hi[m][j][s]);
+          }
+#pragma unroll 1
+        for (int nt = 0; nt < tiles_n; ++nt) {
+          float acc[2][4];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
+#pragma unroll
+          for (int part = T::kParts - 1; part >= 0; --part) {  // (the small parts first)
+            const uint4* q = reinterpret_cast<const uint4*>(s_q + (part * kWeighCols + nt * 8 + g8) * T::kStride + t4 * 16);
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+              const uint4 q0 = q[j * 8], q1 = q[j * 8 + 1];
+              const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                  mma_16816(acc[m], lo[2 * m][j][s], lo[2 * m + 1][j][s], hi[2 * m][j][s], hi[2 * m + 1][j][s], w[2 * s], w[2 * s + 1]);
+            }
+          }
+          const int col = nt * 8 + t4 * 2;
+          const float2 rq = *reinterpret_cast<const float2*>(s_rq + col), neg = *reinterpret_cast<const float2*>(s_neg + col);
+          const int2 lim = *reinterpret_cast<const int2*>(s_lim + col);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const float* c = &acc[m >> 1][(m & 1) * 2];
+            const int tok = tb + g8 + 8 * m;
+            // the difference in natural units, where it is small, then in binary ones
+            const float e0 = ex2(fmaf(c[0] * ks[m], rq.x, neg.x) * 1.4426950408889634f);
+            const float e1 = ex2(fmaf(c[1] * ks[m], rq.y, neg.y) * 1.4426950408889634f);
+            sum[m] += (tok < lim.x ? e0 : 0.f) + (tok < lim.y ? e1 : 0.f);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          sum[m] += __shfl_xor_sync(kFull, sum[m], 1);
+          sum[m] += __shfl_xor_sync(kFull, sum[m], 2);
+        }
+        // lane l's token is in the lanes of l % 8: the sum of number l / 8
+        float mine = 0.f;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float x = __shfl_sync(kFull, sum[m], (lane & 7) * 4);
+          if ((lane >> 3) == m) mine = x;
+        }
+        if (vec >= 0) p.mass[vec] = fmaf(c0 == 0 ? p.keep : 1.f, old, mine);
+      }
+    }
+  }
+  if (bits) atomicOr(a.status, bits);
+}
+
+}  // namespace sv

@@ -9,99 +9,11 @@
 #include "kernels_attn_prefix.cuh"
 #include "kernels_attn_tc.cuh"
 #include "kernels_kv.cuh"
+#include "kv_host.h"
 #include "spec_kv.h"
-
-#include <nvtx3/nvToolsExt.h>
-
-#include <atomic>
 
 namespace sv {
 namespace {
-
-struct KvRange {
-  explicit KvRange(const char* name) { nvtxRangePushA(name); }
-  ~KvRange() { nvtxRangePop(); }
-  KvRange(const KvRange&) = delete;
-  KvRange& operator=(const KvRange&) = delete;
-};
-
-inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
-inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-inline bool on(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
-
-int page_shift_of(int page_size) {
-  for (int s = 4; s <= 8; ++s)
-    if (page_size == 1 << s) return s;
-  return -1;
-}
-
-spec_status check_cache(const spec_kv_cache& c) {
-  if (c.num_pages < 1 || page_shift_of(c.page_size) < 0 || c.kv_heads < 1 || c.kv_heads > 256 ||
-      (c.head_dim != 64 && c.head_dim != 128))
-    return SPEC_ERR_INVALID_ARG;
-  if (!c.k || !c.v || !c.k_exp || !c.v_exp) return SPEC_ERR_INVALID_ARG;
-  if (!on(c.k, 16) || !on(c.v, 16) || !on(c.k_exp, 16) || !on(c.v_exp, 16)) return SPEC_ERR_INVALID_ARG;
-  return SPEC_OK;
-}
-
-spec_status check_rows(const spec_kv_rows& r) {
-  if (r.rows < 0 || r.sequences < 0 || r.pages_per_seq < 0 || r.rows > (1 << 22)) return SPEC_ERR_INVALID_ARG;
-  if (r.rows == 0) return SPEC_OK;
-  if (!r.row_seq || !r.row_pos || (r.sequences > 0 && r.pages_per_seq > 0 && !r.page_table)) return SPEC_ERR_INVALID_ARG;
-  if (!on(r.row_seq, 4) || !on(r.row_pos, 4) || !on(r.page_table, 4)) return SPEC_ERR_INVALID_ARG;
-  return SPEC_OK;
-}
-
-int sm_count() {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  const bool cached = dev >= 0 && dev < 64;
-  int n = cached ? known[dev].load(std::memory_order_relaxed) : 0;
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (cached) known[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
-// A launch with programmatic stream serialisation: the kernel may start while its
-// predecessor drains, and waits for it before it touches memory.
-template <typename... Args>
-cudaError_t start(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
-KvParams kv_params(const spec_kv_cache& c, const spec_kv_rows& r, uint32_t* status) {
-  KvParams p;
-  memset(&p, 0, sizeof(p));
-  p.k = static_cast<uint8_t*>(c.k);
-  p.v = static_cast<uint8_t*>(c.v);
-  p.k_exp = c.k_exp;
-  p.v_exp = c.v_exp;
-  p.num_pages = c.num_pages;
-  p.page_shift = page_shift_of(c.page_size);
-  p.Hk = c.kv_heads;
-  p.rows = r.rows;
-  p.seqs = r.sequences;
-  p.pps = r.pages_per_seq;
-  p.table = r.page_table;
-  p.row_seq = r.row_seq;
-  p.row_pos = r.row_pos;
-  p.status = status;
-  return p;
-}
 
 // The split of an append or a read: an item is one side of a row and as many of its heads as
 // a warp has on the way at once (four steps of what it holds side by side), or only what it
@@ -153,7 +65,6 @@ constexpr int kMaxGridS = 1024;  // largest grid of the 32-bit kernel (its works
 // tiles that a segment's beginning and end count for on the line of tiles (the tensor-core kernel, 3 / 4 / 5: 64 x 6 rows
 // 57.5 / 57.6 / 58.0 us, 256 x 1 row to 8192 327.7 / 328.6 / 330.7, 2304 rows behind 16384 541.1 / 539.5 / 540.6)
 constexpr int kSegCostT = 4, kSegCostS = 1, kSegCostP = 2;
-constexpr long long kMaxLine = 1LL << 30;  // a line of tiles is counted in ints
 constexpr int kMaxGridP = 160;   // of attn_prefix_kernel (one block an SM)
 // The prefix is widened and computed in 128-row tiles where that pays for the widening: from
 // this many row-tiles of keys on (rows that share keys x tiles x kv heads). Below, the 48- or
@@ -172,8 +83,6 @@ struct AttnLayout {
   long long tiles;     // of the prefix
   size_t part, cut, pre_part, pre_cut, pre_o, pre_lse, k16, v16, exp, total;
 };
-
-long long rows_of(const spec_attn_batch& g) { return (long long)g.total_draft + g.B; }
 
 // Rows of a row block of the tensor-core kernel, for `flat` rows that share keys: as few
 // blocks as hold them, each as small as that allows in steps of 8 from 16 on (what a softmax
@@ -227,62 +136,6 @@ AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dt
   if (L.wide) off = up256(off + sizeof(float) * (size_t)c.kv_heads * L.tiles);
   L.total = off;
   return L;
-}
-
-spec_status check_attn(const spec_attn_batch& g, const spec_kv_cache& c) {
-  const spec_status e = check_cache(c);
-  if (e != SPEC_OK) return e;
-  if (g.B < 0 || g.gamma < 0 || g.gamma > SPEC_MAX_GAMMA || g.total_draft < 0) return SPEC_ERR_INVALID_ARG;
-  if (g.cu_draft == nullptr && (long long)g.B * g.gamma != g.total_draft) return SPEC_ERR_INVALID_ARG;
-  if ((long long)g.total_draft > (long long)g.B * g.gamma) return SPEC_ERR_INVALID_ARG;
-  if (g.q_heads < 1 || g.q_heads % c.kv_heads != 0 || g.q_heads / c.kv_heads > 64) return SPEC_ERR_INVALID_ARG;
-  // flat rows (row * group + head) and row indices stay inside int
-  if (rows_of(g) * g.q_heads > (1LL << 30)) return SPEC_ERR_INVALID_ARG;
-  if (g.pages_per_seq < 0 || (long long)g.pages_per_seq * c.page_size > (1LL << 30)) return SPEC_ERR_INVALID_ARG;
-  if (g.prefix_len < 0 || g.prefix_len > (1 << 30)) return SPEC_ERR_INVALID_ARG;
-  if (!(g.scale > 0.f) || !isfinite(g.scale)) return SPEC_ERR_INVALID_ARG;
-  if (g.parent != nullptr) {
-    if (g.cu_draft != nullptr || g.gamma < 1 || g.gamma > SPEC_MAX_TREE_NODES) return SPEC_ERR_INVALID_ARG;
-    for (int j = 0; j < g.gamma; ++j)
-      if (g.parent[j] < -1 || g.parent[j] >= j) return SPEC_ERR_INVALID_ARG;
-  }
-  return SPEC_OK;
-}
-
-AttnParams attn_params(const spec_attn_batch& g, const spec_kv_cache& c, const void* q, int64_t q_row, int64_t q_head,
-                       void* o, float* lse, uint32_t* status, int seg_cost) {
-  AttnParams p;
-  memset(&p, 0, sizeof(p));
-  p.k = static_cast<const uint8_t*>(c.k);
-  p.v = static_cast<const uint8_t*>(c.v);
-  p.k_exp = c.k_exp;
-  p.v_exp = c.v_exp;
-  p.num_pages = c.num_pages;
-  p.page_shift = page_shift_of(c.page_size);
-  p.Hk = c.kv_heads;
-  p.Hq = g.q_heads;
-  p.G = g.q_heads / c.kv_heads;
-  p.q = q;
-  p.q_row = q_row;
-  p.q_head = q_head;
-  p.B = g.B;
-  p.gamma = g.gamma;
-  p.total_draft = g.total_draft;
-  p.R = (int)rows_of(g);
-  p.cu = g.cu_draft;
-  p.table = g.page_table;
-  p.pps = g.pages_per_seq;
-  p.kv_len = g.kv_len;
-  p.mask = g.parent != nullptr ? A_TREE : A_CHAIN;
-  p.c = g.scale * 1.4426950408889634f;
-  p.seg_cost = seg_cost;
-  p.o = o;
-  p.lse = lse;
-  p.status = status;
-  if (g.parent != nullptr)
-    for (int i = 0; i < g.gamma; ++i)
-      for (int j = i; j >= 0; j = g.parent[j]) p.sees[j] |= 1ull << i;
-  return p;
 }
 
 // The prefix as one sequence whose rows are all rows of the batch.
@@ -370,19 +223,6 @@ struct Maps {
   CUtensorMap k, v;
 };
 
-// Lets a kernel use `bytes` of shared memory on the current device, once (`done`: a bit a device).
-template <typename K>
-cudaError_t allow_smem(K kern, std::atomic<unsigned long long>& done, int bytes) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 template <int D, int NR>
 cudaError_t pass_tc(const AttnParams& p, long long grid, const Maps& m, cudaStream_t s) {
   auto kern = attn_tc_kernel<D, NR>;
@@ -449,6 +289,60 @@ cudaError_t attn_pass(spec_dtype dtype, int D, int nr, const AttnParams& p, long
   return D == 64 ? pass_tc_nr<64>(nr, p, grid, m, s) : pass_tc_nr<128>(nr, p, grid, m, s);
 }
 
+// Both entry points of the attention: checks, the passes.
+size_t attn_bytes(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype, int max_gamma) {
+  if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || check_attn(g, c, max_gamma) != SPEC_OK) return 0;
+  const AttnLayout L = attn_layout(g, c, dtype);
+  return L.line <= kMaxLine ? L.total : 0;
+}
+
+spec_status attend(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype, const void* q, int64_t q_row_stride,
+                   int64_t q_head_stride, void* o, float* lse, uint32_t* device_status, void* workspace, size_t workspace_bytes,
+                   spec_stream_t stream_, int max_gamma) {
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
+  const spec_status e = check_attn(g, c, max_gamma);
+  if (e != SPEC_OK) return e;
+  if (!device_status || !on(device_status, 4)) return SPEC_ERR_INVALID_ARG;
+  if (g.B == 0) return SPEC_OK;
+  const size_t es = dtype == SPEC_BF16 ? 2 : 4;
+  if (!q || !o || !on(q, es) || !on(o, 16) || !on(lse, 4) || q_row_stride < 0 || q_head_stride < 0)
+    return SPEC_ERR_INVALID_ARG;
+  if (!g.kv_len || !on(g.kv_len, 4) || !on(g.cu_draft, 4)) return SPEC_ERR_INVALID_ARG;
+  if ((g.pages_per_seq > 0 && !g.page_table) || !on(g.page_table, 4)) return SPEC_ERR_INVALID_ARG;
+  if ((g.prefix_len > 0 && !g.prefix_table) || !on(g.prefix_table, 4)) return SPEC_ERR_INVALID_ARG;
+  const AttnLayout L = attn_layout(g, c, dtype);
+  if (L.line > kMaxLine) return SPEC_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < L.total || !on(workspace, 256)) return SPEC_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  AttnParams p = attn_params(g, c, q, q_row_stride, q_head_stride, o, lse, device_status,
+                             dtype == SPEC_BF16 ? kSegCostT : kSegCostS);
+  p.part = reinterpret_cast<float*>(ws + L.part);
+  p.cut = reinterpret_cast<CutRec*>(ws + L.cut);
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (dtype == SPEC_BF16 && (!page_map(&maps.k, c.k, c) || !page_map(&maps.v, c.v, c))) return SPEC_ERR_CUDA;
+  cudaError_t err = cudaSuccess;
+  if (g.prefix_len > 0) {
+    float* pre_o = reinterpret_cast<float*>(ws + L.pre_o);
+    float* pre_lse = reinterpret_cast<float*>(ws + L.pre_lse);
+    AttnParams pp = prefix_params(p, g, c, pre_o, pre_lse);
+    pp.part = reinterpret_cast<float*>(ws + L.pre_part);
+    pp.cut = reinterpret_cast<CutRec*>(ws + L.pre_cut);
+    if (L.wide) pp.seg_cost = kSegCostP;
+    if (L.wide)
+      err = c.head_dim == 64 ? pass_prefix<64>(pp, c, L, ws, s) : pass_prefix<128>(pp, c, L, ws, s);
+    else
+      err = attn_pass(dtype, c.head_dim, L.pre_nr, pp, L.pre_grid, maps, s);
+    if (err != cudaSuccess) return SPEC_ERR_CUDA;
+    p.pre_o = pre_o;
+    p.pre_lse = pre_lse;
+    p.late_wait = 1;
+  }
+  err = attn_pass(dtype, c.head_dim, L.nr, p, L.grid, maps, s);
+  return err == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace sv
 
@@ -510,57 +404,28 @@ spec_status spec_kv_read(spec_kv_cache c, spec_kv_rows r, spec_dtype dtype, void
 }
 
 size_t spec_attention_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype) {
-  if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || check_attn(g, c) != SPEC_OK) return 0;
-  const AttnLayout L = attn_layout(g, c, dtype);
-  return L.line <= kMaxLine ? L.total : 0;
+  return attn_bytes(g, c, dtype, SPEC_MAX_GAMMA);
 }
 
 spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,
                            int64_t q_head_stride, void* o, float* lse, uint32_t* device_status, void* workspace,
                            size_t workspace_bytes, spec_stream_t stream_) {
   const KvRange range("spec_attention");
-  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
-  const spec_status e = check_attn(g, c);
-  if (e != SPEC_OK) return e;
-  if (!device_status || !on(device_status, 4)) return SPEC_ERR_INVALID_ARG;
-  if (g.B == 0) return SPEC_OK;
-  const size_t es = dtype == SPEC_BF16 ? 2 : 4;
-  if (!q || !o || !on(q, es) || !on(o, 16) || !on(lse, 4) || q_row_stride < 0 || q_head_stride < 0)
-    return SPEC_ERR_INVALID_ARG;
-  if (!g.kv_len || !on(g.kv_len, 4) || !on(g.cu_draft, 4)) return SPEC_ERR_INVALID_ARG;
-  if ((g.pages_per_seq > 0 && !g.page_table) || !on(g.page_table, 4)) return SPEC_ERR_INVALID_ARG;
-  if ((g.prefix_len > 0 && !g.prefix_table) || !on(g.prefix_table, 4)) return SPEC_ERR_INVALID_ARG;
-  const AttnLayout L = attn_layout(g, c, dtype);
-  if (L.line > kMaxLine) return SPEC_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < L.total || !on(workspace, 256)) return SPEC_ERR_WORKSPACE;
-  char* ws = static_cast<char*>(workspace);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
-  AttnParams p = attn_params(g, c, q, q_row_stride, q_head_stride, o, lse, device_status,
-                             dtype == SPEC_BF16 ? kSegCostT : kSegCostS);
-  p.part = reinterpret_cast<float*>(ws + L.part);
-  p.cut = reinterpret_cast<CutRec*>(ws + L.cut);
-  Maps maps;
-  memset(&maps, 0, sizeof(maps));
-  if (dtype == SPEC_BF16 && (!page_map(&maps.k, c.k, c) || !page_map(&maps.v, c.v, c))) return SPEC_ERR_CUDA;
-  cudaError_t err = cudaSuccess;
-  if (g.prefix_len > 0) {
-    float* pre_o = reinterpret_cast<float*>(ws + L.pre_o);
-    float* pre_lse = reinterpret_cast<float*>(ws + L.pre_lse);
-    AttnParams pp = prefix_params(p, g, c, pre_o, pre_lse);
-    pp.part = reinterpret_cast<float*>(ws + L.pre_part);
-    pp.cut = reinterpret_cast<CutRec*>(ws + L.pre_cut);
-    if (L.wide) pp.seg_cost = kSegCostP;
-    if (L.wide)
-      err = c.head_dim == 64 ? pass_prefix<64>(pp, c, L, ws, s) : pass_prefix<128>(pp, c, L, ws, s);
-    else
-      err = attn_pass(dtype, c.head_dim, L.pre_nr, pp, L.pre_grid, maps, s);
-    if (err != cudaSuccess) return SPEC_ERR_CUDA;
-    p.pre_o = pre_o;
-    p.pre_lse = pre_lse;
-    p.late_wait = 1;
-  }
-  err = attn_pass(dtype, c.head_dim, L.nr, p, L.grid, maps, s);
-  return err == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return attend(g, c, dtype, q, q_row_stride, q_head_stride, o, lse, device_status, workspace, workspace_bytes, stream_,
+                SPEC_MAX_GAMMA);
+}
+
+size_t spec_attention_chunk_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype) {
+  return g.parent == nullptr ? attn_bytes(g, c, dtype, SPEC_MAX_CHUNK_GAMMA) : 0;
+}
+
+spec_status spec_attention_chunk(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,
+                                 int64_t q_head_stride, void* o, float* lse, uint32_t* device_status, void* workspace,
+                                 size_t workspace_bytes, spec_stream_t stream_) {
+  const KvRange range("spec_attention_chunk");
+  if (g.parent != nullptr) return SPEC_ERR_INVALID_ARG;
+  return attend(g, c, dtype, q, q_row_stride, q_head_stride, o, lse, device_status, workspace, workspace_bytes, stream_,
+                SPEC_MAX_CHUNK_GAMMA);
 }
 
 }  // extern "C"
