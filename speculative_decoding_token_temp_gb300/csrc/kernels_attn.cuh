@@ -38,6 +38,7 @@ struct AttnParams {
   const int32_t* kv_len;  // null: every sequence has fixed_len tokens
   int fixed_len;
   int mask;
+  int skip_flat;            // sequences with at least so many rows (times G) are left out; 0: none
   int late_wait;            // the pass over the sequences' own tokens behind a prefix pass: see attn_tc_kernel
   int seg_cost;             // tiles that a segment's beginning and end count for
   float c;                  // scale * log2(e)
@@ -80,10 +81,13 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
 
 __device__ __forceinline__ int seq_ntiles(const SeqInfo& s) { return s.len > 0 ? (s.len - 1) / kTile + 1 : 1; }
 
+// Left to another pass (a batch of chunks that has both long and short ones).
+__device__ __forceinline__ bool skipped(const AttnParams& p, const SeqInfo& s) { return p.skip_flat > 0 && s.rows * p.G >= p.skip_flat; }
+
 // Tiles on the line of a sequence, over all its row blocks and kv heads.
 template <int NR>
 __device__ __forceinline__ int seq_tiles(const AttnParams& p, const SeqInfo& s) {
-  return (s.rows * p.G + NR - 1) / NR * p.Hk * (seq_ntiles(s) + p.seg_cost);
+  return skipped(p, s) ? 0 : (s.rows * p.G + NR - 1) / NR * p.Hk * (seq_ntiles(s) + p.seg_cost);
 }
 
 // A place on the line of tiles: sequence b, tile `off` of it.
@@ -175,7 +179,8 @@ struct Seg {
 template <int NR>
 __device__ __forceinline__ Seg next_seg(const AttnParams& p, Place& at, int& left) {
   Seg g;
-  const SeqInfo s = seq_info(p, at.b);
+  SeqInfo s = seq_info(p, at.b);
+  while (skipped(p, s)) s = seq_info(p, ++at.b);  // (there is one that is not: its tiles are `left`)
   g.row0 = s.row0, g.rows = s.rows, g.len = s.len, g.bad = s.bad;
   g.nt = seq_ntiles(s);
   const int nrb = (s.rows * p.G + NR - 1) / NR, line = g.nt + p.seg_cost;

@@ -26,7 +26,7 @@
 // heads: 410 us, and 17 us to widen (34 MB read, 67 MB written, mostly to L2).
 #pragma once
 
-#include "kernels_attn_tc.cuh"
+#include "kernels_attn_chunk.cuh"
 
 namespace sv {
 
@@ -35,7 +35,6 @@ constexpr int kPreThreads = 576;    // two softmax groups of eight warps, one wa
 constexpr int kPreSoft = 512;
 constexpr float kTopP = 8.f;        // a fresh reference puts a row's largest weight at 2^8 ...
 constexpr float kOverP = 15.f;      // ... and is renewed when one would pass 2^15
-constexpr int kValueShift = 6;      // the largest value of a tile comes to at most 448 * 2^6
 
 template <int D>
 struct PreShape {
@@ -47,13 +46,6 @@ struct PreShape {
   static constexpr int oV = oK + kStages * kTileBytes;
   static constexpr int kSmem = oV + kStages * kTileBytes + 1024;
   static constexpr int cS = 0, cO = 256;                 // columns of tensor memory: scores (and weights), values' sums
-};
-
-// The widened prefix in the workspace: [kv head][tokens, up to whole tiles][D].
-struct WideParams {
-  uint16_t *k16, *v16;
-  float* exp;  // [kv head][tile]: E, kSumShift more than the values are relative to (so the sums of 2^(x - m) are that much smaller)
-  int tiles;
 };
 
 // One block a tile and kv head. Its first 128 threads look the tokens up; then D / 8 lanes
@@ -181,7 +173,9 @@ struct PreShared {
   float top[2][2][128];  // of the halves of a row: the largest score, then the sum
 };
 
-template <int D>
+// CHUNK: the rows of every sequence over the prefix and its own tokens, causal (kernels_attn_chunk.cuh);
+// otherwise the rows of the whole batch over the prefix, whose part goes to dst_o and dst_lse.
+template <int D, bool CHUNK>
 __global__ void __launch_bounds__(kPreThreads, 1)
 attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WideParams wide,
                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
@@ -222,11 +216,23 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   }
   griddep_wait();
   griddep_launch();
-  const Part line = locate_block<NR>(p, sh.line);  // (one dense sequence: no cu)
+  const Part line = CHUNK ? locate_chunk(wide.c, sh.line) : locate_block<NR>(p, sh.line);  // (the prefix: one dense sequence, no cu)
   tc_after();
   const uint32_t tmem = sh.tmem;
   Place at = line.at;
   int left = line.end - line.begin;
+  if (CHUNK && !line.ok) fill_nan<uint16_t, D>(p, blockIdx.x, gridDim.x, kPreThreads);
+  auto next = [&]() -> WideSeg {
+    if constexpr (CHUNK) {
+      return next_chunk<NR>(p, wide.c, at, left);
+    } else {
+      WideSeg g;
+      static_cast<Seg&>(g) = next_seg<NR>(p, at, left);
+      g.w0 = 0;
+      return g;
+    }
+  };
+  auto wide_tile = [&](const WideSeg& g, int tile) { return CHUNK ? tile + (tile < wide.c.pre_tiles ? 0 : g.w0) : tile; };
 
   if (warp == 16) {
     // ---- the rings of tiles ----
@@ -234,9 +240,9 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       asm volatile("fence.proxy.async.global;" ::: "memory");  // the widened prefix was written with ordinary stores
       int gi = 0;
       while (left > 0) {
-        const Seg g = next_seg<NR>(p, at, left);
+        const WideSeg g = next();
         for (int k = 0; k < g.n; ++k, ++gi) {
-          const int st = gi % NST, row = (g.h * wide.tiles + g.t0 + k) * kTile;
+          const int st = gi % NST, row = (g.h * wide.tiles + wide_tile(g, g.t0 + k)) * kTile;
           const uint32_t bk = bar(sh.k_full[st]), bv = bar(sh.v_full[st]);
           if (gi >= NST) tc_wait_one(bar(sh.k_free[st]), (gi / NST - 1) & 1, gave_up, p.status);
           mbar_expect_arrive(bk, T::kTileBytes);
@@ -274,7 +280,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       mma_commit(bar(sh.s_full[w]));
     };
     while (left > 0) {
-      const Seg g = next_seg<NR>(p, at, left);
+      const WideSeg g = next();
       const int n = __shfl_sync(kFull, g.n, 0), groups = __shfl_sync(kFull, g.rows * p.G - g.f0 > 128 ? 2 : 1, 0);
       if (n == 0) continue;
       tc_wait(bar(sh.q_full), nseg & 1, gave_up, p.status);
@@ -333,7 +339,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     unsigned tiles_done = 0, ends = 0;
     if (tid == 0) p.cut[blockIdx.x].parts = 0;
     while (left > 0) {
-      const Seg g = next_seg<NR>(p, at, left);
+      const WideSeg g = next();
       if (g.n == 0) continue;
       if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, line.end, line.total);
       const int flat = g.rows * p.G, f = g.f0 + c;
@@ -341,7 +347,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       bool bad = false;
       {
         uint8_t* const q = mem + T::oQ + w * 128 * D * 2;
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(f / p.G) * p.q_row +
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(g.row0 + f / p.G) * p.q_row +
                               (long long)(g.h * p.G + f % p.G) * p.q_head;
         const bool vec = ((uintptr_t)src & 15) == 0;
 #pragma unroll
@@ -366,11 +372,22 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       fence_async();
       mbar_arrive(bar(sh.q_full));
       const bool have = flat - g.f0 > w * 128;  // this group has rows
+      // of the sequence's own tokens this row sees the first `own`
+      const int own = CHUNK ? (f < flat ? g.len - g.rows + f / p.G + 1 : 0) : g.len, pre_tiles = CHUNK ? wide.c.pre_tiles : 0;
       float m = 0.f, l = 0.f;
       if (have) {
         for (int k = 0; k < g.n; ++k, ++tiles_done) {
-          const int tile = g.t0 + k, valid = g.len - tile * kTile - half * 64;
-          const float E = __ldcg(wide.exp + (long long)g.h * wide.tiles + tile);
+          const int tile = g.t0 + k, valid = (tile < pre_tiles ? wide.c.pre_len - tile * kTile : own - (tile - pre_tiles) * kTile) - half * 64;
+          const long long info = (long long)g.h * wide.tiles + wide_tile(g, tile);
+          float E;
+          bool mixed = false;
+          if constexpr (CHUNK) {
+            const float2 e = __ldcg(wide.info + info);
+            E = e.x;
+            mixed = e.y != 0.f;
+          } else {
+            E = __ldcg(wide.exp + info);
+          }
           tc_wait(bar(sh.s_full[w]), tiles_done & 1, gave_up, p.status);
           tc_after();
           float s[64];
@@ -381,6 +398,13 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 64; ++i)
               if (i >= valid) s[i] = ninf;
+          }
+          if (CHUNK && mixed) {  // the values' exponents join the scores
+            const float inv = 1.f / p.c;
+            const float* ev = wide.ev + info * kTile + half * 64;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) s[i] = fmaf(__ldcg(ev + i), inv, s[i]);
+            E = 0.f;
           }
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -412,6 +436,11 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             }
           }
           const float off = E - m;
+          if (CHUNK && mixed) {
+            const float* ev = wide.ev + info * kTile + half * 64;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) l += ex2(fmaf(s[i], p.c, off) - __ldcg(ev + i));
+          }
           const f2 c2 = pack(p.c, p.c), off2 = pack(off, off);
           f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -434,10 +463,10 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           if (lane == 0) mbar_arrive(bar(sh.p_full[w]));
           float a, b;
           unpack(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
-          l += (a + b) * ex2(-E);
+          if (!(CHUNK && mixed)) l += (a + b) * ex2(-E);
         }
         // ---- the end of the stretch ----
-        if (bad) l = nan;
+        if (bad && (!CHUNK || g.t0 < pre_tiles || own > (g.t0 - pre_tiles) * kTile)) l = nan;  // (of a row that sees some of the stretch)
         bar_sync(pair_bar, 64);  // the last maxima are read
         sh.top[w][half][t] = l;
         bar_sync(pair_bar, 64);
@@ -447,25 +476,34 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         tc_after();
         const bool whole = g.n == g.nt;
         float* slot = whole ? nullptr : slot_of<NR, D>(p, 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0));
-        const long long idx = (long long)(f / p.G) * p.Hq + g.h * p.G + f % p.G;
+        const long long idx = (long long)(g.row0 + f / p.G) * p.Hq + g.h * p.G + f % p.G;
         Coef r{};
         if (!whole) {
           if (half == 0) {
-            slot[c] = m;
+            slot[c] = CHUNK && l == 0.f ? ninf : m;  // a row that saw nothing has no reference
             slot[NR + c] = l;
           }
         } else if (f < flat) {
-          r = row_coef(ninf, m, l, false);
+          r = row_coef(ninf, m, l, CHUNK && g.bad);
           if (half == 0) finish_lse(p, idx, r);
         }
-        float* dst = whole ? p.dst_o + idx * D : slot + 2 * NR + c * D;
+        float* dst = whole ? (CHUNK ? nullptr : p.dst_o + idx * D) : slot + 2 * NR + c * D;
         const float scale = (whole ? r.a : 1.f) * (1.f / (1 << (kValueShift + kSumShift)));
 #pragma unroll 1
         for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
           float o[32];
           tc_ld32(tO + i, o);
           tc_wait_ld();
-          if (f < flat && in_idx(idx, (long long)p.R * p.Hq, p.status)) {
+          if (CHUNK && whole) {
+            if (f < flat && in_idx(idx, (long long)p.R * p.Hq, p.status)) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                const float x[8] = {o[j] * scale,     o[j + 1] * scale, o[j + 2] * scale, o[j + 3] * scale,
+                                    o[j + 4] * scale, o[j + 5] * scale, o[j + 6] * scale, o[j + 7] * scale};
+                store8(static_cast<uint16_t*>(p.o) + idx * D + i + j, x);
+              }
+            }
+          } else if (f < flat && in_idx(idx, (long long)p.R * p.Hq, p.status)) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
               *reinterpret_cast<float4*>(dst + i + j) = make_float4(o[j] * scale, o[j + 1] * scale, o[j + 2] * scale, o[j + 3] * scale);

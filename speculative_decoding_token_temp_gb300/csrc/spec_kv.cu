@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "kernels_attn.cuh"
+#include "kernels_attn_chunk.cuh"
 #include "kernels_attn_prefix.cuh"
 #include "kernels_attn_tc.cuh"
 #include "kernels_kv.cuh"
@@ -72,6 +73,10 @@ constexpr int kMaxGridP = 160;   // of attn_prefix_kernel (one block an SM)
 // 288 rows x 2000 tokens 34 / 43 us, 1152 x 2000 51 / 57, 576 x 8192 66 / 69, 1152 x 8192
 // 105 / 83; head_dim 64, 576 x 2000 34.5 / 35.6, 1152 x 2000 51 / 47, 576 x 8192 64 / 51.
 constexpr long long kWideWork128 = 300000, kWideWork64 = 75000;
+// A chunk's sequences with at least so many rows (times heads of a kv head) are widened and
+// computed in 256-row blocks, the others in the 48- or 32-row blocks of attn_tc_kernel.
+constexpr int kChunkFlat = 256;
+constexpr size_t kChunkBytes = (size_t)48 << 30;  // most that a chunk's widened keys and values may take; past it, narrow blocks
 constexpr int kMaxGridT = 512;   // of the tensor-core kernel (two blocks an SM)
 
 struct AttnLayout {
@@ -81,7 +86,11 @@ struct AttnLayout {
   long long line;      // the longer pass's line of tiles, at most
   bool wide;           // the prefix widened and computed by attn_prefix_kernel
   long long tiles;     // of the prefix
+  bool chunk;          // long chunks widened and computed by attn_prefix_kernel's CHUNK form
+  bool chunk_only;     // ... and so all sequences
+  long long chunk_grid, chunk_tiles, chunk_entries;  // at most
   size_t part, cut, pre_part, pre_cut, pre_o, pre_lse, k16, v16, exp, total;
+  size_t c_part, c_cut, c_k16, c_v16, c_info, c_ev, c_entry, c_first, c_head;
 };
 
 // Rows of a row block of the tensor-core kernel, for `flat` rows that share keys: as few
@@ -94,12 +103,53 @@ int tc_rows(long long flat, int head_dim) {
   return per <= 16 ? 16 : (int)(cdiv(per, 8) * 8);
 }
 
-AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype) {
+// The CHUNK pass: what it takes of the workspace from `off` on, and whether the call uses it.
+void chunk_layout(AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& c, size_t& off) {
+  const long long G = g.q_heads / c.kv_heads, flat = rows_of(g) * G, pre = cdiv(g.prefix_len, kTile);
+  const long long most = cdiv((long long)g.pages_per_seq * c.page_size, kTile), nt = most > 1 ? most : 1;
+  L.chunk = false;
+  if ((long long)(g.gamma + 1) * G < kChunkFlat) return;
+  L.chunk_tiles = pre + g.B * nt;
+  L.chunk_entries = flat / kRowsP + g.B;
+  const long long line = L.chunk_entries * c.kv_heads * (pre + nt + kSegCostP);
+  const size_t wide = (size_t)2 * c.kv_heads * L.chunk_tiles * kTile * c.head_dim;
+  if (line > kMaxLine || L.chunk_tiles * c.kv_heads > (1LL << 23) || 2 * wide > kChunkBytes) return;  // (tokens of the widened memory count in ints)
+  L.chunk = true;
+  // with a prefix the narrow pass would be two; without one it is there for the short sequences of a packed batch
+  L.chunk_only = g.cu_draft == nullptr || g.prefix_len > 0;
+  L.chunk_grid = line < kMaxGridP ? line : kMaxGridP;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = up256(off + bytes);
+    return at;
+  };
+  L.c_part = take(sizeof(float) * (size_t)(2 * L.chunk_grid * kRowsP) * (c.head_dim + 2));
+  L.c_cut = take(sizeof(CutRec) * (size_t)L.chunk_grid);
+  L.c_k16 = take(wide);
+  L.c_v16 = take(wide);
+  L.c_info = take(sizeof(float2) * (size_t)(c.kv_heads * L.chunk_tiles));
+  L.c_ev = take(sizeof(float) * (size_t)(c.kv_heads * L.chunk_tiles) * kTile);
+  L.c_entry = take(sizeof(ChunkEntry) * (size_t)L.chunk_entries);
+  L.c_first = take(sizeof(int) * (size_t)g.B);
+  L.c_head = take(sizeof(ChunkHead));
+}
+
+// `chunk`: a call of spec_attention_chunk.
+AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype, bool chunk) {
   AttnLayout L;
   const int G = g.q_heads / c.kv_heads;
+  size_t off = 0;
+  L.chunk = L.chunk_only = false;
+  if (chunk && dtype == SPEC_BF16) chunk_layout(L, g, c, off);
+  if (L.chunk && L.chunk_only) {
+    L.total = off;
+    L.line = 0;
+    return L;
+  }
   const bool tc = dtype == SPEC_BF16;
   const long long cap = tc ? kMaxGridT : kMaxGridS;
-  L.nr = tc ? tc_rows((long long)(g.gamma + 1) * G, c.head_dim) : kRowsS;
+  const long long most_flat = L.chunk ? kChunkFlat - 1 : (long long)(g.gamma + 1) * G;  // rows that share keys in the narrow pass
+  L.nr = tc ? tc_rows(most_flat, c.head_dim) : kRowsS;
   const long long flat = rows_of(g) * G;
   L.tiles = cdiv(g.prefix_len, kTile);
   L.wide = tc && flat >= 128 && flat * L.tiles * c.kv_heads >= (c.head_dim == 64 ? kWideWork64 : kWideWork128);
@@ -107,14 +157,13 @@ AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dt
   const long long most_tiles = cdiv((long long)g.pages_per_seq * c.page_size, kTile);
   const long long nt = most_tiles > 1 ? most_tiles : 1;
   const int more = tc ? kSegCostT : kSegCostS;  // a block for every tile of the line at most
-  const long long own = (long long)g.B * cdiv((long long)(g.gamma + 1) * G, L.nr) * c.kv_heads * (nt + more);
+  const long long own = (long long)g.B * cdiv(most_flat, L.nr) * c.kv_heads * (nt + more);
   const long long pre = g.prefix_len > 0 ? cdiv(rows_of(g) * G, L.pre_nr) * c.kv_heads * (cdiv(g.prefix_len, kTile) + more) : 0;
   L.line = own > pre ? own : pre;
   L.grid = own < cap ? own : cap;
   const long long pre_cap = L.wide ? kMaxGridP : cap;
   L.pre_grid = pre < pre_cap ? pre : pre_cap;
   // each pass has parts and records of its own: the second may begin before the first has ended
-  size_t off = 0;
   L.part = off;
   off = up256(off + sizeof(float) * (size_t)(2 * L.grid * L.nr) * (c.head_dim + 2));
   L.cut = off;
@@ -262,6 +311,7 @@ bool wide_map(CUtensorMap* m, void* base, const spec_kv_cache& c, long long rows
 template <int D>
 cudaError_t pass_prefix(const AttnParams& p, const spec_kv_cache& c, const AttnLayout& L, char* ws, cudaStream_t s) {
   WideParams w;
+  memset(&w, 0, sizeof(w));
   w.k16 = reinterpret_cast<uint16_t*>(ws + L.k16);
   w.v16 = reinterpret_cast<uint16_t*>(ws + L.v16);
   w.exp = reinterpret_cast<float*>(ws + L.exp);
@@ -273,12 +323,53 @@ cudaError_t pass_prefix(const AttnParams& p, const spec_kv_cache& c, const AttnL
     return cudaErrorInvalidValue;
   cudaError_t e = start(widen_kernel<D>, dim3((unsigned)L.tiles, (unsigned)c.kv_heads), 256, 0, s, p, w);
   if (e != cudaSuccess) return e;
-  auto kern = attn_prefix_kernel<D>;
+  auto kern = attn_prefix_kernel<D, false>;
   static std::atomic<unsigned long long> done{0};
   if ((e = allow_smem(kern, done, PreShape<D>::kSmem)) != cudaSuccess) return e;
   const long long sms = sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
   const int n = (int)(L.pre_grid < sms ? L.pre_grid : sms);
+  e = start(kern, dim3((unsigned)n), kPreThreads, PreShape<D>::kSmem, s, p, w, m.k, m.v);
+  return e != cudaSuccess ? e : launch_merge<uint16_t, D, kRowsP>(p, n, s);
+}
+
+// Long chunks: the plan, the widening, the attention, the joining of cut segments.
+template <int D>
+cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const spec_kv_cache& c, const AttnLayout& L, char* ws, cudaStream_t s) {
+  AttnParams p = own;
+  p.part = reinterpret_cast<float*>(ws + L.c_part);
+  p.cut = reinterpret_cast<CutRec*>(ws + L.c_cut);
+  p.seg_cost = kSegCostP;
+  WideParams w;
+  memset(&w, 0, sizeof(w));
+  w.k16 = reinterpret_cast<uint16_t*>(ws + L.c_k16);
+  w.v16 = reinterpret_cast<uint16_t*>(ws + L.c_v16);
+  w.tiles = (int)L.chunk_tiles;
+  w.info = reinterpret_cast<float2*>(ws + L.c_info);
+  w.ev = reinterpret_cast<float*>(ws + L.c_ev);
+  w.c.head = reinterpret_cast<ChunkHead*>(ws + L.c_head);
+  w.c.entry = reinterpret_cast<ChunkEntry*>(ws + L.c_entry);
+  w.c.first = reinterpret_cast<int*>(ws + L.c_first);
+  w.c.pre_table = g.prefix_table;
+  w.c.pre_len = g.prefix_len;
+  w.c.pre_tiles = (int)cdiv(g.prefix_len, kTile);
+  w.c.min_flat = L.chunk_only ? 0 : kChunkFlat;
+  Maps m;
+  const long long rows = L.chunk_tiles * kTile * c.kv_heads;
+  if (!wide_map(&m.k, w.k16, c, rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) ||
+      !wide_map(&m.v, w.v16, c, rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
+    return cudaErrorInvalidValue;
+  const long long sms = sm_count();
+  if (sms < 1) return cudaErrorInvalidConfiguration;
+  cudaError_t e = start(chunk_plan_kernel<kRowsP>, dim3(1), kPlanThreads, 0, s, p, w.c);
+  if (e != cudaSuccess) return e;
+  const long long units = L.chunk_tiles * c.kv_heads;
+  e = start(chunk_widen_kernel<D>, dim3((unsigned)(units < 8 * sms ? units : 8 * sms)), kWidenThreads, 0, s, p, w);
+  if (e != cudaSuccess) return e;
+  auto kern = attn_prefix_kernel<D, true>;
+  static std::atomic<unsigned long long> done{0};
+  if ((e = allow_smem(kern, done, PreShape<D>::kSmem)) != cudaSuccess) return e;
+  const int n = (int)(L.chunk_grid < sms ? L.chunk_grid : sms);
   e = start(kern, dim3((unsigned)n), kPreThreads, PreShape<D>::kSmem, s, p, w, m.k, m.v);
   return e != cudaSuccess ? e : launch_merge<uint16_t, D, kRowsP>(p, n, s);
 }
@@ -290,15 +381,15 @@ cudaError_t attn_pass(spec_dtype dtype, int D, int nr, const AttnParams& p, long
 }
 
 // Both entry points of the attention: checks, the passes.
-size_t attn_bytes(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype, int max_gamma) {
+size_t attn_bytes(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype, int max_gamma, bool chunk) {
   if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || check_attn(g, c, max_gamma) != SPEC_OK) return 0;
-  const AttnLayout L = attn_layout(g, c, dtype);
+  const AttnLayout L = attn_layout(g, c, dtype, chunk);
   return L.line <= kMaxLine ? L.total : 0;
 }
 
 spec_status attend(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype, const void* q, int64_t q_row_stride,
                    int64_t q_head_stride, void* o, float* lse, uint32_t* device_status, void* workspace, size_t workspace_bytes,
-                   spec_stream_t stream_, int max_gamma) {
+                   spec_stream_t stream_, int max_gamma, bool chunk) {
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_DTYPE;
   const spec_status e = check_attn(g, c, max_gamma);
   if (e != SPEC_OK) return e;
@@ -310,13 +401,19 @@ spec_status attend(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype 
   if (!g.kv_len || !on(g.kv_len, 4) || !on(g.cu_draft, 4)) return SPEC_ERR_INVALID_ARG;
   if ((g.pages_per_seq > 0 && !g.page_table) || !on(g.page_table, 4)) return SPEC_ERR_INVALID_ARG;
   if ((g.prefix_len > 0 && !g.prefix_table) || !on(g.prefix_table, 4)) return SPEC_ERR_INVALID_ARG;
-  const AttnLayout L = attn_layout(g, c, dtype);
+  const AttnLayout L = attn_layout(g, c, dtype, chunk);
   if (L.line > kMaxLine) return SPEC_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < L.total || !on(workspace, 256)) return SPEC_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   AttnParams p = attn_params(g, c, q, q_row_stride, q_head_stride, o, lse, device_status,
                              dtype == SPEC_BF16 ? kSegCostT : kSegCostS);
+  if (L.chunk) {
+    const cudaError_t err = c.head_dim == 64 ? pass_chunk<64>(p, g, c, L, ws, s) : pass_chunk<128>(p, g, c, L, ws, s);
+    if (err != cudaSuccess) return SPEC_ERR_CUDA;
+    if (L.chunk_only) return SPEC_OK;
+    p.skip_flat = kChunkFlat;
+  }
   p.part = reinterpret_cast<float*>(ws + L.part);
   p.cut = reinterpret_cast<CutRec*>(ws + L.cut);
   Maps maps;
@@ -404,7 +501,7 @@ spec_status spec_kv_read(spec_kv_cache c, spec_kv_rows r, spec_dtype dtype, void
 }
 
 size_t spec_attention_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype) {
-  return attn_bytes(g, c, dtype, SPEC_MAX_GAMMA);
+  return attn_bytes(g, c, dtype, SPEC_MAX_GAMMA, false);
 }
 
 spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,
@@ -412,11 +509,11 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
                            size_t workspace_bytes, spec_stream_t stream_) {
   const KvRange range("spec_attention");
   return attend(g, c, dtype, q, q_row_stride, q_head_stride, o, lse, device_status, workspace, workspace_bytes, stream_,
-                SPEC_MAX_GAMMA);
+                SPEC_MAX_GAMMA, false);
 }
 
 size_t spec_attention_chunk_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype) {
-  return g.parent == nullptr ? attn_bytes(g, c, dtype, SPEC_MAX_CHUNK_GAMMA) : 0;
+  return g.parent == nullptr ? attn_bytes(g, c, dtype, SPEC_MAX_CHUNK_GAMMA, true) : 0;
 }
 
 spec_status spec_attention_chunk(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,
@@ -425,7 +522,7 @@ spec_status spec_attention_chunk(spec_attn_batch g, spec_kv_cache c, spec_dtype 
   const KvRange range("spec_attention_chunk");
   if (g.parent != nullptr) return SPEC_ERR_INVALID_ARG;
   return attend(g, c, dtype, q, q_row_stride, q_head_stride, o, lse, device_status, workspace, workspace_bytes, stream_,
-                SPEC_MAX_CHUNK_GAMMA);
+                SPEC_MAX_CHUNK_GAMMA, true);
 }
 
 }  // extern "C"

@@ -146,3 +146,52 @@ def test_a_short_chunk_is_a_round(dev):  # noqa: F811
     for out in (c.call(), A.Case.call(c)):
         assert int(out["device_status"][0]) == 0
         U.compare(out["o"], out["lse"], c.ref(), c.dtype, 300)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("spread", [12, 30, 70])
+def test_values_of_very_different_size(dev, dim, spread):  # noqa: F811
+    """Tokens whose values are 2^spread times their neighbours': rows before them do not see them and keep their places."""
+    c = Case(dev, [300, 420], [300, 270], heads=8, kv_heads=2, dim=dim, page=32, seed=3)
+    for b, t in ((0, 100), (0, 255), (1, 333)):
+        c.exps[1][c.table[b][t // 32], 1, t % 32] += spread
+    c.exps[1][c.table[1][40 // 32], 0, 40 % 32] -= min(spread, 60)
+    c.check()
+
+
+def test_infinite_queries_and_rows_that_see_nothing(dev):  # noqa: F811
+    c = Case(dev, [290, 200], [290, 270], heads=4, kv_heads=1, dim=64)
+    c.q[5, 1, 3], c.q[100, 2, 0], c.q[300, 0, 9], c.q[500, 3, 1] = np.inf, np.nan, np.inf, -np.inf  # (row 300 sees nothing)
+    out = c.call()
+    assert int(out["device_status"][0]) == 0
+    c.q[300, 0, 9] = 0  # what it holds does not matter (and an infinity has no bound)
+    U.compare(out["o"], out["lse"], c.ref(), c.dtype, 290)
+    bad = torch.isnan(out["o"]).any(-1)
+    assert bad[5, 1] and bad[100, 2] and bad[500, 3] and int(bad.sum()) == 3
+
+
+@pytest.mark.parametrize("batch,rows,ctx", [(40, 70, 100), (3, 900, 2000), (1100, 65, 0)])
+def test_many_and_long_sequences_repeat_bit_for_bit(dev, batch, rows, ctx):  # noqa: F811
+    """More sequences than threads plan at once, cut segments; some sequences against the restatement."""
+    lens = [rows + ctx * (i % 3) // 2 for i in range(batch)]
+    c = Case(dev, lens, [rows] * batch, heads=4, kv_heads=1, dim=64, page=16, size=0.7)
+    a, b = c.call(), c.call()
+    assert int(a["device_status"][0]) == 0 and torch.equal(a["o"], b["o"]) and torch.equal(a["lse"], b["lse"])
+    saved, U.visible = U.visible, visible
+    try:
+        for i in {0, batch // 2, batch - 1}:
+            at = np.arange(i * rows, (i + 1) * rows)
+            ref = U.attention(c.q[at].double().numpy(), c.cache(), [c.table[i]], [lens[i]], [rows])
+            U.compare(a["o"][at], a["lse"][at], ref, c.dtype, lens[i])
+    finally:
+        U.visible = saved
+
+
+def test_bounds_checked_build_of_a_ragged_batch(dev):  # noqa: F811
+    rows = [1, 400, 3, 64, 1, 129]
+    c = Case(dev, [900, 400, 300, 64, 1, 500], rows, heads=8, kv_heads=2, dim=128, page=64)
+    a = c.check()
+    with checked_build():
+        b = c.call()
+        assert int(b["device_status"][0]) == 0
+    assert torch.equal(a["o"], b["o"]) and torch.equal(a["lse"], b["lse"])
