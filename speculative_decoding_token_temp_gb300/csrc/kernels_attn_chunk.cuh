@@ -159,6 +159,7 @@ struct WideParams {
   // chunks
   float2* info;  // [kv head][tile]: E, and whether the tile is mixed
   float* ev;     // [kv head][tile][128]: a mixed tile's E, token by token
+  int q_tma;     // queries come by TMA (kv head groups of a power of two, rows on the 16-byte grid)
   ChunkParams c;
 };
 

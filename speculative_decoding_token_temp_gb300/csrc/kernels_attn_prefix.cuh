@@ -162,12 +162,19 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ void tma_queries(uint32_t dst, const CUtensorMap* map, int x, int head, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(head), "r"(row), "r"(bar)
+      : "memory");
+}
+
 template <int D>
 struct PreShared {
   using T = PreShape<D>;
   Part line;
   uint64_t k_full[T::kStages], k_free[T::kStages], v_full[T::kStages], v_free[T::kStages];
-  uint64_t q_full, drained, s_full[2], p_full[2], o_done[2];
+  uint64_t q_full, q_free, drained, s_full[2], p_full[2], o_done[2];
   uint32_t tmem;
   int gave_up;
   float top[2][2][128];  // of the halves of a row: the largest score, then the sum
@@ -178,7 +185,8 @@ struct PreShared {
 template <int D, bool CHUNK>
 __global__ void __launch_bounds__(kPreThreads, 1)
 attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WideParams wide,
-                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+                   const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ CUtensorMap map_q) {
   using T = PreShape<D>;
   constexpr int NR = kRowsP, NST = T::kStages;
   extern __shared__ uint8_t dyn[];
@@ -197,7 +205,8 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       mbar_init(bar(sh.v_full[i]), 1);
       mbar_init(bar(sh.v_free[i]), 1);
     }
-    mbar_init(bar(sh.q_full), kPreSoft);
+    mbar_init(bar(sh.q_full), CHUNK && wide.q_tma ? 1 : kPreSoft);
+    mbar_init(bar(sh.q_free), 1);
     mbar_init(bar(sh.drained), 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(sh.s_full[w]), 1);
@@ -238,9 +247,20 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     // ---- the rings of tiles ----
     if (lane == 0) {
       asm volatile("fence.proxy.async.global;" ::: "memory");  // the widened prefix was written with ordinary stores
-      int gi = 0;
+      int gi = 0, nseg = 0;
       while (left > 0) {
         const WideSeg g = next();
+        if (CHUNK && wide.q_tma && g.n > 0) {
+          // the stretch's queries, as soon as the last scores of the one before are computed: while its ends are worked on
+          const int groups = g.rows * p.G - g.f0 > 128 ? 2 : 1;
+          if (nseg > 0) tc_wait_one(bar(sh.q_free), (nseg - 1) & 1, gave_up, p.status);
+          ++nseg;
+          mbar_expect_arrive(bar(sh.q_full), groups * 128 * D * 2);
+          for (int w = 0; w < groups; ++w)
+#pragma unroll
+            for (int a = 0; a < T::kAtoms; ++a)
+              tma_queries(base + T::oQ + w * 128 * D * 2 + a * 16384, &map_q, a * 64, g.h * p.G, g.row0 + (g.f0 + w * 128) / p.G, bar(sh.q_full));
+        }
         for (int k = 0; k < g.n; ++k, ++gi) {
           const int st = gi % NST, row = (g.h * wide.tiles + wide_tile(g, g.t0 + k)) * kTile;
           const uint32_t bk = bar(sh.k_full[st]), bv = bar(sh.v_full[st]);
@@ -257,6 +277,8 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
       }
       // no copy is left in flight when the block ends, even after a wait that gave up
+      for (int it = 0; nseg > 0 && it < kTcPollLimit && !mbar_try_wait(bar(sh.q_full), (nseg - 1) & 1); ++it) {
+      }
       for (int i = 0; i < NST; ++i)
         for (int it = 0; gi > i && it < kTcPollLimit && !(mbar_try_wait(bar(sh.k_full[i]), ((gi - 1 - i) / NST) & 1) &&
                                                          mbar_try_wait(bar(sh.v_full[i]), ((gi - 1 - i) / NST) & 1)); ++it) {
@@ -292,6 +314,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         scores(0, gi);
         if (groups == 2) scores(1, gi);
         mma_commit(bar(sh.k_free[gi % NST]));
+        if (CHUNK && n == 1) mma_commit(bar(sh.q_free));
       }
       __syncwarp();
       for (int k = 0; k < n; ++k, ++gi) {
@@ -318,6 +341,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             if (w + 1 == groups) {
               mma_commit(bar(sh.v_free[st]));
               if (k + 1 < n) mma_commit(bar(sh.k_free[(gi + 1) % NST]));
+              if (CHUNK && k + 2 == n) mma_commit(bar(sh.q_free));
             }
           }
           __syncwarp();
@@ -344,8 +368,8 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, line.end, line.total);
       const int flat = g.rows * p.G, f = g.f0 + c;
       // half of this thread's query row into shared memory, swizzled
-      bool bad = false;
-      {
+      bool bad = false;  // a query that is no finite number
+      if (!(CHUNK && wide.q_tma)) {
         uint8_t* const q = mem + T::oQ + w * 128 * D * 2;
         const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(g.row0 + f / p.G) * p.q_row +
                               (long long)(g.h * p.G + f % p.G) * p.q_head;
@@ -368,9 +392,9 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           for (int i = 0; i < 4; ++i) bad |= (x[i] & 0x7f80u) == 0x7f80u || (x[i] & 0x7f800000u) == 0x7f800000u;
           *reinterpret_cast<uint4*>(q + (ch >> 3) * 16384 + t * 128 + (((ch & 7) ^ (t & 7)) * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
         }
+        fence_async();
+        mbar_arrive(bar(sh.q_full));
       }
-      fence_async();
-      mbar_arrive(bar(sh.q_full));
       const bool have = flat - g.f0 > w * 128;  // this group has rows
       // of the sequence's own tokens this row sees the first `own`
       const int own = CHUNK ? (f < flat ? g.len - g.rows + f / p.G + 1 : 0) : g.len, pre_tiles = CHUNK ? wide.c.pre_tiles : 0;
@@ -466,7 +490,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           if (!(CHUNK && mixed)) l += (a + b) * ex2(-E);
         }
         // ---- the end of the stretch ----
-        if (bad && (!CHUNK || g.t0 < pre_tiles || own > (g.t0 - pre_tiles) * kTile)) l = nan;  // (of a row that sees some of the stretch)
+        if (!CHUNK && bad) l = nan;
         bar_sync(pair_bar, 64);  // the last maxima are read
         sh.top[w][half][t] = l;
         bar_sync(pair_bar, 64);
@@ -511,7 +535,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
         tc_before();
       }
-      bar_sync(9, kPreSoft);  // both groups are done with the queries' memory
+      if (!(CHUNK && wide.q_tma)) bar_sync(9, kPreSoft);  // both groups are done with the queries' memory
     }
   }
   tc_before();

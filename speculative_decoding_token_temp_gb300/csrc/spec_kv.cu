@@ -65,7 +65,7 @@ constexpr int kMaxGridS = 1024;  // largest grid of the 32-bit kernel (its works
 
 // tiles that a segment's beginning and end count for on the line of tiles (the tensor-core kernel, 3 / 4 / 5: 64 x 6 rows
 // 57.5 / 57.6 / 58.0 us, 256 x 1 row to 8192 327.7 / 328.6 / 330.7, 2304 rows behind 16384 541.1 / 539.5 / 540.6)
-constexpr int kSegCostT = 4, kSegCostS = 1, kSegCostP = 2;
+constexpr int kSegCostT = 4, kSegCostS = 1, kSegCostP = 2, kSegCostC = 4;
 constexpr int kMaxGridP = 160;   // of attn_prefix_kernel (one block an SM)
 // The prefix is widened and computed in 128-row tiles where that pays for the widening: from
 // this many row-tiles of keys on (rows that share keys x tiles x kv heads). Below, the 48- or
@@ -111,7 +111,7 @@ void chunk_layout(AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& 
   if ((long long)(g.gamma + 1) * G < kChunkFlat) return;
   L.chunk_tiles = pre + g.B * nt;
   L.chunk_entries = flat / kRowsP + g.B;
-  const long long line = L.chunk_entries * c.kv_heads * (pre + nt + kSegCostP);
+  const long long line = L.chunk_entries * c.kv_heads * (pre + nt + kSegCostC);
   const size_t wide = (size_t)2 * c.kv_heads * L.chunk_tiles * kTile * c.head_dim;
   if (line > kMaxLine || L.chunk_tiles * c.kv_heads > (1LL << 23) || 2 * wide > kChunkBytes) return;  // (tokens of the widened memory count in ints)
   L.chunk = true;
@@ -329,8 +329,22 @@ cudaError_t pass_prefix(const AttnParams& p, const spec_kv_cache& c, const AttnL
   const long long sms = sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
   const int n = (int)(L.pre_grid < sms ? L.pre_grid : sms);
-  e = start(kern, dim3((unsigned)n), kPreThreads, PreShape<D>::kSmem, s, p, w, m.k, m.v);
+  e = start(kern, dim3((unsigned)n), kPreThreads, PreShape<D>::kSmem, s, p, w, m.k, m.v, m.v);
   return e != cudaSuccess ? e : launch_merge<uint16_t, D, kRowsP>(p, n, s);
+}
+
+// The queries as a tensor of rows and heads: a load takes 64 elements of 128 flat rows. False where
+// their layout does not allow it.
+bool query_map(CUtensorMap* m, const AttnParams& p, int D) {
+  memset(m, 0, sizeof(*m));
+  const EncodeFn f = encode_fn();
+  if (f == nullptr || 128 % p.G != 0 || !on(p.q, 16) || p.q_row % 8 != 0 || p.q_head % 8 != 0 || p.q_row <= 0 || p.q_head <= 0) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.R};
+  const cuuint64_t strides[2] = {(cuuint64_t)p.q_head * 2, (cuuint64_t)p.q_row * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(128 / p.G)};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Long chunks: the plan, the widening, the attention, the joining of cut segments.
@@ -339,7 +353,7 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
   AttnParams p = own;
   p.part = reinterpret_cast<float*>(ws + L.c_part);
   p.cut = reinterpret_cast<CutRec*>(ws + L.c_cut);
-  p.seg_cost = kSegCostP;
+  p.seg_cost = kSegCostC;
   WideParams w;
   memset(&w, 0, sizeof(w));
   w.k16 = reinterpret_cast<uint16_t*>(ws + L.c_k16);
@@ -359,6 +373,8 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
   if (!wide_map(&m.k, w.k16, c, rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) ||
       !wide_map(&m.v, w.v16, c, rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
     return cudaErrorInvalidValue;
+  CUtensorMap map_q;
+  w.q_tma = query_map(&map_q, p, D);
   const long long sms = sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
   cudaError_t e = start(chunk_plan_kernel<kRowsP>, dim3(1), kPlanThreads, 0, s, p, w.c);
@@ -370,7 +386,7 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
   static std::atomic<unsigned long long> done{0};
   if ((e = allow_smem(kern, done, PreShape<D>::kSmem)) != cudaSuccess) return e;
   const int n = (int)(L.chunk_grid < sms ? L.chunk_grid : sms);
-  e = start(kern, dim3((unsigned)n), kPreThreads, PreShape<D>::kSmem, s, p, w, m.k, m.v);
+  e = start(kern, dim3((unsigned)n), kPreThreads, PreShape<D>::kSmem, s, p, w, m.k, m.v, map_q);
   return e != cudaSuccess ? e : launch_merge<uint16_t, D, kRowsP>(p, n, s);
 }
 
