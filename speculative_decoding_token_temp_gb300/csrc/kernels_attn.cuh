@@ -39,6 +39,7 @@ struct AttnParams {
   int fixed_len;
   int mask;
   int skip_flat;            // sequences with at least so many rows (times G) are left out; 0: none
+  int block_rows;           // flat rows of a row block where they are fewer than the kernel's; 0: as many
   int late_wait;            // the pass over the sequences' own tokens behind a prefix pass: see attn_tc_kernel
   int seg_cost;             // tiles that a segment's beginning and end count for
   float c;                  // scale * log2(e)
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_merge_kernel(AttnParams p,
   griddep_wait();
   const CutRec r = p.cut[blockIdx.x];
   const int i = blockIdx.x, lane = threadIdx.x & 31, c = blockIdx.y * 8 + (threadIdx.x >> 5), f = r.f0 + c;
-  if (r.parts == 0 || c >= NR || f >= r.rows * p.G) return;
+  if (r.parts == 0 || c >= (p.block_rows > 0 ? p.block_rows : NR) || f >= r.rows * p.G) return;
   // part j: slot 2 i + 1 of the first block, slot 2 (i + j) of the others
   auto part_of = [&](int j) { return slot_of<NR, D>(p, j == 0 ? 2 * i + 1 : 2 * (i + j)); };
   const int some = r.total >= grid ? grid : r.total;  // blocks that have a part of the line

@@ -1,7 +1,7 @@
 // Chunks of new tokens over the cache, on the fifth-generation tensor cores: what
 // attn_prefix_kernel (its CHUNK form) works from.
 //
-// Rows of a sequence that fill 256-row blocks make a dense product, so every sequence's keys
+// Rows of a sequence that fill 256-row blocks (whole tokens: 252 rows with 7 heads a kv head) make a dense product, so every sequence's keys
 // and values are widened once per call into the workspace, as a shared prefix is, and read as
 // 16-bit operands by all its row blocks: the prefix's tiles first, then the sequence's own, up
 // to the last token that the row block sees.
@@ -76,12 +76,11 @@ __device__ __forceinline__ int plan_scan(int x, int* s_warp, int& total) {
   return (warp > 0 ? s_warp[warp - 1] : 0) + incl - x;
 }
 
-template <int NR>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ AttnParams p, ChunkParams c) {
   __shared__ int s_warp[32], s_er[kPlanThreads], s_nrb[kPlanThreads];
   griddep_wait();
   griddep_launch();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NR = p.block_rows;
   // cu first: only of a prefix sum do the sequences' row blocks fit where they are to stand
   bool bad_cu = false;
   if (p.cu != nullptr) {
@@ -302,7 +301,6 @@ __device__ __forceinline__ Part locate_chunk(const ChunkParams& c, Part& shared)
   return shared;
 }
 
-template <int NR>
 __device__ __forceinline__ WideSeg next_chunk(const AttnParams& p, const ChunkParams& c, Place& at, int& left) {
   const ChunkEntry e = c.entry[at.b];
   WideSeg g;
@@ -312,7 +310,7 @@ __device__ __forceinline__ WideSeg next_chunk(const AttnParams& p, const ChunkPa
   g.t0 = max(0, r - p.seg_cost);
   g.n = max(0, r + take - p.seg_cost - g.t0);
   g.h = h;
-  g.f0 = e.rb * NR;
+  g.f0 = e.rb * p.block_rows;
   g.pages = nullptr;
   g.w0 = e.w0;
   at.off += take;

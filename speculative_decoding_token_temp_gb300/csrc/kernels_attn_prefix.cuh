@@ -162,6 +162,21 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// 64 bytes of a row; whole sectors at once where they lie on the 32-byte grid (a warp's rows are far apart).
+__device__ __forceinline__ void store64(void* p, const uint32_t (&y)[16]) {
+  if (((uintptr_t)p & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<char*>(p) + 32 * i), "r"(y[8 * i]),
+                   "r"(y[8 * i + 1]), "r"(y[8 * i + 2]), "r"(y[8 * i + 3]), "r"(y[8 * i + 4]), "r"(y[8 * i + 5]), "r"(y[8 * i + 6]),
+                   "r"(y[8 * i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) static_cast<uint4*>(p)[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+  }
+}
+
 __device__ __forceinline__ void tma_queries(uint32_t dst, const CUtensorMap* map, int x, int head, int row, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
@@ -230,10 +245,11 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   const uint32_t tmem = sh.tmem;
   Place at = line.at;
   int left = line.end - line.begin;
+  const int group = CHUNK ? p.block_rows / 2 : 128;  // rows of a group
   if (CHUNK && !line.ok) fill_nan<uint16_t, D>(p, blockIdx.x, gridDim.x, kPreThreads);
   auto next = [&]() -> WideSeg {
     if constexpr (CHUNK) {
-      return next_chunk<NR>(p, wide.c, at, left);
+      return next_chunk(p, wide.c, at, left);
     } else {
       WideSeg g;
       static_cast<Seg&>(g) = next_seg<NR>(p, at, left);
@@ -252,14 +268,14 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         const WideSeg g = next();
         if (CHUNK && wide.q_tma && g.n > 0) {
           // the stretch's queries, as soon as the last scores of the one before are computed: while its ends are worked on
-          const int groups = g.rows * p.G - g.f0 > 128 ? 2 : 1;
+          const int groups = g.rows * p.G - g.f0 > group ? 2 : 1;
           if (nseg > 0) tc_wait_one(bar(sh.q_free), (nseg - 1) & 1, gave_up, p.status);
           ++nseg;
-          mbar_expect_arrive(bar(sh.q_full), groups * 128 * D * 2);
+          mbar_expect_arrive(bar(sh.q_full), groups * group * D * 2);
           for (int w = 0; w < groups; ++w)
 #pragma unroll
             for (int a = 0; a < T::kAtoms; ++a)
-              tma_queries(base + T::oQ + w * 128 * D * 2 + a * 16384, &map_q, a * 64, g.h * p.G, g.row0 + (g.f0 + w * 128) / p.G, bar(sh.q_full));
+              tma_queries(base + T::oQ + w * 128 * D * 2 + a * 16384, &map_q, a * 64, g.h * p.G, g.row0 + (g.f0 + w * group) / p.G, bar(sh.q_full));
         }
         for (int k = 0; k < g.n; ++k, ++gi) {
           const int st = gi % NST, row = (g.h * wide.tiles + wide_tile(g, g.t0 + k)) * kTile;
@@ -303,7 +319,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     };
     while (left > 0) {
       const WideSeg g = next();
-      const int n = __shfl_sync(kFull, g.n, 0), groups = __shfl_sync(kFull, g.rows * p.G - g.f0 > 128 ? 2 : 1, 0);
+      const int n = __shfl_sync(kFull, g.n, 0), groups = __shfl_sync(kFull, g.rows * p.G - g.f0 > group ? 2 : 1, 0);
       if (n == 0) continue;
       tc_wait(bar(sh.q_full), nseg & 1, gave_up, p.status);
       ++nseg;
@@ -355,7 +371,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     }
   } else {
     // ---- softmax: group w, a row and half of a tile's tokens a thread ----
-    const int w = warp >> 3, half = (warp >> 2) & 1, t = tid & 127, c = w * 128 + t;
+    const int w = warp >> 3, half = (warp >> 2) & 1, t = tid & 127, c = w * group + t;
     const int pair_bar = 1 + w * 4 + (warp & 3);  // the two warps that share 32 rows
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + T::cS + w * 128, tO = tmem + lanes + T::cO + w * 128;
@@ -366,7 +382,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       const WideSeg g = next();
       if (g.n == 0) continue;
       if (left == 0 && tid == 0) p.cut[blockIdx.x] = cut_rec(g, blockIdx.x, gridDim.x, line.end, line.total);
-      const int flat = g.rows * p.G, f = g.f0 + c;
+      const int f = g.f0 + c, flat = CHUNK && t >= group ? 0 : g.rows * p.G;  // (rows past the group's are none)
       // half of this thread's query row into shared memory, swizzled
       bool bad = false;  // a query that is no finite number
       if (!(CHUNK && wide.q_tma)) {
@@ -395,13 +411,13 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         fence_async();
         mbar_arrive(bar(sh.q_full));
       }
-      const bool have = flat - g.f0 > w * 128;  // this group has rows
+      const bool have = g.rows * p.G - g.f0 > w * group;  // this group has rows
       // of the sequence's own tokens this row sees the first `own`
       const int own = CHUNK ? (f < flat ? g.len - g.rows + f / p.G + 1 : 0) : g.len, pre_tiles = CHUNK ? wide.c.pre_tiles : 0;
       float m = 0.f, l = 0.f;
       if (have) {
         for (int k = 0; k < g.n; ++k, ++tiles_done) {
-          const int tile = g.t0 + k, valid = (tile < pre_tiles ? wide.c.pre_len - tile * kTile : own - (tile - pre_tiles) * kTile) - half * 64;
+          const int tile = g.t0 + k, valid = (tile < pre_tiles ? (f < flat ? wide.c.pre_len : 0) - tile * kTile : own - (tile - pre_tiles) * kTile) - half * 64;
           const long long info = (long long)g.h * wide.tiles + wide_tile(g, tile);
           float E;
           bool mixed = false;
@@ -503,7 +519,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         const long long idx = (long long)(g.row0 + f / p.G) * p.Hq + g.h * p.G + f % p.G;
         Coef r{};
         if (!whole) {
-          if (half == 0) {
+          if (half == 0 && (!CHUNK || t < group)) {
             slot[c] = CHUNK && l == 0.f ? ninf : m;  // a row that saw nothing has no reference
             slot[NR + c] = l;
           }
@@ -520,12 +536,13 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           tc_wait_ld();
           if (CHUNK && whole) {
             if (f < flat && in_idx(idx, (long long)p.R * p.Hq, p.status)) {
+              uint32_t y[16];
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                const float x[8] = {o[j] * scale,     o[j + 1] * scale, o[j + 2] * scale, o[j + 3] * scale,
-                                    o[j + 4] * scale, o[j + 5] * scale, o[j + 6] * scale, o[j + 7] * scale};
-                store8(static_cast<uint16_t*>(p.o) + idx * D + i + j, x);
+              for (int j = 0; j < 16; ++j) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * j] * scale, o[2 * j + 1] * scale);
+                y[j] = *reinterpret_cast<const uint32_t*>(&b);
               }
+              store64(static_cast<uint16_t*>(p.o) + idx * D + i, y);
             }
           } else if (f < flat && in_idx(idx, (long long)p.R * p.Hq, p.status)) {
 #pragma unroll

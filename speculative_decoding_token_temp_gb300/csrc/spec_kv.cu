@@ -103,6 +103,9 @@ int tc_rows(long long flat, int head_dim) {
   return per <= 16 ? 16 : (int)(cdiv(per, 8) * 8);
 }
 
+// Rows of a chunk's 128-row tile: whole tokens, so that one load brings them.
+int chunk_group(int G) { return 128 / G * G; }
+
 // The CHUNK pass: what it takes of the workspace from `off` on, and whether the call uses it.
 void chunk_layout(AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& c, size_t& off) {
   const long long G = g.q_heads / c.kv_heads, flat = rows_of(g) * G, pre = cdiv(g.prefix_len, kTile);
@@ -110,7 +113,7 @@ void chunk_layout(AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& 
   L.chunk = false;
   if ((long long)(g.gamma + 1) * G < kChunkFlat) return;
   L.chunk_tiles = pre + g.B * nt;
-  L.chunk_entries = flat / kRowsP + g.B;
+  L.chunk_entries = flat / (2 * chunk_group((int)G)) + g.B;
   const long long line = L.chunk_entries * c.kv_heads * (pre + nt + kSegCostC);
   const size_t wide = (size_t)2 * c.kv_heads * L.chunk_tiles * kTile * c.head_dim;
   if (line > kMaxLine || L.chunk_tiles * c.kv_heads > (1LL << 23) || 2 * wide > kChunkBytes) return;  // (tokens of the widened memory count in ints)
@@ -338,7 +341,7 @@ cudaError_t pass_prefix(const AttnParams& p, const spec_kv_cache& c, const AttnL
 bool query_map(CUtensorMap* m, const AttnParams& p, int D) {
   memset(m, 0, sizeof(*m));
   const EncodeFn f = encode_fn();
-  if (f == nullptr || 128 % p.G != 0 || !on(p.q, 16) || p.q_row % 8 != 0 || p.q_head % 8 != 0 || p.q_row <= 0 || p.q_head <= 0) return false;
+  if (f == nullptr || !on(p.q, 16) || p.q_row % 8 != 0 || p.q_head % 8 != 0 || p.q_row <= 0 || p.q_head <= 0) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.R};
   const cuuint64_t strides[2] = {(cuuint64_t)p.q_head * 2, (cuuint64_t)p.q_row * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(128 / p.G)};
@@ -354,6 +357,7 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
   p.part = reinterpret_cast<float*>(ws + L.c_part);
   p.cut = reinterpret_cast<CutRec*>(ws + L.c_cut);
   p.seg_cost = kSegCostC;
+  p.block_rows = 2 * chunk_group(p.G);
   WideParams w;
   memset(&w, 0, sizeof(w));
   w.k16 = reinterpret_cast<uint16_t*>(ws + L.c_k16);
@@ -377,7 +381,7 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
   w.q_tma = query_map(&map_q, p, D);
   const long long sms = sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
-  cudaError_t e = start(chunk_plan_kernel<kRowsP>, dim3(1), kPlanThreads, 0, s, p, w.c);
+  cudaError_t e = start(chunk_plan_kernel, dim3(1), kPlanThreads, 0, s, p, w.c);
   if (e != cudaSuccess) return e;
   const long long units = L.chunk_tiles * c.kv_heads;
   e = start(chunk_widen_kernel<D>, dim3((unsigned)(units < 8 * sms ? units : 8 * sms)), kWidenThreads, 0, s, p, w);
