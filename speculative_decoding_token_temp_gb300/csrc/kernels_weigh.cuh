@@ -149,32 +149,44 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
       weigh_stage<E, D>(p, g, counted, c0, s_q, s_rq, s_neg, s_lim);
       __syncthreads();
       const int tiles_n = min(kWeighCols, counted * a.G - c0 + 7) / 8;  // of 8 columns
-      for (int tile = g.t0; tile < g.t0 + g.n; ++tile) {
-        const int tb = tile * kTile + warp * 32, own_t = tb + lane;
-        if (tb >= g.len) break;
-        // this lane's token: its place, exponent, weight so far
-        long long vec = -1;
-        if (own_t < g.len) {
-          const int page = __ldg(g.pages + (own_t >> a.page_shift));
+      // a tile's loads go out before the tile in front of it is worked on, its page's number before those
+      auto page_of = [&](int tile) -> int {
+        const int t = tile * kTile + warp * 32 + lane;
+        return tile < g.t0 + g.n && t < g.len ? __ldg(g.pages + (t >> a.page_shift)) : -1;
+      };
+      uint4 ahead[4][CH];
+      long long vec_ahead = -1;  // of this lane's token
+      unsigned exp_ahead = 0;
+      float old_ahead = 0.f;
+      auto fetch = [&](int tile, int page) {
+        const int t = tile * kTile + warp * 32 + lane;
+        vec_ahead = -1;
+        if (tile < g.t0 + g.n && t < g.len) {
           if ((unsigned)page < (unsigned)a.num_pages)
-            vec = (((long long)page * a.Hk + g.h) << a.page_shift) + (own_t & ((1 << a.page_shift) - 1));
+            vec_ahead = (((long long)page * a.Hk + g.h) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
           else
             bits |= SPEC_DEV_PAGE;
-          if (vec >= 0 && !in_idx(vec, ((long long)a.num_pages * a.Hk) << a.page_shift, a.status)) vec = -1;
+          if (vec_ahead >= 0 && !in_idx(vec_ahead, ((long long)a.num_pages * a.Hk) << a.page_shift, a.status)) vec_ahead = -1;
         }
-        uint4 raw[4][CH];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const long long v = __shfl_sync(kFull, vec, g8 + 8 * m);
+          const long long v = __shfl_sync(kFull, vec_ahead, g8 + 8 * m);
 #pragma unroll
           for (int j = 0; j < CH; ++j) {
-            raw[m][j] = make_uint4(0, 0, 0, 0);
-            if (v >= 0) raw[m][j] = __ldg(reinterpret_cast<const uint4*>(a.k + v * D) + 4 * j + t4);
+            ahead[m][j] = make_uint4(0, 0, 0, 0);
+            if (v >= 0) ahead[m][j] = __ldg(reinterpret_cast<const uint4*>(a.k + v * D) + 4 * j + t4);
           }
         }
-        const unsigned kb = vec >= 0 ? __ldg(a.k_exp + vec) : 0u;
-        const float old = vec < 0 || (c0 == 0 && (own_t >= ctx || p.keep == 0.f)) ? 0.f : p.mass[vec];
-        const float own_ks = exp_value(kb);
+        exp_ahead = vec_ahead >= 0 ? __ldg(a.k_exp + vec_ahead) : 0u;
+        old_ahead = vec_ahead < 0 || (c0 == 0 && (t >= ctx || p.keep == 0.f)) ? 0.f : p.mass[vec_ahead];
+      };
+      int page = page_of(g.t0 + 1);
+      fetch(g.t0, page_of(g.t0));
+      for (int tile = g.t0; tile < g.t0 + g.n; ++tile) {
+        const int tb = tile * kTile + warp * 32;
+        if (tb >= g.len) break;
+        const long long vec = vec_ahead;
+        const float old = old_ahead, own_ks = exp_value(exp_ahead);
         float ks[4], sum[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -186,10 +198,12 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
         for (int m = 0; m < 4; ++m)
 #pragma unroll
           for (int j = 0; j < CH; ++j) {
-            const uint32_t w[4] = {raw[m][j].x, raw[m][j].y, raw[m][j].z, raw[m][j].w};
+            const uint32_t w[4] = {ahead[m][j].x, ahead[m][j].y, ahead[m][j].z, ahead[m][j].w};
 #pragma unroll
             for (int s = 0; s < 4; ++s) widen4(w[s], lo[m][j][s], hi[m][j][s]);
           }
+        fetch(tile + 1, page);
+        page = page_of(tile + 2);
 #pragma unroll 1
         for (int nt = 0; nt < tiles_n; ++nt) {
           float acc[2][4];

@@ -38,9 +38,23 @@ void fill_rope(RopeParams& p, const spec_rope& r, const spec_head_norm& n, const
   p.interleaved = r.interleaved != 0;
 }
 
+// Rows of a block: 8 (a warp a row, its sines and weights set up once for all heads) once that
+// gives every SM a block, fewer below, down to all warps on one row. With the cache, 32/8 heads of
+// 128 in bf16, 1 / 2 / 4 / 8 rows: 128 rows 4.2 / 5.2 / 7.2 / 10.0 us, 512 rows 7.3 / 6.7 / 7.3 /
+// 10.1, 1024 rows 11.9 / 10.1 / 9.2 / 10.2, 2304 rows 24.3 / 18.3 / 14.1 / 12.9, 8192 rows 82.6 /
+// 61.4 / 47.2 / 38.3. In fp32 8 are no better than 4 (4096 rows 49.6 / 39.6 / 39.3 / 42.9).
+template <typename E, int D, bool CACHE, bool VEC, int R>
+cudaError_t start_rope(const RopeParams& p, cudaStream_t s) {
+  return start(rope_kernel<E, D, CACHE, VEC, R>, dim3((unsigned)cdiv(p.rows, R)), kRopeThreads, 0, s, p);
+}
 template <typename E, int D, bool CACHE, bool VEC>
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t s) {
-  return start(rope_kernel<E, D, CACHE, VEC, 1>, dim3((unsigned)p.rows), kRopeThreads, 0, s, p);
+  const long long rows = p.rows, sms = sm_count();
+  if constexpr (VEC) {
+    if (sizeof(E) == 2 && rows >= 8 * sms) return start_rope<E, D, CACHE, VEC, sizeof(E) == 2 ? 8 : 4>(p, s);
+    if (2 * rows >= 3 * sms && rows < 3 * sms) return start_rope<E, D, CACHE, VEC, 2>(p, s);
+  }
+  return rows >= 3 * sms ? start_rope<E, D, CACHE, VEC, 4>(p, s) : start_rope<E, D, CACHE, VEC, 1>(p, s);
 }
 template <bool CACHE>
 cudaError_t launch_rope(const RopeParams& p, spec_dtype dtype, int D, bool vec, cudaStream_t s) {
@@ -114,7 +128,6 @@ spec_status spec_qk_rope(int32_t rows, int32_t q_heads, int32_t k_heads, int32_t
   p.k_out = k_out;
   p.rows = rows;
   p.Hq = q_heads;
-  p.heads = q_heads + k_heads;
   fill_rope(p, rope, norm, positions);
   const long long per = 16 / (long long)es;
   const bool vec = on(q, 16) && on(k, 16) && q_row_stride % per == 0 && q_head_stride % per == 0 && k_row_stride % per == 0 &&
@@ -155,7 +168,6 @@ spec_status spec_qk_rope_append(spec_kv_cache c, spec_kv_rows r, int32_t q_heads
   p.q_out = q_out;
   p.rows = r.rows;
   p.Hq = q_heads;
-  p.heads = q_heads + 2 * c.kv_heads;
   fill_rope(p, rope, norm, positions);
   const long long per = 16 / (long long)es;
   const bool vec = on(q, 16) && on(k, 16) && on(v, 16) && q_row_stride % per == 0 && q_head_stride % per == 0 &&

@@ -81,7 +81,7 @@ def plan(dev, dim, rot, axes, interleaved):
     (1, 1, 1, 128, 128, 1, False, True), (5, 32, 8, 128, 128, 1, False, True), (300, 7, 1, 64, 64, 1, True, True),
     (33, 12, 4, 64, 32, 3, False, False), (67, 5, 5, 128, 48, 2, False, True), (9, 3, 1, 128, 96, 4, True, False),
     (17, 8, 2, 64, 16, 1, False, True), (4, 6, 2, 128, 0, 1, False, True), (2, 40, 40, 64, 48, 1, True, True),
-    (5003, 3, 1, 128, 128, 1, False, True), (4099, 5, 2, 64, 64, 2, True, True)])
+    (301, 5, 3, 128, 128, 1, False, True), (700, 2, 3, 128, 64, 1, True, True), (5003, 3, 1, 128, 128, 1, False, True), (4099, 5, 2, 64, 64, 2, True, True)])
 def test_norm_and_rotation(dev, dtype, layout, rows, heads, kv_heads, dim, rot, axes, interleaved, normed):  # noqa: F811
     q, k, _ = inputs(dev, rows, heads, kv_heads, dim, dtype, layout)
     rng = np.random.default_rng(rows)
