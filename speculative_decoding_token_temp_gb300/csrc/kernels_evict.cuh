@@ -22,7 +22,6 @@ constexpr int kSelThreads = 512;
 constexpr int kSelPer = 8;       // tokens of a thread and step
 constexpr int kSelKeys = 16384;  // keys of a sequence's beginning that stay in shared memory
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;
 
 struct EvictParams {
   uint8_t *k, *v, *k_exp, *v_exp;
@@ -32,7 +31,8 @@ struct EvictParams {
   const int32_t *table, *new_table;  // the same in place
   const int32_t* kv_len;
   int budget, sinks, recent;
-  int cached_keys;  // keys in shared memory
+  int cached_keys;  // keys in shared memory (a multiple of 16)
+  int wide;         // mass on the 16-byte grid
   int32_t *kept, *kv_len_out;
   uint32_t* status;
 };
@@ -68,7 +68,7 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long x, u
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t s_key[];  // cached_keys
+  extern __shared__ __align__(16) uint32_t s_key[];  // cached_keys
   __shared__ int s_hist[2048];
   __shared__ unsigned long long s_warp[kSelThreads / 32];
   __shared__ uint32_t s_digit;
@@ -106,9 +106,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
     const long long vec = (((long long)__ldg(pages + (t >> p.page_shift)) * p.Hk + h) << p.page_shift) + (t & mask);
     return mass_key(__ldcg(p.mass + vec));
   };
-  for (int t = lo + tid; t < min(hi, p.cached_keys); t += kSelThreads) {
-    const long long vec = (((long long)__ldg(pages + (t >> p.page_shift)) * p.Hk + h) << p.page_shift) + (t & mask);
-    s_key[t] = in_idx(vec, ((long long)p.num_pages * p.Hk) << p.page_shift, p.status) ? mass_key(__ldcg(p.mass + vec)) : 0u;
+  // the weights of four neighbouring tokens at once (they share a page), all of a thread's on their way together
+  const int upto = min(n, p.cached_keys);
+  if (p.wide) {
+#pragma unroll 4
+    for (int t = tid * 4; t < upto; t += kSelThreads * 4) {
+      const long long vec = (((long long)__ldg(pages + (t >> p.page_shift)) * p.Hk + h) << p.page_shift) + (t & mask);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (in_idx(vec, ((long long)p.num_pages * p.Hk) << p.page_shift, p.status)) x = __ldcg(reinterpret_cast<const float4*>(p.mass + vec));
+      *reinterpret_cast<uint4*>(s_key + t) = make_uint4(mass_key(x.x), mass_key(x.y), mass_key(x.z), mass_key(x.w));
+    }
+  } else {
+    for (int t = tid; t < upto; t += kSelThreads) {
+      const long long vec = (((long long)__ldg(pages + (t >> p.page_shift)) * p.Hk + h) << p.page_shift) + (t & mask);
+      s_key[t] = in_idx(vec, ((long long)p.num_pages * p.Hk) << p.page_shift, p.status) ? mass_key(__ldcg(p.mass + vec)) : 0u;
+    }
   }
   // the key of the last that stays: its digits from the top, among the keys that share the ones before
   uint32_t border = 0;
@@ -187,19 +199,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   }
 }
 
-// blockIdx.x = unit + units * step: units of a head are `slices` pieces of the vectors of the
-// keys, as many of the values, and one for exponents and weights; a unit's blocks walk its
-// tokens in steps, `steps` of them side by side (1 in place).
-struct MoveSplit {
-  int units, slices, steps;
-};
+// A block moves one kv head's tokens in steps of kMoveStep: its threads look the step's places up,
+// a token each, and move the tokens' exponents and weights; then D / 16 lanes a vector move the
+// keys and the values. blockIdx.x = slice + slices * step: to other pages (PLACE false) every step
+// has a block of its own; in place a block walks all of them, and `slices` blocks share a head's
+// vectors, a piece each.
+constexpr int kMoveStep = 256;
 
-template <int D>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p, MoveSplit m) {
+template <int D, bool PLACE>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p, int slices) {
+  constexpr int LANES = D / 16, U = 8;  // vectors of a thread on their way
+  __shared__ long long s_src[kMoveStep], s_dst[kMoveStep];
   griddep_wait();
   griddep_launch();
-  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, unit = blockIdx.x % m.units, mask = (1 << p.page_shift) - 1;
-  const bool moves = p.new_table != p.table;
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, mask = (1 << p.page_shift) - 1;
   const int32_t* pages = p.table + (long long)b * p.pps;
   const int32_t* new_pages = p.new_table + (long long)b * p.new_pps;
   const int32_t* kept = p.kept + ((long long)b * p.Hk + h) * p.budget;
@@ -208,56 +221,66 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     const long long vec = (((long long)__ldg(table + (t >> p.page_shift)) * p.Hk + h) << p.page_shift) + (t & mask);
     return in_idx(vec, places, p.status) ? vec : -1;
   };
-  const bool vectors = unit < 2 * m.slices;
-  const int lanes = vectors ? D / 16 / m.slices : 1, rows = kMoveThreads / lanes, piece = tid % lanes + (vectors ? unit % m.slices : 0) * lanes;
-  uint8_t* const side = unit < m.slices ? p.k : p.v;
-  const long long step = (long long)rows * kMoveUnroll;
-  for (long long j0 = blockIdx.x / m.units * step; j0 < p.budget; j0 += m.steps * step) {
-    int src[kMoveUnroll];
-    bool some = false;
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const long long j = j0 + u * rows + tid / lanes;
-      src[u] = j < p.budget ? __ldcg(kept + j) : -1;
-      some |= src[u] >= 0;
-      if (!moves && src[u] == j) src[u] = -1;  // where it is already
+  const int slice = PLACE ? blockIdx.x % slices : 0, lanes = PLACE ? LANES / slices : LANES;
+  const int rows = kMoveThreads / lanes, row0 = tid / lanes, piece = slice * lanes + tid % lanes;
+  for (int j0 = PLACE ? 0 : blockIdx.x * kMoveStep; j0 < p.budget; j0 += PLACE ? kMoveStep : p.budget) {
+    const int j = j0 + tid, t = j < p.budget ? __ldcg(kept + j) : -1;
+    long long src = -1, dst = -1;
+    if (t >= 0 && !(PLACE && t == j)) {  // (in place: where it is already)
+      src = place(pages, t);
+      dst = place(new_pages, j);
+      if (src < 0 || dst < 0) src = dst = -1;
     }
-    if (__syncthreads_or(some) == 0) return;  // (past the last that stays)
-    if (vectors) {
-      uint4 x[kMoveUnroll];
+    s_src[tid] = src;
+    s_dst[tid] = dst;
+    if (__syncthreads_or(t >= 0) == 0) return;  // (past the last that stays)
+    float w;
+    uint8_t ke, ve;
+    if (src >= 0 && slice == 0) {
+      w = __ldcg(p.mass + src);
+      ke = __ldcg(p.k_exp + src);
+      ve = __ldcg(p.v_exp + src);
+    }
+    if (!PLACE && src >= 0) {
+      p.mass[dst] = w;
+      p.k_exp[dst] = ke;
+      p.v_exp[dst] = ve;
+    }
+    // (with slices a step is fewer than U vectors of a thread)
+    uint4 x[2][U];
+    auto load = [&](int side) {
 #pragma unroll
-      for (int u = 0; u < kMoveUnroll; ++u) {
-        const long long at = src[u] >= 0 ? place(pages, src[u]) : -1;
-        if (at >= 0) x[u] = __ldcg(reinterpret_cast<const uint4*>(side + at * D) + piece);
+      for (int u = 0; u < U; ++u) {
+        const int r = row0 + u * rows;
+        const long long at = r < kMoveStep ? s_src[r] : -1;
+        if (at >= 0) x[side][u] = __ldcg(reinterpret_cast<const uint4*>((side ? p.v : p.k) + at * D) + piece);
       }
-      if (!moves) __syncthreads();
+    };
+    auto store = [&](int side) {
 #pragma unroll
-      for (int u = 0; u < kMoveUnroll; ++u) {
-        const long long at = src[u] >= 0 ? place(new_pages, (int)j0 + u * rows + tid / lanes) : -1;
-        if (at >= 0) *(reinterpret_cast<uint4*>(side + at * D) + piece) = x[u];
+      for (int u = 0; u < U; ++u) {
+        const int r = row0 + u * rows;
+        const long long at = r < kMoveStep ? s_dst[r] : -1;
+        if (at >= 0) *(reinterpret_cast<uint4*>((side ? p.v : p.k) + at * D) + piece) = x[side][u];
       }
+    };
+    if (PLACE) {
+      load(0);
+      load(1);
+      __syncthreads();  // every load of the step before its stores
+      store(0);
+      store(1);
+      if (src >= 0 && slice == 0) {
+        p.mass[dst] = w;
+        p.k_exp[dst] = ke;
+        p.v_exp[dst] = ve;
+      }
+      __syncthreads();  // (the places are read)
     } else {
-      float w[kMoveUnroll];
-      uint8_t ke[kMoveUnroll], ve[kMoveUnroll];
-#pragma unroll
-      for (int u = 0; u < kMoveUnroll; ++u) {
-        const long long at = src[u] >= 0 ? place(pages, src[u]) : -1;
-        if (at >= 0) {
-          w[u] = __ldcg(p.mass + at);
-          ke[u] = __ldcg(p.k_exp + at);
-          ve[u] = __ldcg(p.v_exp + at);
-        }
-      }
-      if (!moves) __syncthreads();
-#pragma unroll
-      for (int u = 0; u < kMoveUnroll; ++u) {
-        const long long at = src[u] >= 0 ? place(new_pages, (int)j0 + u * rows + tid / lanes) : -1;
-        if (at >= 0) {
-          p.mass[at] = w[u];
-          p.k_exp[at] = ke[u];
-          p.v_exp[at] = ve[u];
-        }
-      }
+      load(0);
+      load(1);
+      store(0);
+      store(1);
     }
   }
 }

@@ -5,8 +5,7 @@
 // Only the keys are read. A warp takes 32 tokens and keeps their codes, widened to f16 (exact),
 // in registers as the first operand of m16n8k16 MMAs; the queries, f16 in shared memory, are
 // the second, 8 rows at a time. Which elements share a step of an MMA does not matter as long
-// as both operands agree, so a lane takes 16 neighbouring codes of a token by one load and no
-// data passes through shared memory on its way. The sum over rows ends in the lanes that hold
+// as both operands agree, so a lane takes 16 neighbouring codes of a token by one load. The sum over rows ends in the lanes that hold
 // the token: no maxima, no second product, and the sum does not depend on what runs when.
 //
 // A bf16 query is, scaled by its row's power of two to below 2^15, exactly an f16 number down
@@ -22,6 +21,7 @@ namespace sv {
 
 constexpr int kWeighThreads = 128;
 constexpr int kWeighCols = 64;          // rows (query rows times heads of a kv head) at a time
+constexpr int kWeighStages = 2;         // tiles of a warp on their way or worked on
 constexpr int kWeighAllRows = 1 << 14;  // a sequence's rows are one row block on the line of tiles
 
 struct WeighParams {
@@ -48,8 +48,14 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
+}
+
 template <typename E, int D>
 struct WeighShape {
+  static constexpr int kRing = kWeighThreads * kWeighStages * D;  // bytes
   static constexpr int kParts = sizeof(E) == 2 ? 1 : 2;
   static constexpr int kStride = D + 8;  // halves of a row: neighbouring rows' 16-byte loads fall into different banks
 };
@@ -120,8 +126,11 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
   __shared__ __align__(16) __half s_q[T::kParts * kWeighCols * T::kStride];
   __shared__ __align__(16) float s_rq[kWeighCols], s_neg[kWeighCols];
   __shared__ __align__(16) int s_lim[kWeighCols];
+  __shared__ long long s_vec[kWeighThreads / 32][kWeighStages][32];
+  extern __shared__ __align__(128) uint8_t s_ring[];  // [warp][stage][32 tokens][D]
   const AttnParams& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t4 = lane & 3, g8 = lane >> 2;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_ring) + warp * kWeighStages * (32 * D);
   griddep_wait();
   griddep_launch();
   const Part line = locate_block<kWeighAllRows>(a, s_part);
@@ -149,61 +158,76 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
       weigh_stage<E, D>(p, g, counted, c0, s_q, s_rq, s_neg, s_lim);
       __syncthreads();
       const int tiles_n = min(kWeighCols, counted * a.G - c0 + 7) / 8;  // of 8 columns
-      // a tile's loads go out before the tile in front of it is worked on, its page's number before those
+      // A warp's tiles pass through a ring of its own: the codes of tiles ahead are on their way to shared memory, and of the
+      // next tile the exponents and the weights so far to registers.
+      const int end = min(g.t0 + g.n, (g.len - warp * 32 + kTile - 1) / kTile);  // tiles that hold tokens of this warp's
       auto page_of = [&](int tile) -> int {
         const int t = tile * kTile + warp * 32 + lane;
-        return tile < g.t0 + g.n && t < g.len ? __ldg(g.pages + (t >> a.page_shift)) : -1;
+        return tile < end && t < g.len ? __ldg(g.pages + (t >> a.page_shift)) : -1;
       };
-      uint4 ahead[4][CH];
-      long long vec_ahead = -1;  // of this lane's token
-      unsigned exp_ahead = 0;
-      float old_ahead = 0.f;
       auto fetch = [&](int tile, int page) {
-        const int t = tile * kTile + warp * 32 + lane;
-        vec_ahead = -1;
-        if (tile < g.t0 + g.n && t < g.len) {
-          if ((unsigned)page < (unsigned)a.num_pages)
-            vec_ahead = (((long long)page * a.Hk + g.h) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-          else
-            bits |= SPEC_DEV_PAGE;
-          if (vec_ahead >= 0 && !in_idx(vec_ahead, ((long long)a.num_pages * a.Hk) << a.page_shift, a.status)) vec_ahead = -1;
-        }
+        const int t = tile * kTile + warp * 32 + lane, st = tile % kWeighStages;
+        long long vec = -1;
+        if (tile < end) {
+          if (t < g.len) {
+            if ((unsigned)page < (unsigned)a.num_pages)
+              vec = (((long long)page * a.Hk + g.h) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+            else
+              bits |= SPEC_DEV_PAGE;
+            if (vec >= 0 && !in_idx(vec, ((long long)a.num_pages * a.Hk) << a.page_shift, a.status)) vec = -1;
+          }
+          s_vec[warp][st][lane] = vec;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const long long v = __shfl_sync(kFull, vec_ahead, g8 + 8 * m);
-#pragma unroll
-          for (int j = 0; j < CH; ++j) {
-            ahead[m][j] = make_uint4(0, 0, 0, 0);
-            if (v >= 0) ahead[m][j] = __ldg(reinterpret_cast<const uint4*>(a.k + v * D) + 4 * j + t4);
+          for (int i = 0; i < D / 16; ++i) {
+            const int row = i * (512 / D) + lane / (D / 16), c = lane % (D / 16);
+            const long long v = __shfl_sync(kFull, vec, row);
+            const uint32_t dst = ring + st * (32 * D) + row * D + (D == 128 ? c ^ (row & 1) * 4 : c) * 16;
+            copy16(dst, a.k + (v >= 0 ? v * D + c * 16 : 0), v >= 0);
           }
         }
-        exp_ahead = vec_ahead >= 0 ? __ldg(a.k_exp + vec_ahead) : 0u;
-        old_ahead = vec_ahead < 0 || (c0 == 0 && (t >= ctx || p.keep == 0.f)) ? 0.f : p.mass[vec_ahead];
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      int page = page_of(g.t0 + 1);
-      fetch(g.t0, page_of(g.t0));
-      for (int tile = g.t0; tile < g.t0 + g.n; ++tile) {
+      long long vec_next;
+      unsigned exp_next = 0;
+      float old_next = 0.f;
+      auto peek = [&](int tile) {
+        vec_next = tile < end ? s_vec[warp][tile % kWeighStages][lane] : -1;
+        exp_next = vec_next >= 0 ? __ldg(a.k_exp + vec_next) : 0u;
+        old_next = vec_next < 0 || (c0 == 0 && (tile * kTile + warp * 32 + lane >= ctx || p.keep == 0.f)) ? 0.f : p.mass[vec_next];
+      };
+      __syncwarp();  // (the stretch before is read)
+#pragma unroll
+      for (int i = 0; i < kWeighStages - 1; ++i) fetch(g.t0 + i, page_of(g.t0 + i));
+      int page = page_of(g.t0 + kWeighStages - 1);
+      peek(g.t0);  // (a lane reads the places that it wrote itself)
+      for (int tile = g.t0; tile < end; ++tile) {
         const int tb = tile * kTile + warp * 32;
-        if (tb >= g.len) break;
-        const long long vec = vec_ahead;
-        const float old = old_ahead, own_ks = exp_value(exp_ahead);
+        const long long vec = vec_next;
+        const float old = old_next, own_ks = exp_value(exp_next);
+        fetch(tile + kWeighStages - 1, page);
+        page = page_of(tile + kWeighStages);
+        peek(tile + 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kWeighStages - 1) : "memory");
+        __syncwarp();
         float ks[4], sum[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           ks[m] = __shfl_sync(kFull, own_ks, g8 + 8 * m);
           sum[m] = 0.f;
         }
+        const uint8_t* const codes = s_ring + (warp * kWeighStages + tile % kWeighStages) * (32 * D);
         uint32_t lo[4][CH][4], hi[4][CH][4];
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
           for (int j = 0; j < CH; ++j) {
-            const uint32_t w[4] = {ahead[m][j].x, ahead[m][j].y, ahead[m][j].z, ahead[m][j].w};
+            const int row = g8 + 8 * m, c = 4 * j + t4;
+            const uint4 raw = *reinterpret_cast<const uint4*>(codes + row * D + (D == 128 ? c ^ (row & 1) * 4 : c) * 16);
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
             for (int s = 0; s < 4; ++s) widen4(w[s], lo[m][j][s], hi[m][j][s]);
           }
-        fetch(tile + 1, page);
-        page = page_of(tile + 2);
+        __syncwarp();  // (the stage may be written again)
 #pragma unroll 1
         for (int nt = 0; nt < tiles_n; ++nt) {
           float acc[2][4];

@@ -68,29 +68,31 @@ cudaError_t launch_rope(const RopeParams& p, spec_dtype dtype, int D, bool vec, 
 
 template <typename E, int D>
 cudaError_t launch_weigh(const WeighParams& p, long long line, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
   static std::atomic<int> per_sm{0};
+  constexpr int ring = WeighShape<E, D>::kRing;
+  cudaError_t e = allow_smem(weigh_kernel<E, D>, done, ring);
+  if (e != cudaSuccess) return e;
   int n = per_sm.load(std::memory_order_relaxed);
   if (n == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, weigh_kernel<E, D>, kWeighThreads, 0);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, weigh_kernel<E, D>, kWeighThreads, ring);
     if (e != cudaSuccess || n < 1) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
     per_sm.store(n, std::memory_order_relaxed);
   }
   const long long wave = (long long)n * sm_count();
   if (wave < 1) return cudaErrorInvalidConfiguration;
-  return start(weigh_kernel<E, D>, dim3((unsigned)(line < wave ? line : wave)), kWeighThreads, 0, s, p);
+  return start(weigh_kernel<E, D>, dim3((unsigned)(line < wave ? line : wave)), kWeighThreads, ring, s, p);
 }
 
 template <int D>
 cudaError_t launch_move(const EvictParams& p, cudaStream_t s) {
-  const bool in_place = p.new_table == p.table;
-  MoveSplit m;
-  m.slices = 1;
-  if (in_place)  // a block walks all tokens of its piece: narrower pieces where there are few heads
-    while (m.slices < D / 32 && 2LL * m.slices * p.B * p.Hk < 2LL * sm_count()) m.slices *= 2;
-  m.units = 2 * m.slices + 1;
-  const int rows = kMoveThreads / (D / 16 / m.slices) * kMoveUnroll;
-  m.steps = in_place ? 1 : (int)cdiv(p.budget, rows);
-  return start(evict_move_kernel<D>, dim3((unsigned)(m.units * m.steps), (unsigned)p.Hk, (unsigned)p.B), kMoveThreads, 0, s, p, m);
+  const long long most = (long long)p.pps << p.page_shift, stay = most < p.budget ? most : p.budget;
+  if (stay == 0) return cudaSuccess;
+  if (p.new_table != p.table)
+    return start(evict_move_kernel<D, false>, dim3((unsigned)cdiv(stay, kMoveStep), (unsigned)p.Hk, (unsigned)p.B), kMoveThreads, 0, s, p, 1);
+  int slices = 1;  // a block walks all tokens of its piece: narrower pieces, down to a sector, where there are few heads
+  while (slices < D / 32 && (long long)slices * p.B * p.Hk < 2LL * sm_count()) slices *= 2;
+  return start(evict_move_kernel<D, true>, dim3((unsigned)slices, (unsigned)p.Hk, (unsigned)p.B), kMoveThreads, 0, s, p, slices);
 }
 
 }  // namespace
@@ -249,6 +251,7 @@ spec_status spec_kv_evict(spec_evict_batch g, spec_kv_cache c, float* mass, int3
   p.sinks = g.sinks;
   p.recent = g.recent;
   p.cached_keys = (int)(most < kSelKeys ? most : kSelKeys);
+  p.wide = on(mass, 16);
   p.kept = kept;
   p.kv_len_out = kv_len_out;
   p.status = device_status;
