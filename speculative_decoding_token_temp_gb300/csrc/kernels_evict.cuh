@@ -21,7 +21,6 @@ namespace sv {
 constexpr int kSelThreads = 512;
 constexpr int kSelPer = 8;       // tokens of a thread and step
 constexpr int kSelKeys = 16384;  // keys of a sequence's beginning that stay in shared memory
-constexpr int kMoveThreads = 256;
 
 struct EvictParams {
   uint8_t *k, *v, *k_exp, *v_exp;
@@ -139,10 +138,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       }
       __syncthreads();
       // from the largest digit down: the one that the count of `need` falls into
-      const int per = bins / kSelThreads;  // 4, 4, 2
-      int c[4], sum = 0;
+      constexpr int kMost = 2048 / kSelThreads;
+      const int per = bins / kSelThreads;
+      int c[kMost], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kMost; ++i) {
         c[i] = i < per ? s_hist[bins - 1 - (tid * per + i)] : 0;
         sum += c[i];
       }
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       int before = (int)block_scan((unsigned long long)sum, s_warp, all);
       if (before < need && need <= before + sum) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kMost; ++i) {
           if (before < need && need <= before + c[i]) {
             s_digit = (uint32_t)(bins - 1 - (tid * per + i));
             s_need = need - before;
@@ -199,17 +199,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   }
 }
 
-// A block moves one kv head's tokens in steps of kMoveStep: its threads look the step's places up,
+// A block moves one kv head's tokens in steps of as many as it has threads (128 to other pages, 256 in place; 64 sequences
+// to 8192 tokens, half kept, to other pages: 128 163 us, 256 175, 512 186): its threads look the step's places up,
 // a token each, and move the tokens' exponents and weights; then D / 16 lanes a vector move the
 // keys and the values. blockIdx.x = slice + slices * step: to other pages (PLACE false) every step
 // has a block of its own; in place a block walks all of them, and `slices` blocks share a head's
 // vectors, a piece each.
-constexpr int kMoveStep = 256;
+template <bool PLACE>
+constexpr int kMoveStep = PLACE ? 256 : 128;
 
 template <int D, bool PLACE>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p, int slices) {
-  constexpr int LANES = D / 16, U = 8;  // vectors of a thread on their way
-  __shared__ long long s_src[kMoveStep], s_dst[kMoveStep];
+__global__ void __launch_bounds__(kMoveStep<PLACE>) evict_move_kernel(const __grid_constant__ EvictParams p, int slices) {
+  constexpr int LANES = D / 16, STEP = kMoveStep<PLACE>, U = LANES;  // U: vectors of a thread on their way
+  __shared__ long long s_src[STEP], s_dst[STEP];
   griddep_wait();
   griddep_launch();
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, mask = (1 << p.page_shift) - 1;
@@ -222,8 +224,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     return in_idx(vec, places, p.status) ? vec : -1;
   };
   const int slice = PLACE ? blockIdx.x % slices : 0, lanes = PLACE ? LANES / slices : LANES;
-  const int rows = kMoveThreads / lanes, row0 = tid / lanes, piece = slice * lanes + tid % lanes;
-  for (int j0 = PLACE ? 0 : blockIdx.x * kMoveStep; j0 < p.budget; j0 += PLACE ? kMoveStep : p.budget) {
+  const int rows = STEP / lanes, row0 = tid / lanes, piece = slice * lanes + tid % lanes;
+  for (int j0 = PLACE ? 0 : blockIdx.x * STEP; j0 < p.budget; j0 += PLACE ? STEP : p.budget) {
     const int j = j0 + tid, t = j < p.budget ? __ldcg(kept + j) : -1;
     long long src = -1, dst = -1;
     if (t >= 0 && !(PLACE && t == j)) {  // (in place: where it is already)
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = row0 + u * rows;
-        const long long at = r < kMoveStep ? s_src[r] : -1;
+        const long long at = r < STEP ? s_src[r] : -1;
         if (at >= 0) x[side][u] = __ldcg(reinterpret_cast<const uint4*>((side ? p.v : p.k) + at * D) + piece);
       }
     };
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = row0 + u * rows;
-        const long long at = r < kMoveStep ? s_dst[r] : -1;
+        const long long at = r < STEP ? s_dst[r] : -1;
         if (at >= 0) *(reinterpret_cast<uint4*>((side ? p.v : p.k) + at * D) + piece) = x[side][u];
       }
     };

@@ -89,10 +89,11 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t s) {
   const long long most = (long long)p.pps << p.page_shift, stay = most < p.budget ? most : p.budget;
   if (stay == 0) return cudaSuccess;
   if (p.new_table != p.table)
-    return start(evict_move_kernel<D, false>, dim3((unsigned)cdiv(stay, kMoveStep), (unsigned)p.Hk, (unsigned)p.B), kMoveThreads, 0, s, p, 1);
+    return start(evict_move_kernel<D, false>, dim3((unsigned)cdiv(stay, kMoveStep<false>), (unsigned)p.Hk, (unsigned)p.B), kMoveStep<false>, 0, s, p,
+                 1);
   int slices = 1;  // a block walks all tokens of its piece: narrower pieces, down to a sector, where there are few heads
   while (slices < D / 32 && (long long)slices * p.B * p.Hk < 2LL * sm_count()) slices *= 2;
-  return start(evict_move_kernel<D, true>, dim3((unsigned)slices, (unsigned)p.Hk, (unsigned)p.B), kMoveThreads, 0, s, p, slices);
+  return start(evict_move_kernel<D, true>, dim3((unsigned)slices, (unsigned)p.Hk, (unsigned)p.B), kMoveStep<true>, 0, s, p, slices);
 }
 
 }  // namespace
