@@ -34,16 +34,25 @@ struct ChunkEntry {
   int w0, row0, rows, len;  // len -1: a bad kv_len
 };
 
+constexpr int kPlanBuckets = 1024;  // of lengths, one a thread of the plan
+constexpr int kJoinCost = 9;        // the joining of cut segments (15 us), in tiles
+
+// The segment that block b of n takes in round r: to and fro, so that who got the longest of a round gets the shortest of the next.
+__device__ __forceinline__ long long chunk_item(int r, int b, int n) { return (long long)r * n + (r & 1 ? n - 1 - b : b); }
+
 struct ChunkHead {
   int entries;  // -1: cu is no prefix sum of the batch
   int line;     // the line's length
   int tiles;    // widened tiles, the prefix's among them
+  int whole;    // blocks take whole segments (entry, head) instead of equal parts of the line
 };
 
 struct ChunkParams {
   ChunkHead* head;
   ChunkEntry* entry;
+  int* order;          // [entries] the longest first
   int* first;          // [B] a sequence's first widened tile
+  int blocks;          // of the attention
   const int32_t* pre_table;
   int pre_len, pre_tiles;
   int min_flat;        // sequences with fewer rows (times heads of a kv head) are left to attn_tc_kernel
@@ -90,7 +99,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     }
   }
   if (__syncthreads_or(bad_cu)) {
-    if (tid == 0) *c.head = ChunkHead{-1, 0, 0};
+    if (tid == 0) *c.head = ChunkHead{-1, 0, 0, 0};
     return;
   }
   uint32_t bits = 0;
@@ -146,7 +155,45 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     if (e < entries) c.entry[e].start = at;
     line += all;
   }
-  if (tid == 0) *c.head = ChunkHead{entries, line, tiles};
+  // Whole segments, or equal parts of the line? Cut segments cost their beginning and end twice and the joining; whole ones
+  // leave blocks with more and with less. Sorted by length and dealt out to and fro they are often even enough: what the
+  // busiest block then gets is added up here.
+  __shared__ int s_hist[kPlanBuckets], s_most, s_long;
+  if (tid == 0) s_most = 0, s_long = 1;
+  for (int i = tid; i < kPlanBuckets; i += kPlanThreads) s_hist[i] = 0;
+  __syncthreads();
+  int longest = 1;
+  for (int e = tid; e < entries; e += kPlanThreads) longest = max(longest, c.entry[e].nt);
+  atomicMax(&s_long, longest);
+  __syncthreads();
+  const int unit = (s_long + kPlanBuckets - 1) / kPlanBuckets;  // tiles of a bucket
+  for (int e = tid; e < entries; e += kPlanThreads) atomicAdd(&s_hist[kPlanBuckets - 1 - (c.entry[e].nt - 1) / unit], 1);
+  __syncthreads();
+  int all;
+  const int count = s_hist[tid], at = plan_scan(count, s_warp, all);
+  __syncthreads();
+  s_hist[tid] = at;
+  __syncthreads();
+  for (int e = tid; e < entries; e += kPlanThreads) c.order[atomicAdd(&s_hist[kPlanBuckets - 1 - (c.entry[e].nt - 1) / unit], 1)] = e;
+  __syncthreads();
+  const long long items = (long long)entries * p.Hk;
+  if (items <= 64LL * c.blocks) {
+    for (int b = tid; b < c.blocks; b += kPlanThreads) {
+      int sum = 0;
+      for (int r = 0; r < 64; ++r) {
+        const long long i = chunk_item(r, b, c.blocks);
+        if (i >= items) break;
+        sum += ((c.entry[c.order[i / p.Hk]].nt - 1) / unit + 1) * unit + p.seg_cost;  // (by its bucket: the same whatever the order within)
+      }
+      atomicMax(&s_most, sum);
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    // past 64 segments a block the line's cuts count for little, and so does the unevenness: whole ones then
+    const bool even = items > 64LL * c.blocks || (s_most > 0 && s_most <= line / c.blocks + p.seg_cost + kJoinCost);
+    *c.head = ChunkHead{entries, line, tiles, even ? 1 : 0};
+  }
   if (bits) atomicOr(p.status, bits);
 }
 
@@ -278,41 +325,61 @@ struct WideSeg : Seg {
 };
 
 // Block i's part of the line, its place: (entry, offset). By the first warp for the block.
-__device__ __forceinline__ Part locate_chunk(const ChunkParams& c, Part& shared) {
+__device__ __forceinline__ Part locate_chunk(const ChunkParams& c, int heads, Part& shared) {
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x, total = c.head->line, n = c.head->entries;
     Part r;
-    r.total = total;
-    r.ok = n >= 0;
-    r.begin = line_at(total, blockIdx.x, gridDim.x);
-    r.end = line_at(total, blockIdx.x + 1, gridDim.x);
-    int lo = 0, hi = max(n, 1);
-    while (hi - lo > 1 && r.begin < total) {
-      const int step = (hi - lo + 31) / 32, e = lo + lane * step;
-      const unsigned in = __ballot_sync(kFull, e < hi && c.entry[e < hi ? e : lo].start <= r.begin);
-      lo += (__popc(in) - 1) * step;  // (the first is among them)
-      hi = min(hi, lo + step);
+    if (c.head->whole) {  // the part: rounds
+      const long long items = (long long)n * heads;
+      const int full = (int)(items / gridDim.x);
+      r.begin = 0;
+      r.end = full + (chunk_item(full, blockIdx.x, gridDim.x) < items ? 1 : 0);
+      r.total = total;
+      r.ok = true;
+      r.at = Place{0, 0};
+      if (lane == 0) shared = r;
+    } else {
+      r.total = total;
+      r.ok = n >= 0;
+      r.begin = line_at(total, blockIdx.x, gridDim.x);
+      r.end = line_at(total, blockIdx.x + 1, gridDim.x);
+      int lo = 0, hi = max(n, 1);
+      while (hi - lo > 1 && r.begin < total) {
+        const int step = (hi - lo + 31) / 32, e = lo + lane * step;
+        const unsigned in = __ballot_sync(kFull, e < hi && c.entry[e < hi ? e : lo].start <= r.begin);
+        lo += (__popc(in) - 1) * step;  // (the first is among them)
+        hi = min(hi, lo + step);
+      }
+      r.at.b = lo;
+      r.at.off = r.begin < total ? r.begin - c.entry[lo].start : 0;
+      if (lane == 0) shared = r;
     }
-    r.at.b = lo;
-    r.at.off = r.begin < total ? r.begin - c.entry[lo].start : 0;
-    if (lane == 0) shared = r;
   }
   __syncthreads();
   return shared;
 }
 
 __device__ __forceinline__ WideSeg next_chunk(const AttnParams& p, const ChunkParams& c, Place& at, int& left) {
-  const ChunkEntry e = c.entry[at.b];
+  const bool whole = c.head->whole;
+  const long long item = whole ? chunk_item(at.b, blockIdx.x, gridDim.x) : 0;
+  const int head = whole ? (int)(item % p.Hk) : 0;
+  const ChunkEntry e = c.entry[whole ? c.order[item / p.Hk] : at.b];
   WideSeg g;
   g.row0 = e.row0, g.rows = e.rows, g.bad = e.len < 0, g.len = max(e.len, 0);
   g.nt = e.nt;
+  g.f0 = e.rb * p.block_rows;
+  g.pages = nullptr;
+  g.w0 = e.w0;
+  if (whole) {
+    g.t0 = 0, g.n = e.nt, g.h = head;
+    at.b += 1;
+    left -= 1;
+    return g;
+  }
   const int line = e.nt + p.seg_cost, h = at.off / line, r = at.off - h * line, take = min(line - r, left);
   g.t0 = max(0, r - p.seg_cost);
   g.n = max(0, r + take - p.seg_cost - g.t0);
   g.h = h;
-  g.f0 = e.rb * p.block_rows;
-  g.pages = nullptr;
-  g.w0 = e.w0;
   at.off += take;
   left -= take;
   if (at.off >= p.Hk * line) {

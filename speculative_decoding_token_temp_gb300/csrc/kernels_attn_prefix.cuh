@@ -240,7 +240,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   }
   griddep_wait();
   griddep_launch();
-  const Part line = CHUNK ? locate_chunk(wide.c, sh.line) : locate_block<NR>(p, sh.line);  // (the prefix: one dense sequence, no cu)
+  const Part line = CHUNK ? locate_chunk(wide.c, p.Hk, sh.line) : locate_block<NR>(p, sh.line);  // (the prefix: one dense sequence, no cu)
   tc_after();
   const uint32_t tmem = sh.tmem;
   Place at = line.at;

@@ -90,7 +90,7 @@ struct AttnLayout {
   bool chunk_only;     // ... and so all sequences
   long long chunk_grid, chunk_tiles, chunk_entries;  // at most
   size_t part, cut, pre_part, pre_cut, pre_o, pre_lse, k16, v16, exp, total;
-  size_t c_part, c_cut, c_k16, c_v16, c_info, c_ev, c_entry, c_first, c_head;
+  size_t c_part, c_cut, c_k16, c_v16, c_info, c_ev, c_entry, c_order, c_first, c_head;
 };
 
 // Rows of a row block of the tensor-core kernel, for `flat` rows that share keys: as few
@@ -133,6 +133,7 @@ void chunk_layout(AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& 
   L.c_info = take(sizeof(float2) * (size_t)(c.kv_heads * L.chunk_tiles));
   L.c_ev = take(sizeof(float) * (size_t)(c.kv_heads * L.chunk_tiles) * kTile);
   L.c_entry = take(sizeof(ChunkEntry) * (size_t)L.chunk_entries);
+  L.c_order = take(sizeof(int) * (size_t)L.chunk_entries);
   L.c_first = take(sizeof(int) * (size_t)g.B);
   L.c_head = take(sizeof(ChunkHead));
 }
@@ -367,6 +368,7 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
   w.ev = reinterpret_cast<float*>(ws + L.c_ev);
   w.c.head = reinterpret_cast<ChunkHead*>(ws + L.c_head);
   w.c.entry = reinterpret_cast<ChunkEntry*>(ws + L.c_entry);
+  w.c.order = reinterpret_cast<int*>(ws + L.c_order);
   w.c.first = reinterpret_cast<int*>(ws + L.c_first);
   w.c.pre_table = g.prefix_table;
   w.c.pre_len = g.prefix_len;
@@ -381,6 +383,8 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
   w.q_tma = query_map(&map_q, p, D);
   const long long sms = sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
+  const int n = (int)(L.chunk_grid < sms ? L.chunk_grid : sms);
+  w.c.blocks = n;
   cudaError_t e = start(chunk_plan_kernel, dim3(1), kPlanThreads, 0, s, p, w.c);
   if (e != cudaSuccess) return e;
   const long long units = L.chunk_tiles * c.kv_heads;
@@ -389,7 +393,6 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
   auto kern = attn_prefix_kernel<D, true>;
   static std::atomic<unsigned long long> done{0};
   if ((e = allow_smem(kern, done, PreShape<D>::kSmem)) != cudaSuccess) return e;
-  const int n = (int)(L.chunk_grid < sms ? L.chunk_grid : sms);
   e = start(kern, dim3((unsigned)n), kPreThreads, PreShape<D>::kSmem, s, p, w, m.k, m.v, map_q);
   return e != cudaSuccess ? e : launch_merge<uint16_t, D, kRowsP>(p, n, s);
 }
