@@ -118,6 +118,54 @@ __device__ __forceinline__ void weigh_stage(const WeighParams& p, const Seg& g, 
   }
 }
 
+// The weights of 8 NB columns from column 8 nt on, added to the sums of this lane's tokens tok, tok + 8, ...
+template <typename E, int D, int NB>
+__device__ __forceinline__ void weigh_columns(const __half* s_q, const float* s_rq, const float* s_neg, const int* s_lim, int nt,
+                                              const uint32_t (&lo)[4][D / 64][4], const uint32_t (&hi)[4][D / 64][4], const float (&ks)[4],
+                                              int tok, float (&sum)[4]) {
+  using T = WeighShape<E, D>;
+  const int t4 = threadIdx.x & 3, g8 = (threadIdx.x & 31) >> 2;
+  float acc[NB][2][4];
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int m = 0; m < 2; ++m) acc[n][m][0] = acc[n][m][1] = acc[n][m][2] = acc[n][m][3] = 0.f;
+#pragma unroll
+  for (int part = T::kParts - 1; part >= 0; --part) {  // (the small parts first)
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      uint32_t w[NB][8];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const uint4* q = reinterpret_cast<const uint4*>(s_q + (part * kWeighCols + (nt + n) * 8 + g8) * T::kStride + t4 * 16) + j * 8;
+        const uint4 q0 = q[0], q1 = q[1];
+        w[n][0] = q0.x, w[n][1] = q0.y, w[n][2] = q0.z, w[n][3] = q0.w, w[n][4] = q1.x, w[n][5] = q1.y, w[n][6] = q1.z, w[n][7] = q1.w;
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            mma_16816(acc[n][m], lo[2 * m][j][s], lo[2 * m + 1][j][s], hi[2 * m][j][s], hi[2 * m + 1][j][s], w[n][2 * s], w[n][2 * s + 1]);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int col = (nt + n) * 8 + t4 * 2;
+    const float2 rq = *reinterpret_cast<const float2*>(s_rq + col), neg = *reinterpret_cast<const float2*>(s_neg + col);
+    const int2 lim = *reinterpret_cast<const int2*>(s_lim + col);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const float* c = &acc[n][m >> 1][(m & 1) * 2];
+      // the difference in natural units, where it is small, then in binary ones
+      const float e0 = ex2(fmaf(c[0] * ks[m], rq.x, neg.x) * 1.4426950408889634f);
+      const float e1 = ex2(fmaf(c[1] * ks[m], rq.y, neg.y) * 1.4426950408889634f);
+      sum[m] += (tok + 8 * m < lim.x ? e0 : 0.f) + (tok + 8 * m < lim.y ? e1 : 0.f);
+    }
+  }
+}
+
 template <typename E, int D>
 __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ WeighParams p) {
   using T = WeighShape<E, D>;
@@ -228,37 +276,12 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
             for (int s = 0; s < 4; ++s) widen4(w[s], lo[m][j][s], hi[m][j][s]);
           }
         __syncwarp();  // (the stage may be written again)
+        // two groups of 8 columns at once where there are more (the MMAs of one wait for one another; columns past the last are zeros)
+        if (tiles_n == 1) {
+          weigh_columns<E, D, 1>(s_q, s_rq, s_neg, s_lim, 0, lo, hi, ks, tb + g8, sum);
+        } else {
 #pragma unroll 1
-        for (int nt = 0; nt < tiles_n; ++nt) {
-          float acc[2][4];
-#pragma unroll
-          for (int m = 0; m < 2; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
-#pragma unroll
-          for (int part = T::kParts - 1; part >= 0; --part) {  // (the small parts first)
-            const uint4* q = reinterpret_cast<const uint4*>(s_q + (part * kWeighCols + nt * 8 + g8) * T::kStride + t4 * 16);
-#pragma unroll
-            for (int j = 0; j < CH; ++j) {
-              const uint4 q0 = q[j * 8], q1 = q[j * 8 + 1];
-              const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-                  mma_16816(acc[m], lo[2 * m][j][s], lo[2 * m + 1][j][s], hi[2 * m][j][s], hi[2 * m + 1][j][s], w[2 * s], w[2 * s + 1]);
-            }
-          }
-          const int col = nt * 8 + t4 * 2;
-          const float2 rq = *reinterpret_cast<const float2*>(s_rq + col), neg = *reinterpret_cast<const float2*>(s_neg + col);
-          const int2 lim = *reinterpret_cast<const int2*>(s_lim + col);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const float* c = &acc[m >> 1][(m & 1) * 2];
-            const int tok = tb + g8 + 8 * m;
-            // the difference in natural units, where it is small, then in binary ones
-            const float e0 = ex2(fmaf(c[0] * ks[m], rq.x, neg.x) * 1.4426950408889634f);
-            const float e1 = ex2(fmaf(c[1] * ks[m], rq.y, neg.y) * 1.4426950408889634f);
-            sum[m] += (tok < lim.x ? e0 : 0.f) + (tok < lim.y ? e1 : 0.f);
-          }
+          for (int nt = 0; nt < tiles_n; nt += 2) weigh_columns<E, D, 2>(s_q, s_rq, s_neg, s_lim, nt, lo, hi, ks, tb + g8, sum);
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {

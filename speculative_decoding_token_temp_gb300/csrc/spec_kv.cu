@@ -76,7 +76,7 @@ constexpr long long kWideWork128 = 300000, kWideWork64 = 75000;
 // A chunk's sequences with at least so many rows (times heads of a kv head) are widened and
 // computed in 256-row blocks, the others in the 48- or 32-row blocks of attn_tc_kernel.
 constexpr int kChunkFlat = 256;
-constexpr size_t kChunkBytes = (size_t)48 << 30;  // most that a chunk's widened keys and values may take; past it, narrow blocks
+constexpr size_t kChunkBytes = (size_t)32 << 30;  // most that a chunk's widened keys and values may take; past it, narrow blocks
 constexpr int kMaxGridT = 512;   // of the tensor-core kernel (two blocks an SM)
 
 struct AttnLayout {
