@@ -693,9 +693,9 @@ def spec_attention_workspace_bytes(q, cache: KVCache, page_table, kv_len, *, gam
     return int(_lib.lib().spec_attention_workspace_bytes(g, cache.desc, _dtype_code(q)))
 
 
-def _attend(name, q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, prefix_table, prefix_len, want_lse, out,
+def _attend(name, entry, workspace_bytes, q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, prefix_table, prefix_len, want_lse, out,
             workspace, device_status) -> dict:
-    """The call of spec_attention or spec_attention_chunk (`name`)."""
+    """The call of spec_attention or spec_attention_chunk: its name, entry point and workspace's size."""
     dt = _KV_DTYPES.get(q.dtype)
     if dt is None:
         raise TypeError(f"q must be bfloat16 or float32, got {q.dtype}")
@@ -712,8 +712,7 @@ def _attend(name, q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, 
         t = _out(o, "lse", lambda: torch.empty(rows, H, dtype=torch.float32, device=cache.k.device))
         _need(t, "lse", torch.float32, rows * H, cache.k.device)
         lse = t.data_ptr()
-    lib = _lib.lib()
-    nbytes = getattr(lib, name + "_workspace_bytes")(g, cache.desc, dt)
+    nbytes = workspace_bytes(g, cache.desc, dt)
     with _on(cache.index):
         stream = _stream_handle(cache.index)
         if workspace is None:
@@ -728,8 +727,8 @@ def _attend(name, q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, 
                     workspace = keep.get(nbytes, cache.k.device)
         else:
             workspace = _workspace(workspace, nbytes, cache.k.device)
-        code = getattr(lib, name)(g, cache.desc, dt, *view, y.data_ptr(), lse, _status_word(o, device_status, cache),
-                                  workspace.data_ptr(), workspace.numel(), stream)
+        code = entry(g, cache.desc, dt, *view, y.data_ptr(), lse, _status_word(o, device_status, cache),
+                     workspace.data_ptr(), workspace.numel(), stream)
     if code:
         check(name, code)
     return o
@@ -751,8 +750,9 @@ def spec_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv
     Returns o [rows, q_heads, head_dim], lse [rows, q_heads] (fp32, with want_lse) and
     device_status. The default workspace is kept for each stream; a call that is captured
     into a graph takes one of the graph's own memory."""
-    return _attend("spec_attention", q, cache, page_table, kv_len, gamma, cu_draft, parent, scale, prefix_table, prefix_len, want_lse,
-                   out, workspace, device_status)
+    lib = _lib.lib()
+    return _attend("spec_attention", lib.spec_attention, lib.spec_attention_workspace_bytes, q, cache, page_table, kv_len, gamma, cu_draft,
+                   parent, scale, prefix_table, prefix_len, want_lse, out, workspace, device_status)
 
 
 def spec_attention_chunk_workspace_bytes(q, cache: KVCache, page_table, kv_len, *, gamma=None, cu_draft=None, scale=None,
@@ -769,8 +769,9 @@ def spec_attention_chunk(q: torch.Tensor, cache: KVCache, page_table: torch.Tens
     """Attention of chunks of new tokens over the cache: spec_attention (without trees) for up to
     2^20 rows a sequence, whose arguments, layouts and results it shares. A chunk of n tokens
     has gamma = n - 1; packed batches (cu_draft) may mix prompts with single tokens."""
-    return _attend("spec_attention_chunk", q, cache, page_table, kv_len, gamma, cu_draft, None, scale, prefix_table, prefix_len,
-                   want_lse, out, workspace, device_status)
+    lib = _lib.lib()
+    return _attend("spec_attention_chunk", lib.spec_attention_chunk, lib.spec_attention_chunk_workspace_bytes, q, cache, page_table, kv_len,
+                   gamma, cu_draft, None, scale, prefix_table, prefix_len, want_lse, out, workspace, device_status)
 
 
 class Rope:

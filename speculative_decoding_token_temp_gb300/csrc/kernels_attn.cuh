@@ -86,9 +86,9 @@ __device__ __forceinline__ int seq_ntiles(const SeqInfo& s) { return s.len > 0 ?
 __device__ __forceinline__ bool skipped(const AttnParams& p, const SeqInfo& s) { return p.skip_flat > 0 && s.rows * p.G >= p.skip_flat; }
 
 // Tiles on the line of a sequence, over all its row blocks and kv heads.
-template <int NR>
+template <int NR, bool SKIP = false>
 __device__ __forceinline__ int seq_tiles(const AttnParams& p, const SeqInfo& s) {
-  return skipped(p, s) ? 0 : (s.rows * p.G + NR - 1) / NR * p.Hk * (seq_ntiles(s) + p.seg_cost);
+  return SKIP && skipped(p, s) ? 0 : (s.rows * p.G + NR - 1) / NR * p.Hk * (seq_ntiles(s) + p.seg_cost);
 }
 
 // A place on the line of tiles: sequence b, tile `off` of it.
@@ -110,7 +110,7 @@ __device__ __forceinline__ int line_at(int total, int i, int n) { return total /
 // Warp-wide: the line's length, block i's part of it (of n), and the place where that
 // begins. Each lane sums a stretch of sequences, the warp scans the sums, and the lane whose
 // stretch holds the place walks to it.
-template <int NR>
+template <int NR, bool SKIP = false>
 __device__ __noinline__ Part locate(const AttnParams& p, int i, int n) {
   const int lane = threadIdx.x & 31, per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
   int sum = 0;
@@ -125,7 +125,7 @@ __device__ __noinline__ Part locate(const AttnParams& p, int i, int n) {
         continue;
       }
     }
-    sum += seq_tiles<NR>(p, seq_info(p, b));
+    sum += seq_tiles<NR, SKIP>(p, seq_info(p, b));
   }
   int incl = sum;
 #pragma unroll
@@ -144,7 +144,7 @@ __device__ __noinline__ Part locate(const AttnParams& p, int i, int n) {
   if (here) {
 #pragma unroll 1
     for (; b < b1 - 1; ++b) {
-      const int t = seq_tiles<NR>(p, seq_info(p, b));
+      const int t = seq_tiles<NR, SKIP>(p, seq_info(p, b));
       if (off < t) break;
       off -= t;
     }
@@ -177,11 +177,13 @@ struct Seg {
 
 // The next stretch at `at` (advanced), at most `left` tiles of the line (reduced). It may
 // be empty (n = 0): the block's part of the line ends among the tiles that only count.
-template <int NR>
+template <int NR, bool SKIP = false>
 __device__ __forceinline__ Seg next_seg(const AttnParams& p, Place& at, int& left) {
   Seg g;
   SeqInfo s = seq_info(p, at.b);
-  while (skipped(p, s)) s = seq_info(p, ++at.b);  // (there is one that is not: its tiles are `left`)
+  if constexpr (SKIP) {
+    while (skipped(p, s)) s = seq_info(p, ++at.b);  // (there is one that is not: its tiles are `left`)
+  }
   g.row0 = s.row0, g.rows = s.rows, g.len = s.len, g.bad = s.bad;
   g.nt = seq_ntiles(s);
   const int nrb = (s.rows * p.G + NR - 1) / NR, line = g.nt + p.seg_cost;

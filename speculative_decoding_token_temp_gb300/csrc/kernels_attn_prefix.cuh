@@ -417,7 +417,9 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       float m = 0.f, l = 0.f;
       if (have) {
         for (int k = 0; k < g.n; ++k, ++tiles_done) {
-          const int tile = g.t0 + k, valid = (tile < pre_tiles ? (f < flat ? wide.c.pre_len : 0) - tile * kTile : own - (tile - pre_tiles) * kTile) - half * 64;
+          const int tile = g.t0 + k;
+          int valid = own - tile * kTile - half * 64;
+          if constexpr (CHUNK) valid = (tile < pre_tiles ? (f < flat ? wide.c.pre_len : 0) - tile * kTile : own - (tile - pre_tiles) * kTile) - half * 64;
           const long long info = (long long)g.h * wide.tiles + wide_tile(g, tile);
           float E;
           bool mixed = false;

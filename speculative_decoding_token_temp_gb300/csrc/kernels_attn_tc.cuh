@@ -357,7 +357,8 @@ __device__ __forceinline__ void stage_queries(const AttnParams& p, const Seg& g,
   }
 }
 
-template <int D, int NR>
+// SKIP: the sequences with p.skip_flat rows and more are another pass's.
+template <int D, int NR, bool SKIP>
 __global__ void __launch_bounds__(kTcThreads, 2)
 attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v) {
@@ -412,14 +413,14 @@ attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUt
     // ---- the rings of tiles ----
     int gi = 0, ns = 0;
     uint32_t bits = 0;
-    const Part line = locate<NR>(p, blockIdx.x, gridDim.x);
+    const Part line = locate<NR, SKIP>(p, blockIdx.x, gridDim.x);
     Place at = line.at;
     int left = line.ok ? line.end - line.begin : 0;
     const int psz = 1 << p.page_shift, box = min(psz, kTile), np = kTile / box;
     const bool bulk = psz >= 64;
     if (lane == 0) p.cut[blockIdx.x].parts = 0;
     while (left > 0) {
-      const Seg g = next_seg<NR>(p, at, left);
+      const Seg g = next_seg<NR, SKIP>(p, at, left);
       if (g.n == 0) continue;
       if (g.bad) bits |= SPEC_DEV_OFFSETS;
       if (lane == 0) {

@@ -76,6 +76,8 @@ constexpr long long kWideWork128 = 300000, kWideWork64 = 75000;
 // A chunk's sequences with at least so many rows (times heads of a kv head) are widened and
 // computed in 256-row blocks, the others in the 48- or 32-row blocks of attn_tc_kernel.
 constexpr int kChunkFlat = 256;
+template <int D>
+constexpr int kSkipRows = D == 64 ? 32 : 48;  // rows of a row block of those
 constexpr size_t kChunkBytes = (size_t)32 << 30;  // most that a chunk's widened keys and values may take; past it, narrow blocks
 constexpr int kMaxGridT = 512;   // of the tensor-core kernel (two blocks an SM)
 
@@ -153,7 +155,7 @@ AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dt
   const bool tc = dtype == SPEC_BF16;
   const long long cap = tc ? kMaxGridT : kMaxGridS;
   const long long most_flat = L.chunk ? kChunkFlat - 1 : (long long)(g.gamma + 1) * G;  // rows that share keys in the narrow pass
-  L.nr = tc ? tc_rows(most_flat, c.head_dim) : kRowsS;
+  L.nr = L.chunk ? (c.head_dim == 64 ? kSkipRows<64> : kSkipRows<128>) : tc ? tc_rows(most_flat, c.head_dim) : kRowsS;
   const long long flat = rows_of(g) * G;
   L.tiles = cdiv(g.prefix_len, kTile);
   L.wide = tc && flat >= 128 && flat * L.tiles * c.kv_heads >= (c.head_dim == 64 ? kWideWork64 : kWideWork128);
@@ -276,9 +278,9 @@ struct Maps {
   CUtensorMap k, v;
 };
 
-template <int D, int NR>
+template <int D, int NR, bool SKIP = false>
 cudaError_t pass_tc(const AttnParams& p, long long grid, const Maps& m, cudaStream_t s) {
-  auto kern = attn_tc_kernel<D, NR>;
+  auto kern = attn_tc_kernel<D, NR, SKIP>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(kern, done, TcShape<D, NR>::kSmem);
   if (e != cudaSuccess) return e;
@@ -291,6 +293,7 @@ cudaError_t pass_tc(const AttnParams& p, long long grid, const Maps& m, cudaStre
 
 template <int D>
 cudaError_t pass_tc_nr(int nr, const AttnParams& p, long long grid, const Maps& m, cudaStream_t s) {
+  if (p.skip_flat > 0) return pass_tc<D, kSkipRows<D>, true>(p, grid, m, s);
   if (nr == 16) return pass_tc<D, 16>(p, grid, m, s);
   if (nr == 24) return pass_tc<D, 24>(p, grid, m, s);
   if constexpr (D == 128) {
