@@ -2,17 +2,22 @@
 // rows and the head's query heads of the softmax weights exp(scale * q . k - lse), from the
 // log-sums that the attention has left.
 //
-// Only the keys are read. A warp takes 32 tokens and keeps their codes, widened to f16 (exact),
-// in registers as the first operand of m16n8k16 MMAs; the queries, f16 in shared memory, are
-// the second, 8 rows at a time. Which elements share a step of an MMA does not matter as long
-// as both operands agree, so a lane takes 16 neighbouring codes of a token by one load. The sum over rows ends in the lanes that hold
-// the token: no maxima, no second product, and the sum does not depend on what runs when.
+// Only the keys are read. A warp takes 32 tokens, whose codes pass through a ring of its own in
+// shared memory (nothing of it is shared between warps, so none waits for another), and are, widened
+// to f16 (exact), the first operand of m16n8k16 MMAs; the queries, f16 in shared memory, are the
+// second, 8 rows at a time. Which elements share a step of an MMA does not matter as long as both
+// operands agree, so a lane takes 16 neighbouring codes of a token by one load. The sum over rows
+// ends in the lanes that hold the token: no maxima, no second product, and the sum does not depend
+// on what runs when.
 //
 // A bf16 query is, scaled by its row's power of two to below 2^15, exactly an f16 number down
 // to 2^-39 of the row's largest element; an fp32 query is two of them (22 bits).
 //
-// Few rows leave it bound by the keys' bytes, so the legacy MMA's rate is enough there. Many
-// rows (a window of 32 rows and 4 heads: 128 columns) are bound by it and by the exponentials.
+// Few rows leave it bound by the keys' bytes: 256 sequences x 1 row x 4 heads to 1-8192 tokens 186
+// us, 6.2 TB/s. More rows are bound by the latency of the MMAs' chains and the instructions around
+// them (12 warps an SM hold the widened codes): 8 windows of 32 rows x 4 heads behind 2000-16384
+// tokens 73 us, 280 TFLOP/s. Those would need the fifth-generation MMAs, whose scores come with
+// tokens on the lanes as well; not built.
 #pragma once
 
 #include "kernels_attn.cuh"
@@ -20,7 +25,6 @@
 namespace sv {
 
 constexpr int kWeighThreads = 128;
-constexpr int kWeighCols = 64;          // rows (query rows times heads of a kv head) at a time
 constexpr int kWeighStages = 2;         // tiles of a warp on their way or worked on
 constexpr int kWeighAllRows = 1 << 14;  // a sequence's rows are one row block on the line of tiles
 
@@ -53,19 +57,23 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
 }
 
-template <typename E, int D>
+// FEW: no sequence has more than 8 rows (times heads of a kv head). Codes are then widened where an MMA takes them, and with
+// half of the registers twice the warps fit an SM.
+template <typename E, int D, bool FEW>
 struct WeighShape {
+  static constexpr int kCols = FEW ? 8 : 64;  // rows (query rows times heads of a kv head) at a time
   static constexpr int kRing = kWeighThreads * kWeighStages * D;  // bytes
   static constexpr int kParts = sizeof(E) == 2 ? 1 : 2;
   static constexpr int kStride = D + 8;  // halves of a row: neighbouring rows' 16-byte loads fall into different banks
 };
 
-// Columns c0 .. c0 + 63 of a segment's rows into shared memory, two threads a column.
-template <typename E, int D>
+// Columns c0 on of a segment's rows into shared memory, two threads a column.
+template <typename E, int D, bool FEW>
 __device__ __forceinline__ void weigh_stage(const WeighParams& p, const Seg& g, int counted, int c0, __half* q, float* rq, float* neg, int* lim) {
-  using T = WeighShape<E, D>;
+  using T = WeighShape<E, D, FEW>;
   const AttnParams& a = p.a;
   const int col = threadIdx.x >> 1, part = threadIdx.x & 1, f = c0 + col, i = f / a.G;
+  if (FEW && threadIdx.x >= 32) return;  // (whole warps)
   bool here = f < g.rows * a.G && i < counted;
   float x[D / 2];
 #pragma unroll
@@ -98,6 +106,7 @@ __device__ __forceinline__ void weigh_stage(const WeighParams& p, const Seg& g, 
 #pragma unroll
   for (int k = 0; k < D / 2; ++k) top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
   top = max(top, __shfl_xor_sync(kFull, top, 1));
+  if (FEW && col >= T::kCols) return;
   const int e = max((int)(top >> 23) - 127, -100) - 14;  // the largest element comes to [2^14, 2^15)
   const float inv = __int_as_float((127 - e) << 23);
   uint32_t* dst = reinterpret_cast<uint32_t*>(q + col * T::kStride + part * (D / 2));
@@ -108,7 +117,7 @@ __device__ __forceinline__ void weigh_stage(const WeighParams& p, const Seg& g, 
     dst[k / 2] = hi;
     if constexpr (T::kParts == 2) {
       const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-      dst[kWeighCols * T::kStride / 2 + k / 2] = pack_f16(y0 - h.x, y1 - h.y);
+      dst[T::kCols * T::kStride / 2 + k / 2] = pack_f16(y0 - h.x, y1 - h.y);
     }
   }
   if (part == 0) {
@@ -119,11 +128,13 @@ __device__ __forceinline__ void weigh_stage(const WeighParams& p, const Seg& g, 
 }
 
 // The weights of 8 NB columns from column 8 nt on, added to the sums of this lane's tokens tok, tok + 8, ...
-template <typename E, int D, int NB>
-__device__ __forceinline__ void weigh_columns(const __half* s_q, const float* s_rq, const float* s_neg, const int* s_lim, int nt,
+// `codes(m, j)`: this lane's 16 codes of piece j of token tok + 8 m, as 4 words; `lo`, `hi`: the same widened, where they are
+// kept (not FEW).
+template <typename E, int D, bool FEW, int NB, typename F>
+__device__ __forceinline__ void weigh_columns(const __half* s_q, const float* s_rq, const float* s_neg, const int* s_lim, int nt, F codes,
                                               const uint32_t (&lo)[4][D / 64][4], const uint32_t (&hi)[4][D / 64][4], const float (&ks)[4],
                                               int tok, float (&sum)[4]) {
-  using T = WeighShape<E, D>;
+  using T = WeighShape<E, D, FEW>;
   const int t4 = threadIdx.x & 3, g8 = (threadIdx.x & 31) >> 2;
   float acc[NB][2][4];
 #pragma unroll
@@ -137,17 +148,32 @@ __device__ __forceinline__ void weigh_columns(const __half* s_q, const float* s_
       uint32_t w[NB][8];
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        const uint4* q = reinterpret_cast<const uint4*>(s_q + (part * kWeighCols + (nt + n) * 8 + g8) * T::kStride + t4 * 16) + j * 8;
+        const uint4* q = reinterpret_cast<const uint4*>(s_q + (part * T::kCols + (nt + n) * 8 + g8) * T::kStride + t4 * 16) + j * 8;
         const uint4 q0 = q[0], q1 = q[1];
         w[n][0] = q0.x, w[n][1] = q0.y, w[n][2] = q0.z, w[n][3] = q0.w, w[n][4] = q1.x, w[n][5] = q1.y, w[n][6] = q1.z, w[n][7] = q1.w;
       }
+      if constexpr (FEW) {
+        const uint4 c[4] = {codes(0, j), codes(1, j), codes(2, j), codes(3, j)};
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 4; ++s) {
+          uint32_t l[4], h[4];
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t x[4] = {c[m].x, c[m].y, c[m].z, c[m].w};
+            widen4(x[s], l[m], h[m]);
+          }
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-            mma_16816(acc[n][m], lo[2 * m][j][s], lo[2 * m + 1][j][s], hi[2 * m][j][s], hi[2 * m + 1][j][s], w[n][2 * s], w[n][2 * s + 1]);
+          for (int m = 0; m < 2; ++m) mma_16816(acc[0][m], l[2 * m], l[2 * m + 1], h[2 * m], h[2 * m + 1], w[0][2 * s], w[0][2 * s + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+              mma_16816(acc[n][m], lo[2 * m][j][s], lo[2 * m + 1][j][s], hi[2 * m][j][s], hi[2 * m + 1][j][s], w[n][2 * s], w[n][2 * s + 1]);
+      }
     }
   }
 #pragma unroll
@@ -166,14 +192,15 @@ __device__ __forceinline__ void weigh_columns(const __half* s_q, const float* s_
   }
 }
 
-template <typename E, int D>
-__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ WeighParams p) {
-  using T = WeighShape<E, D>;
+template <typename E, int D, bool FEW>
+__global__ void __launch_bounds__(kWeighThreads, FEW ? (sizeof(E) == 2 ? 5 : 4) : 3) weigh_kernel(const __grid_constant__ WeighParams p) {
+  using T = WeighShape<E, D, FEW>;
+  constexpr int kCols = T::kCols;
   constexpr int CH = D / 64;  // 16-byte pieces of a token in a lane
   __shared__ Part s_part;
-  __shared__ __align__(16) __half s_q[T::kParts * kWeighCols * T::kStride];
-  __shared__ __align__(16) float s_rq[kWeighCols], s_neg[kWeighCols];
-  __shared__ __align__(16) int s_lim[kWeighCols];
+  __shared__ __align__(16) __half s_q[T::kParts * kCols * T::kStride];
+  __shared__ __align__(16) float s_rq[kCols], s_neg[kCols];
+  __shared__ __align__(16) int s_lim[kCols];
   __shared__ long long s_vec[kWeighThreads / 32][kWeighStages][32];
   extern __shared__ __align__(128) uint8_t s_ring[];  // [warp][stage][32 tokens][D]
   const AttnParams& a = p.a;
@@ -201,11 +228,11 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
       continue;
     }
     const int ctx = g.len - g.rows;
-    for (int c0 = 0; c0 == 0 || c0 < counted * a.G; c0 += kWeighCols) {
+    for (int c0 = 0; c0 == 0 || c0 < counted * a.G; c0 += kCols) {
       __syncthreads();
-      weigh_stage<E, D>(p, g, counted, c0, s_q, s_rq, s_neg, s_lim);
+      weigh_stage<E, D, FEW>(p, g, counted, c0, s_q, s_rq, s_neg, s_lim);
       __syncthreads();
-      const int tiles_n = min(kWeighCols, counted * a.G - c0 + 7) / 8;  // of 8 columns
+      const int tiles_n = min(kCols, counted * a.G - c0 + 7) / 8;  // of 8 columns
       // A warp's tiles pass through a ring of its own: the codes of tiles ahead are on their way to shared memory, and of the
       // next tile the exponents and the weights so far to registers.
       const int end = min(g.t0 + g.n, (g.len - warp * 32 + kTile - 1) / kTile);  // tiles that hold tokens of this warp's
@@ -264,24 +291,32 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
           sum[m] = 0.f;
         }
         const uint8_t* const codes = s_ring + (warp * kWeighStages + tile % kWeighStages) * (32 * D);
+        auto raw = [&](int m, int j) {
+          const int row = g8 + 8 * m, c = 4 * j + t4;
+          return *reinterpret_cast<const uint4*>(codes + row * D + (D == 128 ? c ^ (row & 1) * 4 : c) * 16);
+        };
         uint32_t lo[4][CH][4], hi[4][CH][4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int j = 0; j < CH; ++j) {
-            const int row = g8 + 8 * m, c = 4 * j + t4;
-            const uint4 raw = *reinterpret_cast<const uint4*>(codes + row * D + (D == 128 ? c ^ (row & 1) * 4 : c) * 16);
-            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-            for (int s = 0; s < 4; ++s) widen4(w[s], lo[m][j][s], hi[m][j][s]);
-          }
-        __syncwarp();  // (the stage may be written again)
-        // two groups of 8 columns at once where there are more (the MMAs of one wait for one another; columns past the last are zeros)
-        if (tiles_n == 1) {
-          weigh_columns<E, D, 1>(s_q, s_rq, s_neg, s_lim, 0, lo, hi, ks, tb + g8, sum);
+        if constexpr (FEW) {
+          weigh_columns<E, D, FEW, 1>(s_q, s_rq, s_neg, s_lim, 0, raw, lo, hi, ks, tb + g8, sum);
+          __syncwarp();  // (the stage may be written again)
         } else {
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+              const uint4 x = raw(m, j);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int s = 0; s < 4; ++s) widen4(w[s], lo[m][j][s], hi[m][j][s]);
+            }
+          __syncwarp();  // (the stage may be written again)
+          // two groups of 8 columns at once where there are more (the MMAs of one wait for one another; columns past the last are zeros)
+          if (tiles_n == 1) {
+            weigh_columns<E, D, FEW, 1>(s_q, s_rq, s_neg, s_lim, 0, raw, lo, hi, ks, tb + g8, sum);
+          } else {
 #pragma unroll 1
-          for (int nt = 0; nt < tiles_n; nt += 2) weigh_columns<E, D, 2>(s_q, s_rq, s_neg, s_lim, nt, lo, hi, ks, tb + g8, sum);
+            for (int nt = 0; nt < tiles_n; nt += 2) weigh_columns<E, D, FEW, 2>(s_q, s_rq, s_neg, s_lim, nt, raw, lo, hi, ks, tb + g8, sum);
+          }
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {

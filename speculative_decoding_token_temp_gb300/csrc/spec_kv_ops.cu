@@ -66,22 +66,28 @@ cudaError_t launch_rope(const RopeParams& p, spec_dtype dtype, int D, bool vec, 
   return vec ? launch_rope<float, 128, CACHE, true>(p, s) : launch_rope<float, 128, CACHE, false>(p, s);
 }
 
-template <typename E, int D>
+template <typename E, int D, bool FEW>
 cudaError_t launch_weigh(const WeighParams& p, long long line, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   static std::atomic<int> per_sm{0};
-  constexpr int ring = WeighShape<E, D>::kRing;
-  cudaError_t e = allow_smem(weigh_kernel<E, D>, done, ring);
+  constexpr int ring = WeighShape<E, D, FEW>::kRing;
+  cudaError_t e = allow_smem(weigh_kernel<E, D, FEW>, done, ring);
   if (e != cudaSuccess) return e;
   int n = per_sm.load(std::memory_order_relaxed);
   if (n == 0) {
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, weigh_kernel<E, D>, kWeighThreads, ring);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, weigh_kernel<E, D, FEW>, kWeighThreads, ring);
     if (e != cudaSuccess || n < 1) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
     per_sm.store(n, std::memory_order_relaxed);
   }
   const long long wave = (long long)n * sm_count();
   if (wave < 1) return cudaErrorInvalidConfiguration;
-  return start(weigh_kernel<E, D>, dim3((unsigned)(line < wave ? line : wave)), kWeighThreads, ring, s, p);
+  return start(weigh_kernel<E, D, FEW>, dim3((unsigned)(line < wave ? line : wave)), kWeighThreads, ring, s, p);
+}
+
+template <typename E>
+cudaError_t launch_weigh(const WeighParams& p, int D, long long line, cudaStream_t s) {
+  if ((p.a.gamma + 1) * p.a.G <= 8) return D == 64 ? launch_weigh<E, 64, true>(p, line, s) : launch_weigh<E, 128, true>(p, line, s);
+  return D == 64 ? launch_weigh<E, 64, false>(p, line, s) : launch_weigh<E, 128, false>(p, line, s);
 }
 
 template <int D>
@@ -205,11 +211,7 @@ spec_status spec_kv_weigh(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, 
   p.keep = keep;
   p.scale = g.scale;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
-  cudaError_t err;
-  if (dtype == SPEC_BF16)
-    err = c.head_dim == 64 ? launch_weigh<uint16_t, 64>(p, line, s) : launch_weigh<uint16_t, 128>(p, line, s);
-  else
-    err = c.head_dim == 64 ? launch_weigh<float, 64>(p, line, s) : launch_weigh<float, 128>(p, line, s);
+  const cudaError_t err = dtype == SPEC_BF16 ? launch_weigh<uint16_t>(p, c.head_dim, line, s) : launch_weigh<float>(p, c.head_dim, line, s);
   return err == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
