@@ -15,6 +15,10 @@
 //
 // All arithmetic is fp32 from the source's elements to the one rounding at the end: bf16 or
 // fp32 out, or the cache's codes (of the fp32 key, which is not rounded to bf16 on the way).
+//
+// What bounds it: HBM where rows are many: 32768 rows of 32 + 8 heads of 128 in bf16, 108 us, 6.2 TB/s
+// of the measured 6.8 (instructions issued in 70 % of cycles). 2304 rows into the cache, whose data
+// is in L2: 13 us. A few rows: 4 us, the chain of loads, sines, barrier, exchange.
 #pragma once
 
 #include "kernels_kv.cuh"
