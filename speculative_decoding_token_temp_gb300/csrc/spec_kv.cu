@@ -142,7 +142,7 @@ void chunk_layout(AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& 
 
 // `chunk`: a call of spec_attention_chunk.
 AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype, bool chunk) {
-  AttnLayout L;
+  AttnLayout L{};
   const int G = g.q_heads / c.kv_heads;
   size_t off = 0;
   L.chunk = L.chunk_only = false;
