@@ -158,7 +158,9 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
  * spec_attention for chunks: the same rows, masks (chains only: parent NULL), prefix,
  * outputs, accuracy and data errors, with gamma up to SPEC_MAX_CHUNK_GAMMA. Row i of a
  * sequence of n_b = gamma_b + 1 rows sees the prefix, the first kv_len[b] - n_b tokens and
- * the chunk's own up to i; a packed batch may mix prompts with single tokens.
+ * the chunk's own up to i; a packed batch may mix prompts with single tokens. Where fp32
+ * queries' rows are many, their 24 bits enter the scores and a weight enters the values' sum
+ * with 22 bits down to 2^-32 of the row's largest weight.
  */
 size_t spec_attention_chunk_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype);
 spec_status spec_attention_chunk(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,

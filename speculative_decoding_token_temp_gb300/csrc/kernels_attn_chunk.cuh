@@ -21,6 +21,9 @@
 // dealt out to and fro, where the plan finds that even enough, and equal parts of the line
 // otherwise. Queries come by TMA while the ends of the stretch before are worked on.
 //
+// fp32 queries are cut into three bf16 parts, exactly, and their weights into two f16 parts: five products where bf16 queries
+// take two, one row tile of 128 a block (2 x 400 rows behind 1000 tokens, 32/8 heads of 128: 75 us, 1002 on the fp32 pipe).
+//
 // What bounds it: a tile of 256 rows x 128 tokens takes about 3000 clocks with either head_dim,
 // and its MMAs 2048 at head_dim 128 and half of that at 64: the softmax warps' instructions (about
 // 400 a warp and tile) and the chain scores, weights, values' sum. A segment's beginning and end

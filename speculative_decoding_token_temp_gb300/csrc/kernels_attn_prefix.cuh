@@ -28,21 +28,28 @@
 
 #include "kernels_attn_chunk.cuh"
 
+#include <type_traits>
+
 namespace sv {
 
 constexpr int kRowsP = 256;         // rows of a block
+constexpr float kFarP = 262144.f;   // scores further than this from a row's reference are counted from a score of its own (`far`)
 constexpr int kPreThreads = 576;    // two softmax groups of eight warps, one warp for copies, one for MMAs
-constexpr int kPreSoft = 512;
 constexpr float kTopP = 8.f;        // a fresh reference puts a row's largest weight at 2^8 ...
 constexpr float kOverP = 15.f;      // ... and is renewed when one would pass 2^15
 
-template <int D>
+// fp32 queries are three bf16 parts (24 bits), their weights two f16 parts (22 bits) side by side where the scores were; one
+// row tile a block then.
+template <int D, bool F32 = false>
 struct PreShape {
+  static constexpr int kGroups = F32 ? 1 : 2;            // row tiles
+  static constexpr int kRows = kGroups * 128, kSoft = kGroups * 256, kThreads = kSoft + 64;
+  static constexpr int kParts = F32 ? 3 : 1;             // of a query
   static constexpr int kAtoms = D / 64;                  // 64 16-bit elements: 128 bytes
   static constexpr int kTileBytes = kTile * D * 2;       // of 16-bit keys or values
   static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int oQ = 0;                           // two row tiles
-  static constexpr int oK = oQ + 2 * 128 * D * 2;
+  static constexpr int oQ = 0;                           // [row tile][part]
+  static constexpr int oK = oQ + kGroups * kParts * 128 * D * 2;
   static constexpr int oV = oK + kStages * kTileBytes;
   static constexpr int kSmem = oV + kStages * kTileBytes + 1024;
   static constexpr int cS = 0, cO = 256;                 // columns of tensor memory: scores (and weights), values' sums
@@ -184,28 +191,30 @@ __device__ __forceinline__ void tma_queries(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-template <int D>
+template <int D, bool F32>
 struct PreShared {
-  using T = PreShape<D>;
+  using T = PreShape<D, F32>;
   Part line;
   uint64_t k_full[T::kStages], k_free[T::kStages], v_full[T::kStages], v_free[T::kStages];
   uint64_t q_full, q_free, drained, s_full[2], p_full[2], o_done[2];
   uint32_t tmem;
   int gave_up;
-  float top[2][2][128];  // of the halves of a row: the largest score, then the sum
+  float top[T::kGroups][2][128];  // of the halves of a row: the largest score, then the sum
 };
 
 // CHUNK: the rows of every sequence over the prefix and its own tokens, causal (kernels_attn_chunk.cuh);
 // otherwise the rows of the whole batch over the prefix, whose part goes to dst_o and dst_lse.
-template <int D, bool CHUNK>
-__global__ void __launch_bounds__(kPreThreads, 1)
+template <int D, bool CHUNK, bool F32>
+__global__ void __launch_bounds__((PreShape<D, F32>::kThreads), 1)
 attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WideParams wide,
                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ CUtensorMap map_q) {
-  using T = PreShape<D>;
-  constexpr int NR = kRowsP, NST = T::kStages;
+  using T = PreShape<D, F32>;
+  using E16 = std::conditional_t<F32, float, uint16_t>;  // queries and output
+  static_assert(CHUNK || !F32, "the prefix pass takes bf16 queries");
+  constexpr int NR = T::kRows, NST = T::kStages, kSoftThreads = T::kSoft, kCopyWarp = T::kSoft / 32, kMmaWarp = kCopyWarp + 1;
   extern __shared__ uint8_t dyn[];
-  __shared__ PreShared<D> sh;
+  __shared__ PreShared<D, F32> sh;
   const uint32_t dyn_raw = (uint32_t)__cvta_generic_to_shared(dyn);
   const uint32_t base = (dyn_raw + 1023u) & ~1023u;
   uint8_t* const mem = dyn + (base - dyn_raw);
@@ -220,7 +229,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       mbar_init(bar(sh.v_full[i]), 1);
       mbar_init(bar(sh.v_free[i]), 1);
     }
-    mbar_init(bar(sh.q_full), CHUNK && wide.q_tma ? 1 : kPreSoft);
+    mbar_init(bar(sh.q_full), CHUNK && wide.q_tma ? 1 : kSoftThreads);
     mbar_init(bar(sh.q_free), 1);
     mbar_init(bar(sh.drained), 1);
     for (int w = 0; w < 2; ++w) {
@@ -231,7 +240,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     sh.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 17) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      (uint32_t)__cvta_generic_to_shared(&sh.tmem))
                  : "memory");
@@ -245,8 +254,8 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   const uint32_t tmem = sh.tmem;
   Place at = line.at;
   int left = line.end - line.begin;
-  const int group = CHUNK ? p.block_rows / 2 : 128;  // rows of a group
-  if (CHUNK && !line.ok) fill_nan<uint16_t, D>(p, blockIdx.x, gridDim.x, kPreThreads);
+  const int group = CHUNK ? p.block_rows / T::kGroups : 128;  // rows of a group
+  if (CHUNK && !line.ok) fill_nan<E16, D>(p, blockIdx.x, gridDim.x, T::kThreads);
   auto next = [&]() -> WideSeg {
     if constexpr (CHUNK) {
       return next_chunk(p, wide.c, at, left);
@@ -259,7 +268,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   };
   auto wide_tile = [&](const WideSeg& g, int tile) { return CHUNK ? tile + (tile < wide.c.pre_tiles ? 0 : g.w0) : tile; };
 
-  if (warp == 16) {
+  if (warp == kCopyWarp) {
     // ---- the rings of tiles ----
     if (lane == 0) {
       asm volatile("fence.proxy.async.global;" ::: "memory");  // the widened prefix was written with ordinary stores
@@ -268,7 +277,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         const WideSeg g = next();
         if (CHUNK && wide.q_tma && g.n > 0) {
           // the stretch's queries, as soon as the last scores of the one before are computed: while its ends are worked on
-          const int groups = g.rows * p.G - g.f0 > group ? 2 : 1;
+          const int groups = T::kGroups == 2 && g.rows * p.G - g.f0 > group ? 2 : 1;
           if (nseg > 0) tc_wait_one(bar(sh.q_free), (nseg - 1) & 1, gave_up, p.status);
           ++nseg;
           mbar_expect_arrive(bar(sh.q_full), groups * group * D * 2);
@@ -301,7 +310,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
     }
     __syncwarp();
-  } else if (warp == 17) {
+  } else if (warp == kMmaWarp) {
     // ---- the MMAs: of one group the values' sum of a tile and the next scores, then of the other ----
     constexpr uint32_t id_s = 1u << 4 | 1u << 7 | 1u << 10 | (128u >> 3) << 17 | 8u << 24;  // bf16 x bf16, K-major
     constexpr uint32_t id_o = 1u << 4 | 1u << 16 | (uint32_t)(D >> 3) << 17 | 8u << 24;      // f16 x f16, values token by token
@@ -309,17 +318,21 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
     int gi = 0, nseg = 0, done[2] = {0, 0};
     auto scores = [&](int w, int i) {
-      const uint32_t a = (base + T::oQ + w * 128 * D * 2) >> 4, b = (base + T::oK + (i % NST) * T::kTileBytes) >> 4;
+      const uint32_t b = (base + T::oK + (i % NST) * T::kTileBytes) >> 4;
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        const uint32_t off = (uint32_t)((s >> 2) * 16384 + (s & 3) * 32) >> 4;
-        mma_f16(tm + T::cS + w * 128, hi | (a + off), hi | (b + off), id_s, s > 0);
+      for (int part = T::kParts - 1; part >= 0; --part) {  // (the small parts first)
+        const uint32_t a = (base + T::oQ + (w * T::kParts + part) * 128 * D * 2) >> 4;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = (uint32_t)((s >> 2) * 16384 + (s & 3) * 32) >> 4;
+          mma_f16(tm + T::cS + w * 128, hi | (a + off), hi | (b + off), id_s, part < T::kParts - 1 || s > 0);
+        }
       }
       mma_commit(bar(sh.s_full[w]));
     };
     while (left > 0) {
       const WideSeg g = next();
-      const int n = __shfl_sync(kFull, g.n, 0), groups = __shfl_sync(kFull, g.rows * p.G - g.f0 > group ? 2 : 1, 0);
+      const int n = __shfl_sync(kFull, g.n, 0), groups = __shfl_sync(kFull, T::kGroups == 2 && g.rows * p.G - g.f0 > group ? 2 : 1, 0);
       if (n == 0) continue;
       tc_wait(bar(sh.q_full), nseg & 1, gave_up, p.status);
       ++nseg;
@@ -347,9 +360,11 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           if (elect()) {
             const uint32_t b = (base + T::oV + st * T::kTileBytes) >> 4;
 #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-              mma_f16_ts(tm + T::cO + w * 128, tm + T::cS + w * 128 + s * 8, hi | lbo_v | (b + s * (2048 >> 4)), id_o,
-                         s > 0 || k > 0);
+            for (int part = F32 ? 1 : 0; part >= 0; --part)
+#pragma unroll
+              for (int s = 0; s < kTile / 16; ++s)
+                mma_f16_ts(tm + T::cO + w * 128, tm + T::cS + w * 128 + part * 64 + s * 8, hi | lbo_v | (b + s * (2048 >> 4)), id_o,
+                           s > 0 || k > 0 || (F32 && part == 0));
             if (k + 1 < n)
               scores(w, gi + 1);
             else
@@ -385,7 +400,40 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       const int f = g.f0 + c, flat = CHUNK && t >= group ? 0 : g.rows * p.G;  // (rows past the group's are none)
       // half of this thread's query row into shared memory, swizzled
       bool bad = false;  // a query that is no finite number
-      if (!(CHUNK && wide.q_tma)) {
+      if constexpr (F32) {
+        // cut to bf16, what is left cut again, and again: exact (and what is no finite number leaves a NaN)
+        uint8_t* const q = mem + T::oQ;
+        const float* src = static_cast<const float*>(p.q) + (long long)(g.row0 + f / p.G) * p.q_row + (long long)(g.h * p.G + f % p.G) * p.q_head;
+        const bool vec = ((uintptr_t)src & 15) == 0;
+#pragma unroll 1
+        for (int i8 = 0; i8 < D / 16; ++i8) {
+          const int ch = half * (D / 16) + i8;
+          Raw8<float> r{};
+          if (f < flat) {
+            if (vec)
+              r.template load<true>(src + ch * 8);
+            else
+              r.template load<false>(src + ch * 8);
+          }
+          float x[8];
+          r.floats(x);
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t u = __float_as_uint(x[2 * i]) & 0xffff0000u, v = __float_as_uint(x[2 * i + 1]) & 0xffff0000u;
+              y[i] = u >> 16 | v;
+              x[2 * i] -= __uint_as_float(u);
+              x[2 * i + 1] -= __uint_as_float(v);
+            }
+            *reinterpret_cast<uint4*>(q + part * 128 * D * 2 + (ch >> 3) * 16384 + t * 128 + (((ch & 7) ^ (t & 7)) * 16)) =
+                make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+        fence_async();
+        mbar_arrive(bar(sh.q_full));
+      } else if (!(CHUNK && wide.q_tma)) {
         uint8_t* const q = mem + T::oQ + w * 128 * D * 2;
         const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(g.row0 + f / p.G) * p.q_row +
                               (long long)(g.h * p.G + f % p.G) * p.q_head;
@@ -414,7 +462,9 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       const bool have = g.rows * p.G - g.f0 > w * group;  // this group has rows
       // of the sequence's own tokens this row sees the first `own`
       const int own = CHUNK ? (f < flat ? g.len - g.rows + f / p.G + 1 : 0) : g.len, pre_tiles = CHUNK ? wide.c.pre_tiles : 0;
-      float m = 0.f, l = 0.f;
+      // Weights are 2^((s - far) c + E - m). Of scores in the millions c s + E - m keeps no places: such a row's are counted from
+      // the largest one, whose difference to others is exact.
+      float m = 0.f, l = 0.f, far = 0.f;
       if (have) {
         for (int k = 0; k < g.n; ++k, ++tiles_done) {
           const int tile = g.t0 + k;
@@ -441,6 +491,10 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             for (int i = 0; i < 64; ++i)
               if (i >= valid) s[i] = ninf;
           }
+          if (CHUNK && far != 0.f) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) s[i] -= far;
+          }
           if (CHUNK && mixed) {  // the values' exponents join the scores
             const float inv = 1.f / p.c;
             const float* ev = wide.ev + info * kTile + half * 64;
@@ -461,8 +515,16 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
             top = fmaxf(top, sh.top[w][half ^ 1][t]);
             const float x = fmaf(top, p.c, E - m);
             const bool renew = top != ninf && (k == 0 || x > kOverP);
-            const float d = renew ? x - kTopP : 0.f, fac = ex2(-d);
+            float d = renew ? x - kTopP : 0.f, shift = 0.f;
+            if (CHUNK && renew && fabsf(x) > kFarP) {
+              shift = top;
+              d = E - kTopP - m;
+#pragma unroll
+              for (int i = 0; i < 64; ++i) s[i] -= shift;
+            }
+            const float fac = ex2(CHUNK ? -fmaf(shift, p.c, d) : -d);
             m += d;
+            far += shift;
             if (k > 0) {  // the tiles before are summed: the scores' barrier stands behind their MMAs
               l *= fac;
 #pragma unroll 1
@@ -487,7 +549,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
           for (int i = 0; i < 64; i += 32) {
-            uint32_t h[16];
+            uint32_t h[16], rest[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
               float a, b;
@@ -496,8 +558,13 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
               b = ex2(b);
               sum[(j >> 1) & 3] = add2(sum[(j >> 1) & 3], pack(a, b));
               h[j / 2] = half2_of(a, b);
+              if constexpr (F32) {
+                const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&h[j / 2]));
+                rest[j / 2] = half2_of(a - r.x, b - r.y);
+              }
             }
             tc_st16(tS + half * 32 + i / 2, h);
+            if constexpr (F32) tc_st16(tS + 64 + half * 32 + i / 2, rest);
           }
           tc_wait_st();
           tc_before();
@@ -509,6 +576,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
         // ---- the end of the stretch ----
         if (!CHUNK && bad) l = nan;
+        if (CHUNK) m = fmaf(far, p.c, m);
         bar_sync(pair_bar, 64);  // the last maxima are read
         sh.top[w][half][t] = l;
         bar_sync(pair_bar, 64);
@@ -530,13 +598,20 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           if (half == 0) finish_lse(p, idx, r);
         }
         float* dst = whole ? (CHUNK ? nullptr : p.dst_o + idx * D) : slot + 2 * NR + c * D;
-        const float scale = (whole ? r.a : 1.f) * (1.f / (1 << (kValueShift + kSumShift)));
+        const float scale = (whole ? r.a : 1.f / kSumUnit<E16>) * (1.f / (1 << (kValueShift + kSumShift)));
 #pragma unroll 1
         for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 32) {
           float o[32];
           tc_ld32(tO + i, o);
           tc_wait_ld();
-          if (CHUNK && whole) {
+          if (F32 && whole) {
+            if (f < flat && in_idx(idx, (long long)p.R * p.Hq, p.status)) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<float4*>(static_cast<float*>(p.o) + idx * D + i + j) =
+                    make_float4(o[j] * scale, o[j + 1] * scale, o[j + 2] * scale, o[j + 3] * scale);
+            }
+          } else if (CHUNK && whole) {
             if (f < flat && in_idx(idx, (long long)p.R * p.Hq, p.status)) {
               uint32_t y[16];
 #pragma unroll
@@ -554,12 +629,12 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         }
         tc_before();
       }
-      if (!(CHUNK && wide.q_tma)) bar_sync(9, kPreSoft);  // both groups are done with the queries' memory
+      if (!(CHUNK && wide.q_tma)) bar_sync(9, kSoftThreads);  // both groups are done with the queries' memory
     }
   }
   tc_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == kMmaWarp) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }

@@ -73,11 +73,16 @@ constexpr int kMaxGridP = 160;   // of attn_prefix_kernel (one block an SM)
 // 288 rows x 2000 tokens 34 / 43 us, 1152 x 2000 51 / 57, 576 x 8192 66 / 69, 1152 x 8192
 // 105 / 83; head_dim 64, 576 x 2000 34.5 / 35.6, 1152 x 2000 51 / 47, 576 x 8192 64 / 51.
 constexpr long long kWideWork128 = 300000, kWideWork64 = 75000;
-// A chunk's sequences with at least so many rows (times heads of a kv head) are widened and
+// bf16 queries: a chunk's sequences with at least so many rows (times heads of a kv head) are widened and
 // computed in 256-row blocks, the others in the 48- or 32-row blocks of attn_tc_kernel.
 constexpr int kChunkFlat = 256;
 template <int D>
 constexpr int kSkipRows = D == 64 ? 32 : 48;  // rows of a row block of those
+// fp32 queries: from this much work on (rows times heads of a kv head, times the tables' tiles, times kv heads), if a sequence
+// may have this many rows; below it attn_f32_kernel. Calls, wide / attn_f32_kernel: work 8000, head_dim 128 33 / 46 us, 64 27 / 26;
+// 32768 in 32 rows a sequence 53 / 152; 281600 (2 x 400 rows behind 1000 tokens, 32/8 heads of 128) 75 / 1002.
+constexpr long long kChunkWork32 = 8000;
+constexpr int kChunkFlat32 = 32;
 constexpr size_t kChunkBytes = (size_t)32 << 30;  // most that a chunk's widened keys and values may take; past it, narrow blocks
 constexpr int kMaxGridT = 512;   // of the tensor-core kernel (two blocks an SM)
 
@@ -105,23 +110,24 @@ int tc_rows(long long flat, int head_dim) {
   return per <= 16 ? 16 : (int)(cdiv(per, 8) * 8);
 }
 
-// Rows of a chunk's 128-row tile: whole tokens, so that one load brings them.
-int chunk_group(int G) { return 128 / G * G; }
+// Rows of a chunk's row block: whole tokens in each 128-row tile, so that one load brings them; two tiles, one with fp32 queries.
+int chunk_rows(int G, spec_dtype dtype) { return (dtype == SPEC_BF16 ? 2 : 1) * (128 / G * G); }
 
 // The CHUNK pass: what it takes of the workspace from `off` on, and whether the call uses it.
-void chunk_layout(AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& c, size_t& off) {
+void chunk_layout(AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype, size_t& off) {
   const long long G = g.q_heads / c.kv_heads, flat = rows_of(g) * G, pre = cdiv(g.prefix_len, kTile);
   const long long most = cdiv((long long)g.pages_per_seq * c.page_size, kTile), nt = most > 1 ? most : 1;
   L.chunk = false;
-  if ((long long)(g.gamma + 1) * G < kChunkFlat) return;
+  if ((long long)(g.gamma + 1) * G < (dtype == SPEC_BF16 ? kChunkFlat : kChunkFlat32)) return;
+  if (dtype == SPEC_F32 && flat * (pre + nt) * c.kv_heads < kChunkWork32) return;
   L.chunk_tiles = pre + g.B * nt;
-  L.chunk_entries = flat / (2 * chunk_group((int)G)) + g.B;
+  L.chunk_entries = flat / chunk_rows((int)G, dtype) + g.B;
   const long long line = L.chunk_entries * c.kv_heads * (pre + nt + kSegCostC);
   const size_t wide = (size_t)2 * c.kv_heads * L.chunk_tiles * kTile * c.head_dim;
   if (line > kMaxLine || L.chunk_tiles * c.kv_heads > (1LL << 23) || 2 * wide > kChunkBytes) return;  // (tokens of the widened memory count in ints)
   L.chunk = true;
-  // with a prefix the narrow pass would be two; without one it is there for the short sequences of a packed batch
-  L.chunk_only = g.cu_draft == nullptr || g.prefix_len > 0;
+  // with a prefix the narrow pass would be two; without one it is there for the short sequences of a packed batch (bf16 queries)
+  L.chunk_only = g.cu_draft == nullptr || g.prefix_len > 0 || dtype == SPEC_F32;
   L.chunk_grid = line < kMaxGridP ? line : kMaxGridP;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -146,7 +152,7 @@ AttnLayout attn_layout(const spec_attn_batch& g, const spec_kv_cache& c, spec_dt
   const int G = g.q_heads / c.kv_heads;
   size_t off = 0;
   L.chunk = L.chunk_only = false;
-  if (chunk && dtype == SPEC_BF16) chunk_layout(L, g, c, off);
+  if (chunk) chunk_layout(L, g, c, dtype, off);
   if (L.chunk && L.chunk_only) {
     L.total = off;
     L.line = 0;
@@ -330,7 +336,7 @@ cudaError_t pass_prefix(const AttnParams& p, const spec_kv_cache& c, const AttnL
     return cudaErrorInvalidValue;
   cudaError_t e = start(widen_kernel<D>, dim3((unsigned)L.tiles, (unsigned)c.kv_heads), 256, 0, s, p, w);
   if (e != cudaSuccess) return e;
-  auto kern = attn_prefix_kernel<D, false>;
+  auto kern = attn_prefix_kernel<D, false, false>;
   static std::atomic<unsigned long long> done{0};
   if ((e = allow_smem(kern, done, PreShape<D>::kSmem)) != cudaSuccess) return e;
   const long long sms = sm_count();
@@ -355,13 +361,13 @@ bool query_map(CUtensorMap* m, const AttnParams& p, int D) {
 }
 
 // Long chunks: the plan, the widening, the attention, the joining of cut segments.
-template <int D>
+template <int D, bool F32>
 cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const spec_kv_cache& c, const AttnLayout& L, char* ws, cudaStream_t s) {
   AttnParams p = own;
   p.part = reinterpret_cast<float*>(ws + L.c_part);
   p.cut = reinterpret_cast<CutRec*>(ws + L.c_cut);
   p.seg_cost = kSegCostC;
-  p.block_rows = 2 * chunk_group(p.G);
+  p.block_rows = chunk_rows(p.G, F32 ? SPEC_F32 : SPEC_BF16);
   WideParams w;
   memset(&w, 0, sizeof(w));
   w.k16 = reinterpret_cast<uint16_t*>(ws + L.c_k16);
@@ -383,7 +389,8 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
       !wide_map(&m.v, w.v16, c, rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT16))
     return cudaErrorInvalidValue;
   CUtensorMap map_q;
-  w.q_tma = query_map(&map_q, p, D);
+  memset(&map_q, 0, sizeof(map_q));
+  w.q_tma = !F32 && query_map(&map_q, p, D);
   const long long sms = sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
   const int n = (int)(L.chunk_grid < sms ? L.chunk_grid : sms);
@@ -393,11 +400,12 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
   const long long units = L.chunk_tiles * c.kv_heads;
   e = start(chunk_widen_kernel<D>, dim3((unsigned)(units < 8 * sms ? units : 8 * sms)), kWidenThreads, 0, s, p, w);
   if (e != cudaSuccess) return e;
-  auto kern = attn_prefix_kernel<D, true>;
+  using T = PreShape<D, F32>;
+  auto kern = attn_prefix_kernel<D, true, F32>;
   static std::atomic<unsigned long long> done{0};
-  if ((e = allow_smem(kern, done, PreShape<D>::kSmem)) != cudaSuccess) return e;
-  e = start(kern, dim3((unsigned)n), kPreThreads, PreShape<D>::kSmem, s, p, w, m.k, m.v, map_q);
-  return e != cudaSuccess ? e : launch_merge<uint16_t, D, kRowsP>(p, n, s);
+  if ((e = allow_smem(kern, done, T::kSmem)) != cudaSuccess) return e;
+  e = start(kern, dim3((unsigned)n), T::kThreads, T::kSmem, s, p, w, m.k, m.v, map_q);
+  return e != cudaSuccess ? e : launch_merge<std::conditional_t<F32, float, uint16_t>, D, T::kRows>(p, n, s);
 }
 
 // One pass over keys: fp32 queries on the 32-bit kernel, bf16 queries on the tensor cores.
@@ -435,7 +443,11 @@ spec_status attend(const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype 
   AttnParams p = attn_params(g, c, q, q_row_stride, q_head_stride, o, lse, device_status,
                              dtype == SPEC_BF16 ? kSegCostT : kSegCostS);
   if (L.chunk) {
-    const cudaError_t err = c.head_dim == 64 ? pass_chunk<64>(p, g, c, L, ws, s) : pass_chunk<128>(p, g, c, L, ws, s);
+    cudaError_t err;
+    if (dtype == SPEC_BF16)
+      err = c.head_dim == 64 ? pass_chunk<64, false>(p, g, c, L, ws, s) : pass_chunk<128, false>(p, g, c, L, ws, s);
+    else
+      err = c.head_dim == 64 ? pass_chunk<64, true>(p, g, c, L, ws, s) : pass_chunk<128, true>(p, g, c, L, ws, s);
     if (err != cudaSuccess) return SPEC_ERR_CUDA;
     if (L.chunk_only) return SPEC_OK;
     p.skip_flat = kChunkFlat;

@@ -61,9 +61,10 @@ def test_prompts_beside_single_tokens(dev, dtype, dim, page, prefix):  # noqa: F
     Case(dev, lens, rows, heads=6, kv_heads=2, dim=dim, page=page, dtype=dtype, prefix=prefix).check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dim", [64, 128])
-def test_a_long_chunk(dev, dim):  # noqa: F811
-    Case(dev, [2200], [1500], heads=8, kv_heads=1, dim=dim, prefix=130).check()
+def test_a_long_chunk(dev, dim, dtype):  # noqa: F811
+    Case(dev, [2200], [1500], heads=8, kv_heads=1, dim=dim, prefix=130, dtype=dtype).check()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -150,17 +151,19 @@ def test_a_short_chunk_is_a_round(dev):  # noqa: F811
 
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("spread", [12, 30, 70])
-def test_values_of_very_different_size(dev, dim, spread):  # noqa: F811
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_of_very_different_size(dev, dim, spread, dtype):  # noqa: F811
     """Tokens whose values are 2^spread times their neighbours': rows before them do not see them and keep their places."""
-    c = Case(dev, [300, 420], [300, 270], heads=8, kv_heads=2, dim=dim, page=32, seed=3)
+    c = Case(dev, [300, 420], [300, 270], heads=8, kv_heads=2, dim=dim, page=32, seed=3, dtype=dtype)
     for b, t in ((0, 100), (0, 255), (1, 333)):
         c.exps[1][c.table[b][t // 32], 1, t % 32] += spread
     c.exps[1][c.table[1][40 // 32], 0, 40 % 32] -= min(spread, 60)
     c.check()
 
 
-def test_infinite_queries_and_rows_that_see_nothing(dev):  # noqa: F811
-    c = Case(dev, [290, 200], [290, 270], heads=4, kv_heads=1, dim=64)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_queries_and_rows_that_see_nothing(dev, dtype):  # noqa: F811
+    c = Case(dev, [290, 200], [290, 270], heads=8, kv_heads=2, dim=64, dtype=dtype)
     c.q[5, 1, 3], c.q[100, 2, 0], c.q[300, 0, 9], c.q[500, 3, 1] = np.inf, np.nan, np.inf, -np.inf  # (row 300 sees nothing)
     out = c.call()
     assert int(out["device_status"][0]) == 0
@@ -170,11 +173,35 @@ def test_infinite_queries_and_rows_that_see_nothing(dev):  # noqa: F811
     assert bad[5, 1] and bad[100, 2] and bad[500, 3] and int(bad.sum()) == 3
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_fp32_queries_of_every_size(dev, dim):  # noqa: F811
+    """Elements from 2^-40 to 2^30 of one another: nothing of a query is lost that its scores' roundings keep."""
+    c = Case(dev, [310, 290], [290, 290], heads=6, kv_heads=2, dim=dim, dtype="f32", seed=5)
+    c.q *= torch.exp2(torch.from_numpy(c.rng.integers(-40, 4, c.q.shape)).float())
+    c.q[7] *= 2.0 ** 30
+    c.q[9] = 0
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e9, 1e12])
+def test_scores_of_every_size(dev, dtype, size):  # noqa: F811
+    """Scores of thousands to 10^13: the weights are those of the largest, nothing overflows. (Where the two largest are nearer
+    than the roundings of such scores, the bounds ask for nothing; the output then lies between the values.)"""
+    c = Case(dev, [290, 700], [290, 290], heads=8, kv_heads=2, dim=128, dtype=dtype, prefix=140, seed=9)
+    c.q *= size
+    c.q[11] = -c.q[12]
+    out = c.check()
+    # values are below 2^9 times their exponent's power of two
+    assert float(out["o"].abs().max()) <= 2.0 ** (int(c.exps[1][c.exps[1] != 255].max()) - 127 + 9)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("batch,rows,ctx", [(40, 70, 100), (3, 900, 2000), (1100, 65, 0)])
-def test_many_and_long_sequences_repeat_bit_for_bit(dev, batch, rows, ctx):  # noqa: F811
+def test_many_and_long_sequences_repeat_bit_for_bit(dev, batch, rows, ctx, dtype):  # noqa: F811
     """More sequences than threads plan at once, cut segments; some sequences against the restatement."""
     lens = [rows + ctx * (i % 3) // 2 for i in range(batch)]
-    c = Case(dev, lens, [rows] * batch, heads=4, kv_heads=1, dim=64, page=16, size=0.7)
+    c = Case(dev, lens, [rows] * batch, heads=4, kv_heads=1, dim=64, page=16, size=0.7, dtype=dtype)
     a, b = c.call(), c.call()
     assert int(a["device_status"][0]) == 0 and torch.equal(a["o"], b["o"]) and torch.equal(a["lse"], b["lse"])
     saved, U.visible = U.visible, visible
@@ -187,9 +214,10 @@ def test_many_and_long_sequences_repeat_bit_for_bit(dev, batch, rows, ctx):  # n
         U.visible = saved
 
 
-def test_bounds_checked_build_of_a_ragged_batch(dev):  # noqa: F811
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bounds_checked_build_of_a_ragged_batch(dev, dtype):  # noqa: F811
     rows = [1, 400, 3, 64, 1, 129]
-    c = Case(dev, [900, 400, 300, 64, 1, 500], rows, heads=8, kv_heads=2, dim=128, page=64)
+    c = Case(dev, [900, 400, 300, 64, 1, 500], rows, heads=8, kv_heads=2, dim=128, page=64, dtype=dtype)
     a = c.check()
     with checked_build():
         b = c.call()
