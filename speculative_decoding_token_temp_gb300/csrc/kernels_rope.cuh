@@ -6,8 +6,8 @@
 //
 // Angles. A pair's frequency is held as turns a position in units of 2^-64 turn. The product
 // with a 32-bit position, modulo 2^64, is the angle reduced to one turn, exactly, for every
-// position: an angle of 10^6 radians in fp32 would be off by 0.03. Its upper 32 bits go to
-// sincospif as half turns (2^-32 of a turn, then fp32's own 2^-24 of the angle).
+// position: an angle of 10^6 radians in fp32 would be off by 0.03. Less its nearest quarter turn it
+// goes to sincospif as half turns of at most 1/4 (off by 2^-25 of that).
 //
 // A head's elements are rotated as f * (x_a * (w_a cos) + x_b * (w_b sin)), f = 1 / sqrt(...): the
 // weights join the row's sines and cosines, once for all its heads, and what lanes exchange are
@@ -16,7 +16,7 @@
 // All arithmetic is fp32 from the source's elements to the one rounding at the end: bf16 or
 // fp32 out, or the cache's codes (of the fp32 key, which is not rounded to bf16 on the way).
 //
-// What bounds it: HBM where rows are many: 32768 rows of 32 + 8 heads of 128 in bf16, 108 us, 6.2 TB/s
+// What bounds it: HBM where rows are many: 32768 rows of 32 + 8 heads of 128 in bf16, 110 us, 6.1 TB/s
 // of the measured 6.8 (instructions issued in 70 % of cycles). 2304 rows into the cache, whose data
 // is in L2: 13 us. A few rows: 4 us, the chain of loads, sines, barrier, exchange.
 #pragma once
@@ -122,10 +122,13 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(E) == 2 ? 4 : 3) rope_ker
       const int a = p.axis != nullptr ? min((int)__ldg(p.axis + j), p.axes - 1) : 0;
       const long long n = __ldg(p.pos + (long long)(row0 + r) * p.axes + a);
       const uint64_t turn = (uint64_t)n * __ldg(reinterpret_cast<const unsigned long long*>(p.step) + j);
+      // the nearest quarter turn, and what is left of it as half turns of at most 1/4 (a small number keeps more places)
+      const unsigned quarter = (unsigned)((turn + (1ull << 61)) >> 62);
+      const long long rest = (long long)(turn - ((uint64_t)quarter << 62));
       float s, c;
-      sincospif((float)(int)(turn >> 32) * (1.f / 2147483648.f), &s, &c);
-      s_cos[r][j] = c;
-      s_sin[r][j] = s;
+      sincospif((float)rest * (1.f / 9223372036854775808.f), &s, &c);
+      s_cos[r][j] = quarter & 1 ? (quarter & 2 ? s : -s) : (quarter & 2 ? -c : c);
+      s_sin[r][j] = quarter & 1 ? (quarter & 2 ? -c : c) : (quarter & 2 ? -s : s);
     }
   }
   for (int i = tid; i < 2 * D; i += kRopeThreads) {
@@ -181,7 +184,10 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(E) == 2 ? 4 : 3) rope_ker
       float sum = ss.x + ss.y;
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      f = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+      const float v = fmaf(sum, 1.f / D, p.eps);
+      f = rsqrtf(v);
+      const float off = fmaf(-v * f, f, 1.f);  // one step of Newton's takes the function's two places
+      f = fmaf(0.5f * f, v > 0.f && off < 1.f ? off : 0.f, f);
     }
     float y[8];
     if (p.interleaved) {
