@@ -223,3 +223,17 @@ def test_bounds_checked_build_of_a_ragged_batch(dev, dtype):  # noqa: F811
         b = c.call()
         assert int(b["device_status"][0]) == 0
     assert torch.equal(a["o"], b["o"]) and torch.equal(a["lse"], b["lse"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [1.0, 1e7])
+def test_segments_cut_into_many_parts(dev, dtype, dim, size):  # noqa: F811
+    """Few rows behind many tokens: parts of a row block's tokens in tens of blocks, joined; with a row that is NaN and a token."""
+    c = Case(dev, [4500, 80], [70, 70], heads=4, kv_heads=1, dim=dim, page=64, dtype=dtype, prefix=200, seed=4)
+    c.q *= size
+    c.q[30, 2, 5] = np.nan
+    c.exps[0][c.table[0][4460 // 64], 0, 4460 % 64] = 255  # token 4460: rows 30 to 69 of the first sequence see it
+    out = c.check()
+    bad = torch.isnan(out["o"]).any(-1)
+    assert not bad[:30].any() and bad[30:70].all() and not bad[70:].any()
