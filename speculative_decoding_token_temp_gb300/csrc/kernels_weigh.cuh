@@ -14,9 +14,9 @@
 // to 2^-39 of the row's largest element; an fp32 query is two of them (22 bits).
 //
 // Few rows leave it bound by the keys' bytes: 256 sequences x 1 row x 4 heads to 1-8192 tokens 186
-// us, 6.2 TB/s. More rows are bound by the latency of the MMAs' chains and the instructions around
-// them (12 warps an SM hold the widened codes): 8 windows of 32 rows x 4 heads behind 2000-16384
-// tokens 73 us, 280 TFLOP/s. Those would need the fifth-generation MMAs, whose scores come with
+// us, 6.2 TB/s. More rows are bound by the MMAs and the instructions around them, hardly side by
+// side (12 warps an SM hold the widened codes; with half of the MMAs left out 50 us): 8 windows of 32 rows x 4 heads behind 2000-16384
+// tokens 68 us, 300 TFLOP/s. Those would need the fifth-generation MMAs, whose scores come with
 // tokens on the lanes as well; not built.
 #pragma once
 
@@ -61,18 +61,21 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some)
 // half of the registers twice the warps fit an SM.
 template <typename E, int D, bool FEW>
 struct WeighShape {
-  static constexpr int kCols = FEW ? 8 : 64;  // rows (query rows times heads of a kv head) at a time
+  // Rows (query rows times heads of a kv head) at a time: the codes are read and widened again for each such number. 128 of
+  // bf16 (35 KB at head_dim 128) leave room for the blocks that the registers allow: 8 windows of 32 rows x 4 heads 68 us,
+  // with 64 at a time 73. fp32 queries are two parts, and 128 of them would cost a block an SM.
+  static constexpr int kCols = FEW ? 8 : sizeof(E) == 2 ? 128 : 64;
   static constexpr int kRing = kWeighThreads * kWeighStages * D;  // bytes
   static constexpr int kParts = sizeof(E) == 2 ? 1 : 2;
   static constexpr int kStride = D + 8;  // halves of a row: neighbouring rows' 16-byte loads fall into different banks
 };
 
-// Columns c0 on of a segment's rows into shared memory, two threads a column.
+// Columns c0 + at on of a segment's rows to columns `at` on of shared memory, two threads a column.
 template <typename E, int D, bool FEW>
-__device__ __forceinline__ void weigh_stage(const WeighParams& p, const Seg& g, int counted, int c0, __half* q, float* rq, float* neg, int* lim) {
+__device__ __forceinline__ void weigh_stage(const WeighParams& p, const Seg& g, int counted, int c0, int at, __half* q, float* rq, float* neg, int* lim) {
   using T = WeighShape<E, D, FEW>;
   const AttnParams& a = p.a;
-  const int col = threadIdx.x >> 1, part = threadIdx.x & 1, f = c0 + col, i = f / a.G;
+  const int col = at + (threadIdx.x >> 1), part = threadIdx.x & 1, f = c0 + col, i = f / a.G;
   if (FEW && threadIdx.x >= 32) return;  // (whole warps)
   bool here = f < g.rows * a.G && i < counted;
   float x[D / 2];
@@ -230,7 +233,9 @@ __global__ void __launch_bounds__(kWeighThreads, FEW ? (sizeof(E) == 2 ? 5 : 4) 
     const int ctx = g.len - g.rows;
     for (int c0 = 0; c0 == 0 || c0 < counted * a.G; c0 += kCols) {
       __syncthreads();
-      weigh_stage<E, D, FEW>(p, g, counted, c0, s_q, s_rq, s_neg, s_lim);
+#pragma unroll 1
+      for (int at_col = 0; at_col < (FEW ? 1 : min(kCols, counted * a.G - c0)); at_col += kWeighThreads / 2)
+        weigh_stage<E, D, FEW>(p, g, counted, c0, at_col, s_q, s_rq, s_neg, s_lim);
       __syncthreads();
       const int tiles_n = min(kCols, counted * a.G - c0 + 7) / 8;  // of 8 columns
       // A warp's tiles pass through a ring of its own: the codes of tiles ahead are on their way to shared memory, and of the

@@ -116,6 +116,19 @@ def test_ragged_rounds_and_accepted_rows(dev, dtype, keep):  # noqa: F811
     check_weigh(c, keep=keep, taken=[0, 1, 5, 8, 0, 3, 0, 11, 7])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_and_heads_at_every_edge_of_what_is_worked_on_at_a_time(dev, dtype, dim):  # noqa: F811
+    # 16 query heads a kv head: 128, 16, 80, 64, 112, 48, 96, 32 of a sequence's rows and heads one behind another, and
+    # three heads a kv head: 129, 126, 66, 63, 15, 18
+    rows = [8, 1, 5, 4, 7, 3, 6, 2]
+    check_weigh(Case(dev, [300 + 41 * i for i in range(8)], rows, heads=32, kv_heads=2, dim=dim, page=32, dtype=dtype), keep=0.5)
+    rows = [43, 42, 22, 21, 5, 6, 86, 85]
+    c = Case(dev, [600 - 17 * i for i in range(8)], rows, heads=6, kv_heads=2, dim=dim, page=32, dtype=dtype)
+    check_weigh(c)
+    check_weigh(c, keep=0.0, taken=[42, 20, 21, 0, 4, 2, 43, 64])
+
+
 def test_weights_of_a_row_sum_to_one_behind_a_prefix_to_less(dev):  # noqa: F811
     c = Case(dev, [500, 700], [4, 4], heads=8, kv_heads=2, dim=128)
     got = check_weigh(c, keep=0.0)
