@@ -581,6 +581,12 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         sh.top[w][half][t] = l;
         bar_sync(pair_bar, 64);
         l += sh.top[w][half ^ 1][t];
+        if constexpr (CHUNK) {
+          // Every score of a row that sees tokens of this stretch was -inf, as a hidden token's is: an infinite query met keys of
+          // one sign (or scores passed fp32's range). That row is NaN; only one that sees none of the stretch has no part in it.
+          const bool sees = f < flat && (g.t0 < pre_tiles || own > (g.t0 - pre_tiles) * kTile);
+          if (sees && l == 0.f) l = nan;
+        }
         tc_wait(bar(sh.o_done[w]), ends & 1, gave_up, p.status);
         ++ends;
         tc_after();

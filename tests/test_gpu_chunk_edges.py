@@ -1,0 +1,67 @@
+"""spec_attention_chunk where single places decide: infinite queries that meet keys of one sign, in rows that see one token
+and in rows that see thousands."""
+import numpy as np
+import pytest
+import torch
+
+import kv_util as U
+from test_gpu_attention import dev  # noqa: F401 (dev: the fixture)
+from test_gpu_chunk import Case
+
+pytestmark = pytest.mark.gpu
+
+PLUS, MINUS = 56, 184  # the codes of 1 and -1
+
+
+def off_the_grid(q, dev):  # noqa: F811
+    """The queries as a view that starts one element into its buffer, rows off the 16-byte grid."""
+    rows, heads, dim = q.shape
+    buf = torch.zeros(rows, heads * dim + 3, dtype=q.dtype, device=dev)
+    view = buf[:, 1:1 + heads * dim].unflatten(1, (heads, dim))
+    view.copy_(q)
+    return view
+
+
+def check_nan_rows(c, layout, bad):
+    """The rows and heads `bad`, and no others, are NaN, log-sums among them; the others are the restatement's."""
+    out = c.call(q=c.q.to(c.dev) if layout == "packed" else off_the_grid(c.q, c.dev))
+    assert int(out["device_status"][0]) == 0
+    got = torch.isnan(out["o"]).any(-1)
+    want = torch.zeros_like(got)
+    for r, h in bad:
+        want[r, h] = True
+        c.q[r, h] = 0  # (an infinity has no bound; what such a row gives is asked for above)
+    assert torch.equal(got, want) and torch.equal(torch.isnan(out["o"]).all(-1), want) and torch.equal(torch.isnan(out["lse"]), want)
+    o, lse, spread, dx = c.ref()
+    keep = ~want.cpu().numpy()
+    U.compare(out["o"][torch.from_numpy(keep)], out["lse"][torch.from_numpy(keep)], (o[keep], lse[keep], spread[keep], dx[:, keep]), c.dtype,
+              max(c.lens) + c.prefix)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["packed", "odd"])
+@pytest.mark.parametrize("code", [PLUS, MINUS])
+@pytest.mark.parametrize("dim,prefix,lens", [(64, 0, [290, 290]), (128, 0, [290, 100]), (128, 1, [290, 290]), (64, 130, [290, 0]),
+                                             (128, 0, [9000, 290]), (64, 257, [6000, 290])])
+def test_infinite_queries_that_meet_keys_of_one_sign(dev, dtype, layout, code, dim, prefix, lens):  # noqa: F811
+    """Every key has the same number in the place that the infinity meets, so that all scores of the row are one infinity:
+    +inf or -inf, in the first rows, in later ones, in several heads, and in whole segments and in cut ones (the long
+    contexts). Rows that see nothing are zeros whatever they hold."""
+    rows = 290
+    c = Case(dev, lens, [rows] * 2, heads=4, kv_heads=2, dim=dim, page=64, dtype=dtype, prefix=prefix, seed=11)
+    c.codes[0][..., 9] = code
+    bad = []
+    for b, n in enumerate(lens):
+        first = 0 if prefix else max(0, rows - n)  # the first row that sees a token
+        for i, (r, h) in enumerate([(first, 0), (first, 3), (first + 1, 1), (first + 2, 2), (first + 2, 3), (rows - 1, 0), (rows - 1, 2)]):
+            if r < rows:
+                c.q[b * rows + r, h, 9] = np.inf if i % 2 else -np.inf
+                bad.append((b * rows + r, h))
+        if first:
+            c.q[b * rows, 1, 9] = c.q[b * rows + first - 1, 2, 9] = -np.inf  # they see nothing
+    for b, n in enumerate(lens):
+        if not prefix and n < rows:
+            zero = c.call()["o"][b * rows:b * rows + rows - n]
+            assert (zero == 0).all()
+            c.q[b * rows, 1, 9] = c.q[b * rows + rows - n - 1, 2, 9] = 0
+    check_nan_rows(c, layout, bad)
