@@ -23,7 +23,7 @@ LIB_BOUNDS = os.path.join(PKG, "libspecverify_bounds.so")
 SOURCES = ["spec_verify.cu", "spec_kv.cu", "spec_kv_ops.cu"]
 HEADERS = ["kernels.cuh", "kernels_rows.cuh", "kernels_sample.cuh", "kernels_multi.cuh", "plan.h",
            "kernels_kv.cuh", "kernels_attn.cuh", "kernels_attn_tc.cuh",
-           "kernels_attn_prefix.cuh", "kernels_attn_chunk.cuh", "kernels_rope.cuh", "kernels_weigh.cuh", "kernels_evict.cuh", "kv_host.h"]
+           "kernels_attn_prefix.cuh", "kernels_attn_chunk.cuh", "chunk_plan.h", "kernels_rope.cuh", "kernels_weigh.cuh", "kernels_evict.cuh", "kv_host.h"]
 PUBLIC = ["spec_verify.h", "spec_kv.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

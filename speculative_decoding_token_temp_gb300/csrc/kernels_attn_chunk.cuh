@@ -32,6 +32,7 @@
 // 0-16384 tokens 767 us, 1.4 PFLOP/s.
 #pragma once
 
+#include "chunk_plan.h"
 #include "kernels_attn_tc.cuh"
 
 namespace sv {
@@ -49,7 +50,6 @@ struct ChunkEntry {
 };
 
 constexpr int kPlanBuckets = 1024;  // of lengths, one a thread of the plan
-constexpr int kJoinCost = 9;        // the joining of cut segments (15 us), in tiles
 
 // The segment that block b of n takes in round r: to and fro, so that who got the longest of a round gets the shortest of the next.
 __device__ __forceinline__ long long chunk_item(int r, int b, int n) { return (long long)r * n + (r & 1 ? n - 1 - b : b); }
@@ -169,9 +169,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     if (e < entries) c.entry[e].start = at;
     line += all;
   }
-  // Whole segments, or equal parts of the line? Cut segments cost their beginning and end twice and the joining; whole ones
-  // leave blocks with more and with less. Sorted by length and dealt out to and fro they are often even enough: what the
-  // busiest block then gets is added up here.
+  // Whole segments, or equal parts of the line (whole_segments)? What the busiest block would get of whole ones, sorted by
+  // length and dealt out to and fro, is added up here.
   __shared__ int s_hist[kPlanBuckets], s_most, s_long;
   if (tid == 0) s_most = 0, s_long = 1;
   for (int i = tid; i < kPlanBuckets; i += kPlanThreads) s_hist[i] = 0;
@@ -191,10 +190,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   for (int e = tid; e < entries; e += kPlanThreads) c.order[atomicAdd(&s_hist[kPlanBuckets - 1 - (c.entry[e].nt - 1) / unit], 1)] = e;
   __syncthreads();
   const long long items = (long long)entries * p.Hk;
-  if (items <= 64LL * c.blocks) {
+  if (items <= (long long)kPlanRounds * c.blocks) {
     for (int b = tid; b < c.blocks; b += kPlanThreads) {
       int sum = 0;
-      for (int r = 0; r < 64; ++r) {
+      for (int r = 0; r < kPlanRounds; ++r) {
         const long long i = chunk_item(r, b, c.blocks);
         if (i >= items) break;
         sum += ((c.entry[c.order[i / p.Hk]].nt - 1) / unit + 1) * unit + p.seg_cost;  // (by its bucket: the same whatever the order within)
@@ -204,8 +203,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   }
   __syncthreads();
   if (tid == 0) {
-    // past 64 segments a block the line's cuts count for little, and so does the unevenness: whole ones then
-    const bool even = items > 64LL * c.blocks || (s_most > 0 && s_most <= line / c.blocks + p.seg_cost + kJoinCost);
+    const bool even = whole_segments(items, c.blocks, s_most, s_long, line, p.seg_cost);
     *c.head = ChunkHead{entries, line, tiles, even ? 1 : 0};
   }
   if (bits) atomicOr(p.status, bits);

@@ -6,7 +6,7 @@ import torch
 
 import kv_util as U
 from test_gpu_attention import dev  # noqa: F401 (dev: the fixture)
-from test_gpu_chunk import Case
+from test_gpu_chunk import Case, visible
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,26 @@ def test_infinite_queries_that_meet_keys_of_one_sign(dev, dtype, layout, code, d
             assert (zero == 0).all()
             c.q[b * rows, 1, 9] = c.q[b * rows + rows - n - 1, 2, 9] = 0
     check_nan_rows(c, layout, bad)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [2997, 6997])
+def test_one_long_sequence_among_many_short_ones(dev, dtype, tokens):  # noqa: F811
+    """More than 64 segments a block, nearly all of two tiles and some of tens (as many as to
+    leave the segments whole, and so many that they are cut): the same bits every time, and rows of short and
+    long sequences as the restatement has them."""
+    B, long = 1250, 777
+    rows, lens = [1] * B, [1 + i % 5 for i in range(B)]
+    rows[long], lens[long] = 256, tokens
+    c = Case(dev, lens, rows, heads=8, kv_heads=8, dim=64, page=256, dtype=dtype, prefix=3, seed=12)
+    a, b = c.call(), c.call()
+    assert int(a["device_status"][0]) == 0 and torch.equal(a["o"], b["o"]) and torch.equal(a["lse"], b["lse"])
+    starts = np.concatenate([[0], np.cumsum(rows)])
+    saved, U.visible = U.visible, visible
+    try:
+        for i in (0, 3, long - 1, long, long + 1, B - 1):
+            at = np.arange(starts[i], starts[i] + rows[i])
+            ref = U.attention(c.q[at].double().numpy(), c.cache(), [c.table[i]], [lens[i]], [rows[i]], prefix_table=c.prefix_table, prefix_len=3)
+            U.compare(a["o"][at], a["lse"][at], ref, c.dtype, lens[i] + 3)
+    finally:
+        U.visible = saved
