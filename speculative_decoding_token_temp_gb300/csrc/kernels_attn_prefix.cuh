@@ -262,7 +262,7 @@ attn_prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     } else {
       WideSeg g;
       static_cast<Seg&>(g) = next_seg<NR>(p, at, left);
-      g.w0 = 0;
+      g.row0 = g.w0 = 0;  // (all rows of the batch)
       return g;
     }
   };
