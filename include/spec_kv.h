@@ -161,6 +161,12 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
  * the chunk's own up to i; a packed batch may mix prompts with single tokens. Where fp32
  * queries' rows are many, their 24 bits enter the scores and a weight enters the values' sum
  * with 22 bits down to 2^-32 of the row's largest weight.
+ *
+ * How much one call takes: its row blocks (of 256 rows times heads of a kv head, 128 with fp32
+ * queries), each counted with the 128-token tiles of the page table that it may see (in a packed
+ * batch of several sequences: all of them) and four more, over all kv heads, come to at most
+ * 2^31 - 2^25. Past that the call is refused (SPEC_ERR_INVALID_ARG, a size of 0). A prompt of
+ * 2^20 rows from the beginning at 32 query and 8 kv heads is a quarter of it, half with fp32 queries.
  */
 size_t spec_attention_chunk_workspace_bytes(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype);
 spec_status spec_attention_chunk(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype, const void* q, int64_t q_row_stride,

@@ -84,6 +84,8 @@ constexpr int kSkipRows = D == 64 ? 32 : 48;  // rows of a row block of those
 constexpr long long kChunkWork32 = 8000;
 constexpr int kChunkFlat32 = 32;
 constexpr size_t kChunkBytes = (size_t)32 << 30;  // most that a chunk's widened keys and values may take; past it, narrow blocks
+// Longest line of a chunk's row blocks: its places, and the end of a segment that begins on it (at most 2^23 tiles), fit an int.
+constexpr long long kMaxChunkLine = (1LL << 31) - (1LL << 25);
 constexpr int kMaxGridT = 512;   // of the tensor-core kernel (two blocks an SM)
 
 struct AttnLayout {
@@ -113,6 +115,21 @@ int tc_rows(long long flat, int head_dim) {
 // Rows of a chunk's row block: whole tokens in each 128-row tile, so that one load brings them; two tiles, one with fp32 queries.
 int chunk_rows(int G, spec_dtype dtype) { return (dtype == SPEC_BF16 ? 2 : 1) * (128 / G * G); }
 
+// At most so many tiles of all row blocks of a chunk call, segments' ends among them, for one kv head. Row block rb of a
+// sequence of n rows sees no more than the table holds less the rows behind its last: half of a long prompt's square. Counted so
+// where every sequence's rows are known and their whole square is too long.
+long long chunk_line(const AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& c, int G, int nr, long long pre, long long nt) {
+  const long long square = L.chunk_entries * (pre + nt + kSegCostC);
+  if (square * c.kv_heads <= kMaxChunkLine || (g.cu_draft != nullptr && g.B > 1)) return square;
+  const long long rows = (long long)g.total_draft / g.B + 1, blocks = cdiv(rows * G, nr), most = (long long)g.pages_per_seq * c.page_size;
+  long long sum = 0;
+  for (long long rb = 0; rb < blocks; ++rb) {
+    const long long last = ((rb + 1) * nr - 1) / G + 1, sees = most - rows + (last < rows ? last : rows), tiles = pre + (sees > 0 ? cdiv(sees, kTile) : 0);
+    sum += (tiles > 1 ? tiles : 1) + kSegCostC;
+  }
+  return sum * g.B;
+}
+
 // The CHUNK pass: what it takes of the workspace from `off` on, and whether the call uses it.
 void chunk_layout(AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& c, spec_dtype dtype, size_t& off) {
   const long long G = g.q_heads / c.kv_heads, flat = rows_of(g) * G, pre = cdiv(g.prefix_len, kTile);
@@ -122,9 +139,9 @@ void chunk_layout(AttnLayout& L, const spec_attn_batch& g, const spec_kv_cache& 
   if (dtype == SPEC_F32 && flat * (pre + nt) * c.kv_heads < kChunkWork32) return;
   L.chunk_tiles = pre + g.B * nt;
   L.chunk_entries = flat / chunk_rows((int)G, dtype) + g.B;
-  const long long line = L.chunk_entries * c.kv_heads * (pre + nt + kSegCostC);
+  const long long line = chunk_line(L, g, c, (int)G, chunk_rows((int)G, dtype), pre, nt) * c.kv_heads;
   const size_t wide = (size_t)2 * c.kv_heads * L.chunk_tiles * kTile * c.head_dim;
-  if (line > kMaxLine || L.chunk_tiles * c.kv_heads > (1LL << 23) || 2 * wide > kChunkBytes) return;  // (tokens of the widened memory count in ints)
+  if (line > kMaxChunkLine || L.chunk_tiles * c.kv_heads > (1LL << 23) || 2 * wide > kChunkBytes) return;  // (tokens of the widened memory count in ints)
   L.chunk = true;
   // with a prefix the narrow pass would be two; without one it is there for the short sequences of a packed batch (bf16 queries)
   L.chunk_only = g.cu_draft == nullptr || g.prefix_len > 0 || dtype == SPEC_F32;

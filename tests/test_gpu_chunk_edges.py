@@ -4,6 +4,8 @@ import numpy as np
 import pytest
 import torch
 
+from speculative_decoding_token_temp_gb300 import api
+
 import kv_util as U
 from test_gpu_attention import dev  # noqa: F401 (dev: the fixture)
 from test_gpu_chunk import Case, visible
@@ -88,3 +90,25 @@ def test_one_long_sequence_among_many_short_ones(dev, dtype, tokens):  # noqa: F
             U.compare(a["o"][at], a["lse"][at], ref, c.dtype, lens[i] + 3)
     finally:
         U.visible = saved
+
+
+def test_the_longest_chunk(dev):  # noqa: F811
+    """2^20 rows from the beginning: rows at both ends and between, each against the definition over its own tokens (bounds of
+    kv_util for the tokens that it sees)."""
+    n, page, heads, dim = 1 << 20, 256, 2, 64
+    gen = torch.Generator(device=dev).manual_seed(3)
+    k, v = ((torch.randn(n // page, 1, page, dim, generator=gen, device=dev) * 100).clamp(-448, 448).to(torch.float8_e4m3fn) for _ in range(2))
+    ke, ve = (torch.randint(118, 122, (n // page, 1, page), generator=gen, device=dev, dtype=torch.uint8) for _ in range(2))
+    order = torch.randperm(n // page, generator=gen, device=dev)
+    q = torch.randn(n, heads, dim, generator=gen, device=dev).bfloat16()
+    out = api.spec_attention_chunk(q, api.KVCache(k, v, ke, ve), order.to(torch.int32).view(1, -1), torch.tensor([n], dtype=torch.int32, device=dev),
+                                   gamma=n - 1, want_lse=True)
+    assert int(out["device_status"][0]) == 0
+    keys, values = (x[order].double().view(n, dim) * torch.exp2(e[order].double().view(n, 1) - 127) for x, e in ((k, ke), (v, ve)))
+    for r in (0, 1, 127, 128, 300, 65_537, 524_287, 1_000_003, n - 2, n - 1):
+        s = q[r].double() @ keys[:r + 1].T * dim ** -0.5
+        w = torch.softmax(s, -1)
+        size = keys[:r + 1].abs()
+        dx = [(q[r].double().abs() @ size.T).amax(-1) * dim ** -0.5, q[r].double().abs().amax(-1) * size.sum(-1).max() * dim ** -0.5]
+        ref = [x.cpu().numpy() for x in (w @ values[:r + 1], torch.logsumexp(s, -1), w @ values[:r + 1].abs(), torch.stack(dx))]
+        U.compare(out["o"][r], out["lse"][r], ref, torch.bfloat16, r + 1)
