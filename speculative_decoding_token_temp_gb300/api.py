@@ -950,8 +950,9 @@ def spec_kv_weigh(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_
     q, kv_len, gamma, cu_draft, scale as in the round's attention call (chains); lse [rows, q_heads]
     is what that call left (want_lse). n_accepted int32 [B]: only rows 0..n_accepted[b] count, as a
     verification leaves it. The round's own tokens begin at 0; keep = 0 reads no old mass, so
-    that mass needs no initialisation before a first call that covers a sequence. Returns the
-    dict with device_status."""
+    that mass needs no initialisation before a first call that covers a sequence. The sequences'
+    pages must be their own: where two sequences of a call share a page with tokens of theirs (a
+    prompt kept once), their sums overwrite one another. Returns the dict with device_status."""
     dt = _KV_DTYPES.get(q.dtype)
     if dt is None:
         raise TypeError(f"q must be bfloat16 or float32, got {q.dtype}")
