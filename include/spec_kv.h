@@ -162,6 +162,12 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
  * queries' rows are many, their 24 bits enter the scores and a weight enters the values' sum
  * with 22 bits down to 2^-32 of the row's largest weight.
  *
+ * Workspace. Long chunks are computed from keys and values widened to 16 bits: 4 bytes for each
+ * element of the keys that the page table and the prefix have room for, not what kv_len says is
+ * there (8.6 GB for 64 sequences of up to 32768 tokens at 8 kv heads of 128). Where that passes 32 GB, or
+ * the tables' 128-token tiles times kv heads 2^23, the call takes smaller row blocks that read the
+ * cache itself, several times slower; fp32 queries' choice counts the tables' tiles too.
+ *
  * How much one call takes: its row blocks (of 256 rows times heads of a kv head, 128 with fp32
  * queries), each counted with the 128-token tiles of the page table that it may see (in a packed
  * batch of several sequences: all of them) and four more, over all kv heads, come to at most

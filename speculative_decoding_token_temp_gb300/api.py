@@ -768,7 +768,14 @@ def spec_attention_chunk(q: torch.Tensor, cache: KVCache, page_table: torch.Tens
                          out: dict | None = None, workspace=None, device_status=None) -> dict:
     """Attention of chunks of new tokens over the cache: spec_attention (without trees) for up to
     2^20 rows a sequence, whose arguments, layouts and results it shares. A chunk of n tokens
-    has gamma = n - 1; packed batches (cu_draft) may mix prompts with single tokens."""
+    has gamma = n - 1; packed batches (cu_draft) may mix prompts with single tokens.
+
+    Long chunks are computed from the cached keys and values in 16 bits, for which the workspace has
+    4 bytes for each element of the keys that page_table (and the prefix) have room for, whatever
+    kv_len says: 8.6 GB for 64 sequences of up to 32768 tokens at 8 kv heads of 128. The default
+    workspace keeps that, for each stream. Pass a page_table no wider than the sequences need; past 32 GB
+    (or 2^23 tiles of 128 tokens and kv heads) the call takes smaller row blocks that read the cache
+    itself, several times slower. fp32 queries choose between their two kernels by that width too."""
     lib = _lib.lib()
     return _attend("spec_attention_chunk", lib.spec_attention_chunk, lib.spec_attention_chunk_workspace_bytes, q, cache, page_table, kv_len,
                    gamma, cu_draft, None, scale, prefix_table, prefix_len, want_lse, out, workspace, device_status)
@@ -882,7 +889,7 @@ def spec_qk_rope(q: torch.Tensor, k: torch.Tensor, rope: Rope, positions: torch.
     q [rows, q_heads, head_dim], k [rows, k_heads, head_dim] in bfloat16 or float32; slices of a
     fused projection are taken as they are. positions int32 [rows] or [rows, rope.axes]. eps
     turns the norms on, x * weight / sqrt(mean(x^2) + eps), with weights [head_dim] of q's type
-    or none. Returns q and k, contiguous, of the same type."""
+    or none. Returns q and k, contiguous, of the same type; what `out` holds must not overlap the inputs."""
     dt = _KV_DTYPES.get(q.dtype)
     if dt is None or k.dtype is not q.dtype:
         raise TypeError(f"q and k must both be bfloat16 or float32, got {q.dtype} and {k.dtype}")
@@ -911,7 +918,7 @@ def spec_qk_rope_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor, v: tor
 
     positions are the rotation's and independent of row_pos, the rows' places in the cache: they
     differ behind a shared prefix, after an eviction, or with several axes. Returns q
-    [rows, q_heads, head_dim] and device_status."""
+    [rows, q_heads, head_dim] (which must not overlap the inputs) and device_status."""
     dt = _KV_DTYPES.get(q.dtype)
     if dt is None or k.dtype is not q.dtype or v.dtype is not q.dtype:
         raise TypeError(f"q, k and v must all be bfloat16 or float32, got {q.dtype}, {k.dtype} and {v.dtype}")
