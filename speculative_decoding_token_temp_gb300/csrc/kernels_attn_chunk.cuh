@@ -217,7 +217,7 @@ struct WideParams {
   // chunks
   float2* info;  // [kv head][tile]: E, and whether the tile is mixed
   float* ev;     // [kv head][tile][128]: a mixed tile's E, token by token
-  int q_tma;     // queries come by TMA (kv head groups of a power of two, rows on the 16-byte grid)
+  int q_tma;     // bf16 queries come by TMA, whole tokens a load (any number of heads a kv head; rows and heads on the 16-byte grid)
   ChunkParams c;
 };
 

@@ -74,7 +74,13 @@ constexpr int kMaxGridP = 160;   // of attn_prefix_kernel (one block an SM)
 // 105 / 83; head_dim 64, 576 x 2000 34.5 / 35.6, 1152 x 2000 51 / 47, 576 x 8192 64 / 51.
 constexpr long long kWideWork128 = 300000, kWideWork64 = 75000;
 // bf16 queries: a chunk's sequences with at least so many rows (times heads of a kv head) are widened and
-// computed in 256-row blocks, the others in the 48- or 32-row blocks of attn_tc_kernel.
+// computed in 256-row blocks, the others in the 48- or 32-row blocks of attn_tc_kernel. Whole calls from the beginning / behind
+// 2000 / behind 16384 tokens, 32/8 heads of 128, wide against narrow, us:
+//   256 rows x 1 sequence 21.7 / 34.9 / 58.9 against 14.0 / 20.6 / 51.4, x 8 24.3 / 64.6 / 259 against 21.9 / 61.6 / 312,
+//   x 32 33.7 / 159 / 933 against 50.5 / 207 / 1186;
+//   512 rows x 1 sequence 23.1 / 35.0 / 70.9 against 14.8 / 25.7 / 81.1, x 8 24.7 / 67.2 / 355 against 30.5 / 102 / 554.
+// head_dim 64: 256 rows x 1 19.6 / 29.6 / 42.7 against 11.7 / 17.7 / 48.2, x 8 21.9 / 48.5 / 168 against 17.7 / 57.9 / 302.
+// One short sequence by itself loses up to 15 us to the plan, the widening and the joining; several, or a long context, gain.
 constexpr int kChunkFlat = 256;
 template <int D>
 constexpr int kSkipRows = D == 64 ? 32 : 48;  // rows of a row block of those
