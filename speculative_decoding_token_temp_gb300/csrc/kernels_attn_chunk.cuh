@@ -221,21 +221,6 @@ struct WideParams {
   ChunkParams c;
 };
 
-// Stands for the exponent of a vector of zeros, which is stored under one far below others': it would spread a tile's exponents,
-// though a zero value needs no places (4096-token prompt with such a value every 128 tokens: 359 -> 127 us).
-constexpr float kZeroValue = -150.f;
-
-template <int D>
-__device__ __noinline__ bool zeros(const uint8_t* codes) {
-  uint32_t any = 0;
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(codes) + i);
-    any |= x.x | x.y | x.z | x.w;
-  }
-  return (any & 0x7f7f7f7fu) == 0;
-}
-
 // A unit is one tile of one kv head; the grid strides over them. The first 128 threads look the
 // tokens up; then D / 8 lanes take a token, 8 codes and one 16-byte store of each operand a lane.
 template <int D>
@@ -285,14 +270,13 @@ __global__ void __launch_bounds__(kWidenThreads) chunk_widen_kernel(const __grid
           if (kb != kNanExp && vb != kNanExp) {
             ks = exp_value(kb);
             ev = (float)((int)vb - kExpBias);
-            if (vb == kExpBias + SPEC_KV_ZERO_EXP && zeros<D>(p.v + vec * D)) ev = kZeroValue;
           }
         }
       }
       s_vec[tid] = vec;
       s_ks[tid] = ks;  // NaN: of a token that is not to be read as numbers
       s_ev[tid] = ev;
-      float most = ev, least = ev <= kZeroValue ? 1e30f : ev;
+      float most = ev, least = ev < -200.f ? 1e30f : ev;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
@@ -303,12 +287,11 @@ __global__ void __launch_bounds__(kWidenThreads) chunk_widen_kernel(const __grid
     __syncthreads();
     float e = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
     const float least = fminf(fminf(s_min[0], s_min[1]), fminf(s_min[2], s_min[3]));
-    if (e <= kZeroValue) e = e < kZeroValue ? 0.f : (float)SPEC_KV_ZERO_EXP;  // no token with values; zeros alone
+    if (e < -200.f) e = 0.f;  // no token with values
     const bool mixed = e - least > (float)kValueSpread;
     const long long at = (long long)h * w.tiles + wt;
     if (tid == 0) w.info[at] = make_float2(e + (float)kSumShift, mixed ? 1.f : 0.f);
-    // (zeros count as the least: no row's reference is then above what its other tokens may need)
-    if (mixed && tid < kTile) w.ev[at * kTile + tid] = (s_ev[tid] <= kZeroValue ? least : s_ev[tid]) + (float)kSumShift;
+    if (mixed && tid < kTile) w.ev[at * kTile + tid] = s_ev[tid] < -200.f ? 0.f : s_ev[tid] + (float)kSumShift;
     const int sub = tid % L, u0 = tid / L;
     uint2 kw[STEPS], vw[STEPS];
 #pragma unroll
@@ -329,7 +312,7 @@ __global__ void __launch_bounds__(kWidenThreads) chunk_widen_kernel(const __grid
       float ks = s_ks[r];
       const float ev = s_ev[r];
       if (nans) ks = nan;
-      const float vs = ks != ks || ev <= kZeroValue ? 0.f : ex2((mixed ? 0.f : ev - e) + (float)kValueShift);
+      const float vs = ks != ks || ev < -200.f ? 0.f : ex2((mixed ? 0.f : ev - e) + (float)kValueShift);
       float x[8], y[8];
       codes4(kw[i].x, x);
       codes4(kw[i].y, x + 4);

@@ -112,55 +112,3 @@ def test_the_longest_chunk(dev):  # noqa: F811
         dx = [(q[r].double().abs() @ size.T).amax(-1) * dim ** -0.5, q[r].double().abs().amax(-1) * size.sum(-1).max() * dim ** -0.5]
         ref = [x.cpu().numpy() for x in (w @ values[:r + 1], torch.logsumexp(s, -1), w @ values[:r + 1].abs(), torch.stack(dx))]
         U.compare(out["o"][r], out["lse"][r], ref, torch.bfloat16, r + 1)
-
-
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("kind", ["some", "tile", "tiny", "mixed", "all", "signed"])
-def test_values_of_zeros(dev, dim, dtype, kind):  # noqa: F811
-    """Vectors of zeros, which are stored under 2^-60: among ordinary ones, a whole tile of them, among values as small as the cache
-    holds, in tiles whose other exponents are far apart (the largest of them hidden from most rows), nothing else, and of both
-    signs. A vector of numbers under the same exponent is no zero."""
-    c = Case(dev, [300, 420], [300, 270], heads=8, kv_heads=2, dim=dim, page=32, seed=13, dtype=dtype, prefix=70)
-    codes, exps = c.codes[1], c.exps[1]
-    def put(b, t, h, code):
-        codes[c.table[b][t // 32], h, t % 32] = code
-        exps[c.table[b][t // 32], h, t % 32] = 127 + U.ZERO_EXP
-    if kind == "tiny":
-        exps[exps != 255] = 127 - 99
-    for b, n in enumerate(c.lens):
-        for t in range(n):
-            for h in (0, 1):
-                if kind == "all" or kind == "tile" and 128 <= t < 256 or kind not in ("all", "tile") and t % 11 == h:
-                    put(b, t, h, 0x80 if kind == "signed" and t % 2 else 0)
-    if kind == "mixed":
-        for b, t in ((0, 255), (1, 383)):
-            exps[c.table[b][t // 32], :, t % 32] += 60
-        put(0, 40, 0, 0x38)  # ones
-    if kind == "signed":
-        put(1, 150, 1, np.arange(dim) % 2 * 0x38)
-    c.check()
-
-
-def test_a_zero_value_costs_no_time(dev):  # noqa: F811
-    """A prompt of 4096 tokens with a value of zeros in every tile, against the same prompt without."""
-    n, page = 4096, 64
-    q = torch.randn(n, 32, 128, device=dev).bfloat16()
-    k, v = (torch.randn(n // page, 8, page, 128, device=dev).mul(80).clamp(-448, 448).to(torch.float8_e4m3fn) for _ in range(2))
-    exps = [torch.full((n // page, 8, page), 120, dtype=torch.uint8, device=dev) for _ in range(3)]
-    w = v.clone()
-    w.view(torch.uint8)[::2, :, 9] = 0
-    exps[2][::2, :, 9] = 127 + U.ZERO_EXP
-    caches = [api.KVCache(k, v, exps[0], exps[1]), api.KVCache(k, w, exps[0], exps[2])]
-    table, lens = torch.arange(n // page, dtype=torch.int32, device=dev).view(1, -1), torch.tensor([n], dtype=torch.int32, device=dev)
-    best = [1e9, 1e9]
-    for _ in range(30):
-        for i, cache in enumerate(caches):
-            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
-            a.record()
-            for _ in range(5):
-                api.spec_attention_chunk(q, cache, table, lens, gamma=n - 1)
-            b.record()
-            torch.cuda.synchronize(dev)
-            best[i] = min(best[i], a.elapsed_time(b))
-    assert best[1] < 1.3 * best[0], best
