@@ -112,3 +112,27 @@ def test_the_longest_chunk(dev):  # noqa: F811
         dx = [(q[r].double().abs() @ size.T).amax(-1) * dim ** -0.5, q[r].double().abs().amax(-1) * size.sum(-1).max() * dim ** -0.5]
         ref = [x.cpu().numpy() for x in (w @ values[:r + 1], torch.logsumexp(s, -1), w @ values[:r + 1].abs(), torch.stack(dx))]
         U.compare(out["o"][r], out["lse"][r], ref, torch.bfloat16, r + 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("depth", [4.0, 12.0, 25.0])
+def test_a_value_of_zeros_that_takes_nearly_all_weight(dev, dim, dtype, depth):  # noqa: F811
+    """The first token's value is zeros and its weight about e^depth times that of each of the others, which are what is left of the
+    output and keep their places: zeros are stored under 2^-60, and a weight counts with its token's power of two. Other zeros,
+    of both signs, stand among the tokens, and a whole tile is of them."""
+    c = Case(dev, [300, 420], [300, 270], heads=8, kv_heads=2, dim=dim, page=32, seed=13, dtype=dtype)
+    c.q.mul_(0.2)
+    c.q[..., 0] = depth * dim ** 0.5 / 4
+    codes, exps = c.codes, c.exps
+    for b, n in enumerate(c.lens):
+        for t in range(n):
+            page, slot = c.table[b][t // 32], t % 32
+            codes[0][page, :, slot, 0] = 0
+            if t == 0 or t % 29 == 7 or 128 <= t < 256 and b == 1:
+                codes[1][page, :, slot], exps[1][page, :, slot] = (0x80 if t % 2 else 0), 127 + U.ZERO_EXP
+    for b in (0, 1):
+        page = c.table[b][0]
+        codes[0][page, :, 0], exps[0][page, :, 0] = 0, 127
+        codes[0][page, :, 0, 0] = 0x48  # 4
+    c.check()
