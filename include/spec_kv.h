@@ -160,7 +160,9 @@ spec_status spec_attention(spec_attn_batch g, spec_kv_cache c, spec_dtype dtype,
  * sequence of n_b = gamma_b + 1 rows sees the prefix, the first kv_len[b] - n_b tokens and
  * the chunk's own up to i; a packed batch may mix prompts with single tokens. Where fp32
  * queries' rows are many, their 24 bits enter the scores and a weight enters the values' sum
- * with 22 bits down to 2^-32 of the row's largest weight.
+ * with 22 bits down to 2^-32 of the row's largest weight. Where rows are many, exponents of 128 neighbouring
+ * tokens that differ by at most 20 (10 with fp32 queries) do not count in a weight's size: one of a token
+ * of the larger exponents is then right to 2^-13 (2^-23) of the row's largest, each times its 2^exponent.
  *
  * Workspace. Long chunks are computed from keys and values widened to 16 bits: 4 bytes for each
  * element of the keys that the page table and the prefix have room for, not what kv_len says is

@@ -12,7 +12,7 @@
 // chunk_widen_kernel  keys to bf16, values to f16 relative to the tile's largest exponent. A
 //                     token stored as NaN, or on a bad page, gets NaN keys and zero values: a
 //                     row that does not see it has the weight 0 there, and 0 * NaN must not
-//                     reach it. Where a tile's exponents differ by more than 20, its values
+//                     reach it. Where a tile's exponents differ by more than 20 (10 with fp32 queries), its values
 //                     would lose places to tokens that a row may not even see: they are then
 //                     widened without their exponents, and these join the scores one by one
 //                     (`mixed`), as in attn_tc_kernel.
@@ -40,7 +40,10 @@ namespace sv {
 constexpr int kPlanThreads = 1024;
 constexpr int kWidenThreads = 256;
 constexpr int kValueShift = 6;    // the largest value of a tile comes to at most 448 * 2^6
-constexpr int kValueSpread = 20;  // code * 2^(6 + e - largest) is exact in f16 down to e = largest - 21
+// Most that the exponents of a tile may differ by while they are left to its values: code * 2^(6 + e - largest) is exact in f16
+// down to e = largest - 21, and a weight, which is then without them, is off by at most 2^-33 of the row's largest by itself, so by
+// 2^-13 of it with them, for bf16 outputs. With fp32 queries 2^-23 of it.
+constexpr int kValueSpread = 20, kValueSpread32 = 10;
 
 // Row block rb of sequence b: its place on the line, its tiles (the prefix's and its own), the
 // widened tile that is the sequence's first less the prefix's number of tiles.
@@ -216,6 +219,7 @@ struct WideParams {
   int tiles;
   // chunks
   float2* info;  // [kv head][tile]: E, and whether the tile is mixed
+  int spread;    // of exponents, past which a tile is mixed
   float* ev;     // [kv head][tile][128]: a mixed tile's E, token by token
   int q_tma;     // bf16 queries come by TMA, whole tokens a load (any number of heads a kv head; rows and heads on the 16-byte grid)
   ChunkParams c;
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kWidenThreads) chunk_widen_kernel(const __grid
     float e = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
     const float least = fminf(fminf(s_min[0], s_min[1]), fminf(s_min[2], s_min[3]));
     if (e < -200.f) e = 0.f;  // no token with values
-    const bool mixed = e - least > (float)kValueSpread;
+    const bool mixed = e - least > (float)w.spread;
     const long long at = (long long)h * w.tiles + wt;
     if (tid == 0) w.info[at] = make_float2(e + (float)kSumShift, mixed ? 1.f : 0.f);
     if (mixed && tid < kTile) w.ev[at * kTile + tid] = s_ev[tid] < -200.f ? 0.f : s_ev[tid] + (float)kSumShift;

@@ -398,6 +398,7 @@ cudaError_t pass_chunk(const AttnParams& own, const spec_attn_batch& g, const sp
   w.tiles = (int)L.chunk_tiles;
   w.info = reinterpret_cast<float2*>(ws + L.c_info);
   w.ev = reinterpret_cast<float*>(ws + L.c_ev);
+  w.spread = F32 ? kValueSpread32 : kValueSpread;
   w.c.head = reinterpret_cast<ChunkHead*>(ws + L.c_head);
   w.c.entry = reinterpret_cast<ChunkEntry*>(ws + L.c_entry);
   w.c.order = reinterpret_cast<int*>(ws + L.c_order);

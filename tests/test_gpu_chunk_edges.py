@@ -136,3 +136,29 @@ def test_a_value_of_zeros_that_takes_nearly_all_weight(dev, dim, dtype, depth): 
         codes[0][page, :, 0], exps[0][page, :, 0] = 0, 127
         codes[0][page, :, 0, 0] = 0x48  # 4
     c.check()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("apart", [11, 15, 20, 30])
+def test_light_tokens_of_larger_values_with_fp32_queries(dev, dim, apart):  # noqa: F811
+    """One token of small values has nearly all weight; every fourth of the others has a weight of 2^-27 to 2^-25 of it and values
+    2^apart times as large, and is all that half of the output's elements hold: these keep fp32's places too."""
+    c = Case(dev, [420], [300], heads=8, kv_heads=2, dim=dim, page=32, seed=14, dtype="f32")
+    codes, exps = c.codes, c.exps
+    c.q.zero_()
+    c.q[..., 0], c.q[..., 1] = 1.0, 1.3
+    rng = np.random.default_rng(15)
+    for t in range(420):
+        page, slot = c.table[0][t // 32], t % 32
+        codes[0][page, :, slot], exps[0][page, :, slot] = 0, 127
+        light = t % 4 == 1
+        codes[0][page, :, slot, 0] = 0 if light else 0xe0  # -32: far below
+        codes[0][page, :, slot, 1] = 0x20 + t % 23 if light else 0  # 0.125 to 0.9: no power of two
+        codes[1][page, :, slot] = 0x30 + rng.integers(0, 64, (2, dim))
+        exps[1][page, :, slot] = 120 + (apart if light else 0)
+        if t == 0:
+            codes[0][page, :, slot, 0] = 0x5b  # 22
+            codes[1][page, :, slot, :dim // 2] = 0
+        elif not light:
+            codes[1][page, :, slot, :dim // 2] = 0
+    c.check(scale=27 * np.log(2) / 22)
