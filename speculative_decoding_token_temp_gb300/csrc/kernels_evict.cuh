@@ -15,8 +15,8 @@
 //
 // What bounds it: the move HBM, 64 sequences of 1000-8192 tokens x 8 heads of 128, at most 4096 kept,
 // to other pages: 161 us for both kernels, of which the selection 24 (counts in shared memory, a
-// barrier at each step); 5.8 TB/s over all. In place 215 us for 64 sequences of 8192 (a block waits for
-// its loads at each step), 40 us for one (the chain of 16 steps). Few tokens: 8 us, two launches.
+// barrier at each step); 5.8 TB/s over all. In place 216 us for 64 sequences of 8192 (a block waits for
+// its loads at each step), 36 us for one (the chain of 16 steps). Few tokens: 8 us, two launches.
 #pragma once
 
 #include "kernels_kv.cuh"
